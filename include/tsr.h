@@ -316,6 +316,105 @@ int beam_step(tsr_handle h, const void* logits, int dtype, int groups, int beam,
               int64_t row_stride, const double* beam_scores, int32_t* out_parent,
               int32_t* out_token, double* out_score, int32_t* out_status, void* hip_stream);
 
+/* 8-bit codes of float rows, one scale per row: the form int8_logits takes
+ * its operands in (hidden states per token, a weight per output channel)
+ * [P1 "int8 weights": per-row absmax].
+ *  x [rows][width] float32 or bfloat16 (dtype), row_stride elements apart.
+ *  out_scale [rows] float32: s = max |x| of the row / 127, rounded to float32.
+ *  out_codes [rows][width] int8, codes_stride bytes apart: x / s rounded to
+ *      the nearest whole number, ties to even, decided on the exact quotient,
+ *      and held to [-127, 127].
+ * A row of zeros gets scale 0 and codes 0. A row that holds NaN or an
+ * infinity gets scale NaN and codes 0, so its logits are NaN and the sampler
+ * reports it as TSR_ROW_NONFINITE. Bytes of out_codes between width and
+ * codes_stride are left as they are.
+ * rows is not bound by the handle's max_rows (a weight has vocab rows); width
+ * <= 2^30 (TSR_EUNSUPPORTED beyond). Uses no workspace. */
+int quantize_rows(tsr_handle h, const void* x, int dtype, int rows, int width, int64_t row_stride,
+                  int8_t* out_codes, int64_t codes_stride, float* out_scale, void* hip_stream);
+
+/* An output projection held in 8 bits (device memory, the caller's).
+ *  weight [vocab][width] int8, weight_stride bytes apart (any alignment).
+ *  scale [vocab] float32: the value of one step of each channel's codes.
+ *  bias [vocab] float32, or NULL. */
+typedef struct {
+  const int8_t* weight;
+  int64_t weight_stride;
+  const float* scale;
+  const float* bias;
+  int32_t vocab;
+  int32_t width;
+} tsr_head;
+
+/* Logits of `rows` hidden states against an 8-bit output projection:
+ *   out[r][n] = (sum_k codes[r][k] * weight[n][k]) * code_scale[r] * scale[n]
+ *               + bias[n].
+ * The sum is exact, in 32-bit integers; it is then scaled in float32 (the sum
+ * rounded, times code_scale, times scale and plus bias in one fma) and
+ * rounded once more where the logits are bfloat16. A NaN scale makes its row's
+ * (or channel's) logits NaN.
+ *  codes [rows][width] int8, codes_stride bytes apart (any alignment).
+ *  out_logits [rows][vocab] of type dtype, out_stride elements apart; what
+ *      lies between vocab and out_stride is left as it is.
+ * width <= 131071 (TSR_EUNSUPPORTED beyond: the sum might leave 32 bits).
+ * Uses no workspace. */
+int int8_logits(tsr_handle h, const int8_t* codes, int64_t codes_stride, const float* code_scale,
+                int rows, const tsr_head* head, void* out_logits, int dtype, int64_t out_stride,
+                void* hip_stream);
+
+/* From hidden states to tokens: quantize_rows, int8_logits and sample_rows
+ * enqueued one after the other.
+ *  hidden [rows][head->width] of type hidden_dtype, hidden_stride elements
+ *      apart.
+ *  codes [rows][width], code_scale [rows] and logits [rows][vocab] (of type
+ *      dtype) are workspace of the caller's and hold the codes, the scales
+ *      and the logits afterwards.
+ * params, step, out_tokens and diag are sample_rows'; so are the limits on
+ * vocab. */
+int sample_hidden(tsr_handle h, const void* hidden, int hidden_dtype, int rows,
+                  int64_t hidden_stride, const tsr_head* head, int8_t* codes, float* code_scale,
+                  void* logits, int dtype, const tsr_params* params, uint64_t step,
+                  int32_t* out_tokens, const tsr_diag* diag, void* hip_stream);
+
+/* The verify step from probabilities and the caller's random numbers
+ * [P2 39.4, Listing 39.4; P3 "The Algorithm", "Batching Speculation"], for
+ * `rows` sequences with up to K drafted tokens each.
+ *  target_probs: p, K + 1 rows of `vocab` per sequence (float32 or bfloat16,
+ *      dtype): position j of sequence b starts at b * target_seq_stride +
+ *      j * target_row_stride elements.
+ *  draft_probs: q, K rows per sequence, laid out by its own strides; NULL:
+ *      each draft token was proposed with certainty (q is 1 at the token).
+ *  draft_tokens [rows][K]; draft_lens [rows] (nullable: K each): how many of
+ *      them sequence b has, 0..K. Positions past that many drafts are not
+ *      read (the rows of p: past draft_lens[b]).
+ *  accept_u [rows][K], draw_u [rows] float32, each in [0, 1).
+ * For j = 0, 1, ...: draft x_j is kept iff accept_u[b][j] < min(1, p(x_j) /
+ * q(x_j)) (eq. 39.3; with q = 0, iff p > 0). At the first refusal the step
+ * ends with a draw from max(0, p - q) (eq. 39.4), or from p where that is
+ * zero everywhere; with every draft kept it ends with a draw from the row of
+ * p after them. The draw is the first id, in ascending order, whose running
+ * total of the weights exceeds draw_u[b] times their sum (the last id with a
+ * weight where rounding leaves none): the weights need not sum to 1. Tests,
+ * weights and sums are formed in 64 bits.
+ *  out_tokens   [rows][K+1]: the kept drafts, the drawn id, then -1.
+ *  out_accepted [rows]: number of drafts kept.
+ *  out_status   [rows] (nullable): TSR_ROW_OK; else the tokens are all -1 and
+ *      the count is 0. The first that holds of: TSR_ROW_BADPARAM (draft_lens
+ *      outside 0..K), TSR_ROW_BADTOKEN (one of the sequence's draft tokens
+ *      outside [0, vocab)), TSR_ROW_NONFINITE (a probability of a tested
+ *      draft is negative, infinite or NaN), TSR_ROW_BADPARAM (accept_u of a
+ *      tested draft, or draw_u, outside [0, 1)), TSR_ROW_NONFINITE (such a
+ *      value in the rows drawn from), TSR_ROW_EMPTY (they are all zero).
+ *      Rows and positions that the step does not come to are not checked.
+ * 1 <= K <= max_k and K <= 32; vocab <= 2^30 (TSR_EUNSUPPORTED beyond).
+ * Strides are not negative; rows may overlap or repeat (stride 0). */
+int verify_probs(tsr_handle h, const void* target_probs, int64_t target_seq_stride,
+                 int64_t target_row_stride, const void* draft_probs, int64_t draft_seq_stride,
+                 int64_t draft_row_stride, int dtype, const int32_t* draft_tokens,
+                 const int32_t* draft_lens, const float* accept_u, const float* draw_u, int rows,
+                 int K, int vocab, int32_t* out_tokens, int32_t* out_accepted,
+                 int32_t* out_status, void* hip_stream);
+
 /* Test hook: out_words[i][0..3] = Philox4x32-10(counters[i][0..3], key = the
  * handle's seed) for i < n, computed on the device by the same function the
  * sampler uses. counters and out_words are device memory. */

@@ -24,8 +24,8 @@ JOINT, SEQUENTIAL = 0, 1
 ROW_OK, ROW_NONFINITE, ROW_EMPTY, ROW_BADTOKEN, ROW_BADPARAM = 0, 1, 2, 3, 4
 EXPORTED_SYMBOLS = ("sampler_init", "sampler_destroy", "greedy_argmax", "sample_rows",
                     "sample_rows_masked", "sample_rows_ex", "spec_verify", "spec_verify_noalloc",
-                    "tree_verify", "beam_step",
-                    "sampler_philox", "sampler_strerror")
+                    "tree_verify", "beam_step", "quantize_rows", "int8_logits",
+                    "sample_hidden", "verify_probs", "sampler_philox", "sampler_strerror")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -63,6 +63,12 @@ class _Constraints(ctypes.Structure):
                 ("row_params", ctypes.c_void_p)]
 
 
+class _Head(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("weight_stride", ctypes.c_int64),
+                ("scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("vocab", ctypes.c_int32), ("width", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -94,6 +100,12 @@ def load_library():
     lib.tree_verify.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, ctypes.POINTER(_Params),
                                 u64, vp, vp, vp, vp, vp]
     lib.beam_step.argtypes = [vp, vp, i32, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp]
+    lib.quantize_rows.argtypes = [vp, vp, i32, i32, i32, i64, vp, i64, vp, vp]
+    lib.int8_logits.argtypes = [vp, vp, i64, vp, i32, ctypes.POINTER(_Head), vp, i32, i64, vp]
+    lib.sample_hidden.argtypes = [vp, vp, i32, i32, i64, ctypes.POINTER(_Head), vp, vp, vp, i32,
+                                  ctypes.POINTER(_Params), u64, vp, ctypes.POINTER(_Diag), vp]
+    lib.verify_probs.argtypes = [vp, vp, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, i32, i32,
+                                 i32, vp, vp, vp, vp]
     lib.sampler_philox.argtypes = [vp, vp, i32, vp, vp]
     lib.sampler_strerror.argtypes = [i32]
     lib.sampler_strerror.restype = ctypes.c_char_p
@@ -165,6 +177,29 @@ def _stream_ptr(stream):
 
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+
+
+def _stream_on(device, stream):
+    """A raw stream handle: `stream`, or the current stream of `device` (which
+    need not be the current device)."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    getter = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return getter(device) if getter is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _made_on(stream):
+    """The context in which a call allocates what it returns: on the stream that
+    writes it, so that memory freed on the current stream is not taken early."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
 
 
 def pack_row_params(params_list):
@@ -378,6 +413,175 @@ class Sampler:
                                         _ptr(token), _ptr(score), _ptr(status),
                                         _stream_ptr(stream)), "beam_step")
         return parent, token, score
+
+    # 8-bit projection and verification from probabilities. Tensors of other
+    # shapes, types or devices than the kernels take raise ValueError (TypeError
+    # for a type of logits, hidden states or probabilities).
+    def quantize_rows(self, x, out=None, scale=None, stream=None):
+        """x [rows, W] float32 or bfloat16 (rows contiguous, any row stride) ->
+        (codes [rows, W] int8, scale [rows] float32): absmax codes per row."""
+        import torch
+        dt = _dtype_code(x)
+        _need(x.dim() == 2 and x.shape[1] > 0 and x.stride(1) == 1 and
+              (x.shape[0] < 2 or x.stride(0) >= x.shape[1]) and x.get_device() == self.device,
+              "x: [rows, width] rows on the handle's GPU, none overlapping")
+        rows, width = x.shape
+        if out is None or scale is None:
+            with _made_on(stream):
+                out = torch.empty(rows, width, dtype=torch.int8, device=x.device) \
+                    if out is None else out
+                scale = torch.empty(rows, dtype=torch.float32, device=x.device) \
+                    if scale is None else scale
+        self._check_codes(out, scale, rows, width, "out")
+        if rows == 0:
+            return out, scale
+        _check(load_library().quantize_rows(
+            self._h, x.data_ptr(), dt, rows, width, max(x.stride(0), width), out.data_ptr(),
+            max(out.stride(0), width), scale.data_ptr(), _stream_on(self.device, stream)),
+            "quantize_rows")
+        return out, scale
+
+    def _check_codes(self, codes, scale, rows, width, what):
+        import torch
+        _need(codes.dtype is torch.int8 and codes.dim() == 2 and codes.shape[0] == rows and
+              codes.shape[1] == width and codes.stride(1) == 1 and
+              (rows < 2 or codes.stride(0) >= width) and codes.get_device() == self.device,
+              f"{what}: [{rows}, {width}] int8 rows on the handle's GPU")
+        _need(scale.dtype is torch.float32 and scale.dim() == 1 and scale.shape[0] == rows and
+              scale.is_contiguous() and scale.get_device() == self.device,
+              f"{what}'s scale: [{rows}] float32 on the handle's GPU")
+
+    def _head(self, weight, w_scale, bias):
+        import torch
+        _need(weight.dim() == 2 and weight.shape[0] > 0 and weight.shape[1] > 0,
+              "weight: [vocab, width]")
+        vocab, width = weight.shape
+        self._check_codes(weight, w_scale, vocab, width, "weight")
+        if bias is not None:
+            _need(bias.dtype is torch.float32 and bias.dim() == 1 and bias.shape[0] == vocab and
+                  bias.is_contiguous() and bias.get_device() == self.device,
+                  f"bias: [{vocab}] float32 on the handle's GPU")
+        return _Head(weight.data_ptr(), max(weight.stride(0), width), w_scale.data_ptr(),
+                     None if bias is None else bias.data_ptr(), vocab, width)
+
+    def _logits_out(self, out, rows, vocab, dtype, like, stream):
+        import torch
+        if out is None:
+            with _made_on(stream):
+                return torch.empty(rows, vocab, dtype=dtype, device=like.device)
+        _need(out.dim() == 2 and out.shape[0] == rows and out.shape[1] == vocab and
+              out.stride(1) == 1 and (rows < 2 or out.stride(0) >= vocab) and
+              out.get_device() == self.device, f"out: [{rows}, {vocab}] rows on the handle's GPU")
+        return out
+
+    def int8_logits(self, codes, scale, weight, w_scale, bias=None, dtype=None, out=None,
+                    stream=None):
+        """codes [rows, W] and weight [V, W] int8 with their scales (see
+        quantize_rows), bias [V] float32 or None -> logits [rows, V], of `dtype`
+        (float32 or bfloat16, the default) or in `out`."""
+        import torch
+        head = self._head(weight, w_scale, bias)
+        rows = codes.shape[0]
+        self._check_codes(codes, scale, rows, head.width, "codes")
+        out = self._logits_out(out, rows, head.vocab, dtype or torch.bfloat16, codes, stream)
+        if rows == 0:
+            return out
+        _check(load_library().int8_logits(
+            self._h, codes.data_ptr(), max(codes.stride(0), head.width), scale.data_ptr(), rows,
+            ctypes.byref(head), out.data_ptr(), _dtype_code(out), max(out.stride(0), head.vocab),
+            _stream_on(self.device, stream)), "int8_logits")
+        return out
+
+    def sample_hidden(self, hidden, weight, w_scale, params, step: int, bias=None, dtype=None,
+                      out=None, logits=None, diag=None, stream=None):
+        """hidden [rows, W] float32 or bfloat16 -> one token per row: quantize_rows,
+        int8_logits and sample_rows in one call. ``logits``: a preallocated
+        contiguous [rows, V] tensor for the logits, or None (then of `dtype`,
+        bfloat16 by default); ``diag`` as in sample_rows."""
+        import torch
+        hdt = _dtype_code(hidden)
+        head = self._head(weight, w_scale, bias)
+        rows, dev = hidden.shape[0], hidden.device
+        _need(hidden.dim() == 2 and hidden.shape[1] == head.width and hidden.stride(1) == 1 and
+              (hidden.shape[0] < 2 or hidden.stride(0) >= head.width) and
+              hidden.get_device() == self.device,
+              f"hidden: [rows, {head.width}] rows on the handle's GPU")
+        logits = self._logits_out(logits, rows, head.vocab, dtype or torch.bfloat16, hidden, stream)
+        _need(logits.is_contiguous(), "logits: contiguous")
+        with _made_on(stream):
+            codes = torch.empty(rows, head.width, dtype=torch.int8, device=dev)
+            scale = torch.empty(rows, dtype=torch.float32, device=dev)
+            out = torch.empty(rows, dtype=torch.int32, device=dev) if out is None else out
+        self._check_ints(out, (rows,), "out")
+        cp = Params.of(params)._c()
+        d = None
+        if diag is not None:
+            d = _Diag(*(ctypes.c_void_p(diag[k].data_ptr()) if diag.get(k) is not None else None
+                        for k in ("status", "kept_count", "threshold", "kept_mass", "probs")))
+        if rows == 0:
+            return out
+        _check(load_library().sample_hidden(
+            self._h, hidden.data_ptr(), hdt, rows, max(hidden.stride(0), head.width),
+            ctypes.byref(head), codes.data_ptr(), scale.data_ptr(), logits.data_ptr(),
+            _dtype_code(logits), ctypes.byref(cp), int(step), out.data_ptr(),
+            ctypes.byref(d) if d is not None else None, _stream_on(self.device, stream)),
+            "sample_hidden")
+        return out
+
+    def _check_ints(self, t, shape, what):
+        import torch
+        _need(t.dtype is torch.int32 and t.shape == shape and t.is_contiguous() and
+              t.get_device() == self.device, f"{what}: {list(shape)} int32 on the handle's GPU")
+
+    def _check_floats(self, t, shape, what):
+        import torch
+        _need(t.dtype is torch.float32 and t.shape == shape and t.is_contiguous() and
+              t.get_device() == self.device, f"{what}: {list(shape)} float32 on the handle's GPU")
+
+    def verify_probs(self, target, draft, draft_tokens, accept_u, draw_u, draft_lens=None,
+                     out_tokens=None, out_accepted=None, out_status=None, stream=None):
+        """The verify step from probabilities and given random numbers: target
+        [rows, K+1, V] and draft [rows, K, V] (None: the draft tokens were
+        proposed with certainty) float32 or bfloat16, draft_tokens [rows, K] and
+        draft_lens [rows] (None: K each) int32, accept_u [rows, K] and draw_u
+        [rows] float32 in [0, 1) -> (tokens [rows, K+1], accepted [rows])."""
+        import torch
+        dt = _dtype_code(target)
+        _need(target.dim() == 3 and target.stride(2) == 1 and target.shape[1] > 1 and
+              target.get_device() == self.device,
+              "target: [rows, K + 1, vocab] rows on the handle's GPU")
+        rows, k1, vocab = target.shape
+        K = k1 - 1
+        if draft is not None:
+            _need(draft.dtype is target.dtype and draft.shape == (rows, K, vocab) and
+                  draft.stride(2) == 1 and draft.get_device() == self.device,
+                  f"draft: [{rows}, {K}, {vocab}] of the target's type on the handle's GPU")
+        self._check_ints(draft_tokens, (rows, K), "draft_tokens")
+        self._check_floats(accept_u, (rows, K), "accept_u")
+        self._check_floats(draw_u, (rows,), "draw_u")
+        if draft_lens is not None:
+            self._check_ints(draft_lens, (rows,), "draft_lens")
+        if out_tokens is None or out_accepted is None:
+            with _made_on(stream):
+                out_tokens = torch.empty(rows, k1, dtype=torch.int32, device=target.device) \
+                    if out_tokens is None else out_tokens
+                out_accepted = torch.empty(rows, dtype=torch.int32, device=target.device) \
+                    if out_accepted is None else out_accepted
+        self._check_ints(out_tokens, (rows, k1), "out_tokens")
+        self._check_ints(out_accepted, (rows,), "out_accepted")
+        if out_status is not None:
+            self._check_ints(out_status, (rows,), "out_status")
+        if rows == 0:
+            return out_tokens, out_accepted
+        _check(load_library().verify_probs(
+            self._h, target.data_ptr(), target.stride(0), target.stride(1),
+            None if draft is None else draft.data_ptr(), 0 if draft is None else draft.stride(0),
+            0 if draft is None else draft.stride(1), dt, draft_tokens.data_ptr(),
+            None if draft_lens is None else draft_lens.data_ptr(), accept_u.data_ptr(),
+            draw_u.data_ptr(), rows, K, vocab, out_tokens.data_ptr(), out_accepted.data_ptr(),
+            None if out_status is None else out_status.data_ptr(),
+            _stream_on(self.device, stream)), "verify_probs")
+        return out_tokens, out_accepted
 
     def philox(self, counters, stream=None):
         """counters: [n, 4] int32/uint32 device tensor -> [n, 4] words (int32 view)."""

@@ -104,6 +104,41 @@ bool elem_aligned(const void* p, int dtype) {
   return ((uintptr_t)p % (uintptr_t)esize(dtype)) == 0;
 }
 
+bool word_aligned(const void* p) { return ((uintptr_t)p % 4) == 0; }
+
+constexpr int kMaxQuantWidth = 1 << 30;
+// sums of products of 8-bit integers fit 32 bits: 2^17 - 1 times (-128)^2
+constexpr int kMaxInt8Width = (1 << 17) - 1;
+constexpr int kMaxVprobsVocab = 1 << 30;
+
+int check_quantize(const void* x, int dtype, int rows, int width, int64_t row_stride,
+                   const int8_t* out_codes, int64_t codes_stride, const float* out_scale) {
+  if (!x || !out_codes || !out_scale) return TSR_EINVAL;
+  if (dtype != TSR_F32 && dtype != TSR_BF16) return TSR_EINVAL;
+  if (rows < 0 || width < 1 || row_stride < width || codes_stride < width) return TSR_EINVAL;
+  if (!elem_aligned(x, dtype) || !word_aligned(out_scale)) return TSR_EINVAL;
+  if (width > kMaxQuantWidth) return TSR_EUNSUPPORTED;
+  return TSR_OK;
+}
+
+int check_int8(tsr_handle h, const int8_t* codes, int64_t codes_stride, const float* code_scale,
+               int rows, const tsr_head* head, const void* out_logits, int dtype,
+               int64_t out_stride) {
+  if (!codes || !code_scale || !head || !out_logits) return TSR_EINVAL;
+  if (!head->weight || !head->scale) return TSR_EINVAL;
+  if (dtype != TSR_F32 && dtype != TSR_BF16) return TSR_EINVAL;
+  if (rows < 0 || rows > h->max_rows || head->vocab < 1 || head->vocab > h->max_vocab ||
+      head->width < 1)
+    return TSR_EINVAL;
+  if (codes_stride < head->width || head->weight_stride < head->width || out_stride < head->vocab)
+    return TSR_EINVAL;
+  if (!word_aligned(code_scale) || !word_aligned(head->scale) || !word_aligned(head->bias) ||
+      !elem_aligned(out_logits, dtype))
+    return TSR_EINVAL;
+  if (head->width > kMaxInt8Width) return TSR_EUNSUPPORTED;
+  return TSR_OK;
+}
+
 // Arguments every verify entry point checks (the handle's limits aside).
 int check_verify(const void* target_logits, const void* draft_logits, int dtype,
                  const int32_t* draft_tokens, int rows, int K, int vocab,
@@ -466,6 +501,116 @@ int beam_step(tsr_handle h, const void* logits, int dtype, int groups, int beam,
     const hipError_t e = tsr::launch_beam(logits, dtype, groups, beam, vocab, sb, ragged,
                                           beam_scores, h->bws, out_parent, out_token, out_score,
                                           out_status, (hipStream_t)hip_stream);
+    return e == hipSuccess ? TSR_OK : TSR_EDEVICE;
+  });
+}
+
+int quantize_rows(tsr_handle h, const void* x, int dtype, int rows, int width, int64_t row_stride,
+                  int8_t* out_codes, int64_t codes_stride, float* out_scale, void* hip_stream) {
+  if (!h) return TSR_EINVAL;
+  const int rc = check_quantize(x, dtype, rows, width, row_stride, out_codes, codes_stride,
+                                out_scale);
+  if (rc != TSR_OK || rows == 0) return rc;
+  return on_device(h->device, [&]() -> int {
+    const hipError_t e = tsr::launch_quantize(x, dtype, rows, width,
+                                              (long long)row_stride * esize(dtype), out_codes,
+                                              (long long)codes_stride, out_scale,
+                                              (hipStream_t)hip_stream);
+    return e == hipSuccess ? TSR_OK : TSR_EDEVICE;
+  });
+}
+
+int int8_logits(tsr_handle h, const int8_t* codes, int64_t codes_stride, const float* code_scale,
+                int rows, const tsr_head* head, void* out_logits, int dtype, int64_t out_stride,
+                void* hip_stream) {
+  if (!h) return TSR_EINVAL;
+  const int rc = check_int8(h, codes, codes_stride, code_scale, rows, head, out_logits, dtype,
+                            out_stride);
+  if (rc != TSR_OK || rows == 0) return rc;
+  tsr::Int8Args a{};
+  a.x = codes;
+  a.x_stride = (long long)codes_stride;
+  a.x_scale = code_scale;
+  a.w = head->weight;
+  a.w_stride = (long long)head->weight_stride;
+  a.w_scale = head->scale;
+  a.bias = head->bias;
+  a.out = static_cast<unsigned char*>(out_logits);
+  a.out_stride_bytes = (long long)out_stride * esize(dtype);
+  a.rows = rows;
+  a.vocab = head->vocab;
+  a.width = head->width;
+  return on_device(h->device, [&]() -> int {
+    const hipError_t e = tsr::launch_int8(a, dtype, (hipStream_t)hip_stream);
+    return e == hipSuccess ? TSR_OK : TSR_EDEVICE;
+  });
+}
+
+int sample_hidden(tsr_handle h, const void* hidden, int hidden_dtype, int rows,
+                  int64_t hidden_stride, const tsr_head* head, int8_t* codes, float* code_scale,
+                  void* logits, int dtype, const tsr_params* params, uint64_t step,
+                  int32_t* out_tokens, const tsr_diag* diag, void* hip_stream) {
+  // every argument of the three steps first: an error leaves nothing enqueued
+  if (!h || !head || !out_tokens) return TSR_EINVAL;
+  int rc = check_quantize(hidden, hidden_dtype, rows, head->width, hidden_stride, codes,
+                          head->width, code_scale);
+  if (rc == TSR_OK)
+    rc = check_int8(h, codes, head->width, code_scale, rows, head, logits, dtype, head->vocab);
+  if (rc == TSR_OK) rc = check_params(params);
+  if (rc == TSR_OK && head->vocab > tsr::max_vocab_sample(dtype)) rc = TSR_EUNSUPPORTED;
+  if (rc != TSR_OK || rows == 0) return rc;
+  rc = quantize_rows(h, hidden, hidden_dtype, rows, head->width, hidden_stride, codes,
+                     head->width, code_scale, hip_stream);
+  if (rc == TSR_OK)
+    rc = int8_logits(h, codes, head->width, code_scale, rows, head, logits, dtype, head->vocab,
+                     hip_stream);
+  if (rc == TSR_OK)
+    rc = sample_rows(h, logits, dtype, rows, head->vocab, head->vocab, params, step, out_tokens,
+                     diag, hip_stream);
+  return rc;
+}
+
+int verify_probs(tsr_handle h, const void* target_probs, int64_t target_seq_stride,
+                 int64_t target_row_stride, const void* draft_probs, int64_t draft_seq_stride,
+                 int64_t draft_row_stride, int dtype, const int32_t* draft_tokens,
+                 const int32_t* draft_lens, const float* accept_u, const float* draw_u, int rows,
+                 int K, int vocab, int32_t* out_tokens, int32_t* out_accepted,
+                 int32_t* out_status, void* hip_stream) {
+  if (!h || !target_probs || !draft_tokens || !accept_u || !draw_u || !out_tokens || !out_accepted)
+    return TSR_EINVAL;
+  if (dtype != TSR_F32 && dtype != TSR_BF16) return TSR_EINVAL;
+  if (rows < 0 || rows > h->max_rows || vocab < 1 || vocab > h->max_vocab) return TSR_EINVAL;
+  if (K < 1 || K > kMaxDraft || K > h->max_k) return TSR_EINVAL;
+  if (target_seq_stride < 0 || target_row_stride < 0) return TSR_EINVAL;
+  if (draft_probs && (draft_seq_stride < 0 || draft_row_stride < 0)) return TSR_EINVAL;
+  if (!elem_aligned(target_probs, dtype) || (draft_probs && !elem_aligned(draft_probs, dtype)))
+    return TSR_EINVAL;
+  if (!word_aligned(draft_tokens) || !word_aligned(draft_lens) || !word_aligned(accept_u) ||
+      !word_aligned(draw_u) || !word_aligned(out_tokens) || !word_aligned(out_accepted) ||
+      !word_aligned(out_status))
+    return TSR_EINVAL;
+  if (vocab > kMaxVprobsVocab) return TSR_EUNSUPPORTED;
+  if (rows == 0) return TSR_OK;
+  const long long es = esize(dtype);
+  tsr::VprobsArgs a{};
+  a.target = static_cast<const unsigned char*>(target_probs);
+  a.t_seq = (long long)target_seq_stride * es;
+  a.t_row = (long long)target_row_stride * es;
+  a.draft = static_cast<const unsigned char*>(draft_probs);
+  a.d_seq = (long long)draft_seq_stride * es;
+  a.d_row = (long long)draft_row_stride * es;
+  a.tokens = draft_tokens;
+  a.lens = draft_lens;
+  a.accept_u = accept_u;
+  a.draw_u = draw_u;
+  a.rows = rows;
+  a.K = K;
+  a.V = vocab;
+  a.out_tokens = out_tokens;
+  a.out_accepted = out_accepted;
+  a.out_status = out_status;
+  return on_device(h->device, [&]() -> int {
+    const hipError_t e = tsr::launch_vprobs(a, dtype, (hipStream_t)hip_stream);
     return e == hipSuccess ? TSR_OK : TSR_EDEVICE;
   });
 }

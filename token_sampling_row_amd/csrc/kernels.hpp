@@ -133,6 +133,43 @@ hipError_t launch_beam(const void* logits, int dtype, int groups, int beam, int 
                        int32_t* out_parent, int32_t* out_tok, double* out_score,
                        int32_t* out_status, hipStream_t s);
 int max_vocab_beam(int dtype);
+
+// quantize_rows: codes and scales of `rows` rows, q_stride bytes apart.
+hipError_t launch_quantize(const void* x, int dtype, int rows, int width, long long stride_bytes,
+                           int8_t* q, long long q_stride, float* scale, hipStream_t s);
+
+// int8_logits: `rows` hidden rows by `vocab` channels, both `width` codes long.
+struct Int8Args {
+  const int8_t* x;
+  long long x_stride;
+  const float* x_scale;
+  const int8_t* w;
+  long long w_stride;
+  const float* w_scale;
+  const float* bias;   // null: none
+  unsigned char* out;
+  long long out_stride_bytes;
+  int rows, vocab, width;
+};
+hipError_t launch_int8(const Int8Args& a, int dtype, hipStream_t s);
+
+// verify_probs: strides in bytes between sequences and between positions.
+struct VprobsArgs {
+  const unsigned char* target;
+  long long t_seq, t_row;
+  const unsigned char* draft;   // null: each draft token is certain
+  long long d_seq, d_row;
+  const int32_t* tokens;        // [rows][K]
+  const int32_t* lens;          // [rows], null: K each
+  const float* accept_u;        // [rows][K]
+  const float* draw_u;          // [rows]
+  int rows, K, V;
+  int32_t* out_tokens;
+  int32_t* out_accepted;
+  int32_t* out_status;
+};
+hipError_t launch_vprobs(const VprobsArgs& a, int dtype, hipStream_t s);
+
 hipError_t launch_philox(const uint32_t* ctr, int n, uint32_t k0, uint32_t k1, uint32_t* out,
                          hipStream_t s);
 

@@ -1,0 +1,102 @@
+// Wide loads and stores at any byte alignment (the unaligned access mode the
+// HSA runtime sets), never outside the row they are given.
+#pragma once
+
+#include "device_common.hpp"
+
+namespace tsr {
+
+struct __attribute__((packed, aligned(1))) Bytes16 { uint32_t w[4]; };
+struct __attribute__((packed, aligned(1))) Bytes8 { uint32_t w[2]; };
+struct __attribute__((packed, aligned(1))) Bytes4 { uint32_t w[1]; };
+
+__device__ __forceinline__ uint4 load16(const void* p) {
+  const Bytes16 b = *static_cast<const Bytes16*>(p);
+  return make_uint4(b.w[0], b.w[1], b.w[2], b.w[3]);
+}
+
+template <int N>
+__device__ __forceinline__ void store_words(void* p, const uint32_t* w) {
+  static_assert(N == 1 || N == 2 || N == 4, "words");
+  if constexpr (N == 1) {
+    *static_cast<Bytes4*>(p) = Bytes4{{w[0]}};
+  } else if constexpr (N == 2) {
+    *static_cast<Bytes8*>(p) = Bytes8{{w[0], w[1]}};
+  } else {
+    *static_cast<Bytes16*>(p) = Bytes16{{w[0], w[1], w[2], w[3]}};
+  }
+}
+
+// Elements [e0, e0 + EPC) of a row of n elements; those at or past n read as 0.
+template <int DT>
+__device__ __forceinline__ uint4 load_chunk_zero(const unsigned char* row, long long e0,
+                                                 long long n) {
+  constexpr int EPC = Fmt<DT>::EPC, ESZ = Fmt<DT>::ESZ;
+  if (e0 + EPC <= n) return load16(row + e0 * ESZ);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < EPC; ++e) {
+    if (e0 + e < n) {
+      if constexpr (DT == 0)
+        w[e] = *reinterpret_cast<const uint32_t*>(row + (e0 + e) * 4);
+      else
+        w[e / 2] |= (uint32_t) * reinterpret_cast<const uint16_t*>(row + (e0 + e) * 2)
+                    << (16 * (e % 2));
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Bytes [k, k + 16) of a row of n bytes; those at or past n read as 0.
+__device__ __forceinline__ uint4 load_bytes_zero(const int8_t* row, int k, int n) {
+  if (k + 16 <= n) return load16(row + k);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (k + e < n) w[e / 4] |= (uint32_t)(uint8_t)row[k + e] << (8 * (e % 4));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float v) {
+  return __builtin_bit_cast(uint16_t, (__bf16)v);   // to nearest even
+}
+
+// N consecutive float results (n0 and up of a row of `n` elements) in the
+// output's type.
+template <int DT, int N>
+__device__ __forceinline__ void store_row(unsigned char* row, int n0, int n, const float* v) {
+  if constexpr (DT == 0) {
+    float* o = reinterpret_cast<float*>(row) + n0;
+    if (n0 + N <= n) {
+#pragma unroll
+      for (int e = 0; e < N; e += 4) {
+        const uint32_t w[4] = {__float_as_uint(v[e]), __float_as_uint(v[e + 1]),
+                               __float_as_uint(v[e + 2]), __float_as_uint(v[e + 3])};
+        store_words<4>(o + e, w);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (n0 + e < n) o[e] = v[e];
+    }
+  } else {
+    uint16_t* o = reinterpret_cast<uint16_t*>(row) + n0;
+    if (n0 + N <= n) {
+      constexpr int S = N >= 8 ? 8 : 4;
+#pragma unroll
+      for (int e = 0; e < N; e += S) {
+        uint32_t w[S / 2];
+#pragma unroll
+        for (int k = 0; k < S / 2; ++k)
+          w[k] = (uint32_t)bf16_bits(v[e + 2 * k]) | ((uint32_t)bf16_bits(v[e + 2 * k + 1]) << 16);
+        store_words<S / 2>(o + e, w);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (n0 + e < n) o[e] = bf16_bits(v[e]);
+    }
+  }
+}
+
+}  // namespace tsr
