@@ -320,7 +320,7 @@ int beam_step(tsr_handle h, const void* logits, int dtype, int groups, int beam,
  * its operands in (hidden states per token, a weight per output channel)
  * [P1 "int8 weights": per-row absmax].
  *  x [rows][width] float32 or bfloat16 (dtype), row_stride elements apart.
- *  out_scale [rows] float32: s = max |x| of the row / 127, rounded to float32.
+ *  out_scale [rows] float32: s = max |x| of the row times 1/127, in float32.
  *  out_codes [rows][width] int8, codes_stride bytes apart: x / s rounded to
  *      the nearest whole number, ties to even, decided on the exact quotient,
  *      and held to [-127, 127].

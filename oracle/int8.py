@@ -1,7 +1,7 @@
 """Plain reference of the 8-bit output projection: row codes and their product.
 
 quantize_rows [P1 "int8 weights": per-row absmax]: the scale of a row is
-max |x| / 127 rounded to float32; a code is the quotient by that float32 scale,
+max |x| times 1/127, in float32; a code is the quotient by that float32 scale,
 to the nearest whole number (ties to even), held to [-127, 127]. Formed in
 float64, which holds every quotient of two float32 values far enough from a
 half that is not one: with |code| <= 127 a quotient other than a half differs
@@ -23,7 +23,7 @@ def quantize_rows(x):
         if not np.isfinite(row).all():
             scale[r] = np.nan
             continue
-        s = np.float32(np.abs(row).max().astype(np.float32) / np.float32(127.0))
+        s = np.float32(np.abs(row).max()) * (np.float32(1.0) / np.float32(127.0))
         scale[r] = s
         if s > 0:
             codes[r] = np.clip(np.rint(row / np.float64(s)), -127, 127)

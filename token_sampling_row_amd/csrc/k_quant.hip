@@ -49,7 +49,7 @@ __global__ __launch_bounds__(kQuantBlock) void quant_kernel(const unsigned char*
 #pragma unroll
   for (int w = 0; w < kQuantBlock / kWave; ++w) m = max(m, wmax[w]);
   const bool bad = m >= 0x7F800000u;   // an infinity or NaN in the row
-  float s = __uint_as_float(m) / 127.0f;
+  float s = __uint_as_float(m) * (1.0f / 127.0f);
   if (threadIdx.x == 0) scale[r] = bad ? __uint_as_float(0x7FC00000u) : s;
   // scales near or below the smallest normal number: both sides times 2^64,
   // which is exact and leaves every quotient as it is

@@ -47,14 +47,36 @@ __device__ __forceinline__ uint4 load_chunk_zero(const unsigned char* row, long 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Bytes [k, k + 16) of a row of n bytes; those at or past n read as 0.
+// Bytes [k, k + 16) of a row of n bytes; those at or past n read as 0. Where
+// the row ends inside them: the row's last 16 bytes, shifted down.
 __device__ __forceinline__ uint4 load_bytes_zero(const int8_t* row, int k, int n) {
   if (k + 16 <= n) return load16(row + k);
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (k + e < n) w[e / 4] |= (uint32_t)(uint8_t)row[k + e] << (8 * (e % 4));
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  uint64_t lo = 0, hi = 0;
+  if (k < n) {
+    if (n >= 16) {
+      const uint4 v = load16(row + n - 16);
+      lo = v.x | (uint64_t)v.y << 32;
+      hi = v.z | (uint64_t)v.w << 32;
+      const int s = (k + 16 - n) * 8;   // 8 .. 120 bits
+      if (s >= 64) {
+        lo = hi >> (s - 64);
+        hi = 0;
+      } else {
+        lo = lo >> s | hi << (64 - s);
+        hi >>= s;
+      }
+    } else {   // k is 0
+#pragma unroll 1
+      for (int e = 0; e < n; ++e) {
+        const uint64_t byte = (uint8_t)row[e];
+        if (e < 8)
+          lo |= byte << (8 * e);
+        else
+          hi |= byte << (8 * (e - 8));
+      }
+    }
+  }
+  return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
 }
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) {
