@@ -109,6 +109,7 @@ bool word_aligned(const void* p) { return ((uintptr_t)p % 4) == 0; }
 constexpr int kMaxQuantWidth = 1 << 30;
 // sums of products of 8-bit integers fit 32 bits: 2^17 - 1 times (-128)^2
 constexpr int kMaxInt8Width = (1 << 17) - 1;
+constexpr int64_t kMaxInt8Stride = 1 << 23;   // a tile's 256 rows within 2^31 bytes
 constexpr int kMaxVprobsVocab = 1 << 30;
 
 int check_quantize(const void* x, int dtype, int rows, int width, int64_t row_stride,
@@ -135,7 +136,9 @@ int check_int8(tsr_handle h, const int8_t* codes, int64_t codes_stride, const fl
   if (!word_aligned(code_scale) || !word_aligned(head->scale) || !word_aligned(head->bias) ||
       !elem_aligned(out_logits, dtype))
     return TSR_EINVAL;
-  if (head->width > kMaxInt8Width) return TSR_EUNSUPPORTED;
+  if (head->width > kMaxInt8Width || codes_stride >= kMaxInt8Stride ||
+      head->weight_stride >= kMaxInt8Stride)
+    return TSR_EUNSUPPORTED;
   return TSR_OK;
 }
 

@@ -1,0 +1,514 @@
+// The 8-bit output projection (int8_logits): out[r][n] = sum_k x[r][k] w[n][k]
+// in 32-bit integers, times the row's and the channel's scale.
+//
+// Few rows are bound by the weight's bytes, many by the matrix pipes. The
+// weight is cut into runs of channels, each read from memory once: every hidden
+// row, or up to 256 of them, meets a run while it is in LDS.
+#pragma once
+
+#include <type_traits>
+
+#include "kernels.hpp"
+#include "wide_mem.hpp"
+
+namespace tsr {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+// 16 bytes per lane from byte at + k of a buffer to `p` + 16 lane in LDS. (The
+// host pass of the compiler does not know the 16-byte form.) ONCE: bytes that
+// no other workgroup reads are not kept in the caches.
+template <bool ONCE>
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t buffer, int8_t* p, uint32_t at,
+                                       int k) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (__attribute__((address_space(3))) void*)p, 16,
+                                           (int)at, k, 0, ONCE ? 2 : 0);
+#endif
+}
+// `bytes` bytes from p (0: every load of it is out of range, and reads nothing).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const int8_t* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p), 0, (int)bytes, 0x00027000);
+}
+// Waits until at most N loads are on their way and every LDS access is done.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "count");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+}
+
+// Tiles of BM hidden rows by BN channels. WM x WN wavefronts each hold MT x NT
+// blocks of 16 x 16 sums.
+//
+// v_mfma_i32_16x16x64_i8: lane l gives row l % 16 of the first operand (here
+// channels) and of the second (hidden rows), 16 bytes at (l / 16) * 16 of 64;
+// it gets channels (l / 16) * 4 + 0..3 of hidden row l % 16. Block t of a
+// wavefront takes channels (i / 4) * 4 NT + t * 4 + i % 4 (i < 16) of its
+// 16 NT, so that a lane ends with 4 NT neighbouring channels of one row and
+// four lanes write a whole line.
+//
+// A stage holds TK bytes of each of the tile's rows in LDS, as 16-byte chunks;
+// chunk c of row r lies at place c ^ turn(r), so that the 16 lanes which read
+// one chunk of 16 rows take every bank in turn.
+template <int BM, int BN, int WM, int WN, int TK>
+struct Tile {
+  static constexpr int WAVES = WM * WN, THREADS = WAVES * kWave;
+  static constexpr int MT = BM / (16 * WM), NT = BN / (16 * WN);
+  static constexpr int CH = TK / 16, PR = 64 / CH;   // chunks of a row, rows of a 1 KiB piece
+  static constexpr int XI = BM / PR / WAVES, WI = BN / PR / WAVES;   // pieces per wavefront
+  static constexpr int H = TK / 64;                                  // products along a stage
+  static_assert(XI * PR * WAVES == BM && WI * PR * WAVES == BN, "pieces");
+  static_assert(MT * 16 * WM == BM && NT * 16 * WN == BN, "blocks");
+
+  int m0, n0;               // the tile's first row and channel
+  int lane, wave, wm, wn;   // wm, wn: this wavefront's place in the tile
+
+  // Workgroups go round the eight XCDs: each XCD gets a run of tiles, the rows'
+  // tiles of one run of channels next to each other (they share its L2).
+  __device__ __forceinline__ bool place(int m_tiles, int tiles) {
+    const int tile = (blockIdx.x & 7) * ((tiles + 7) / 8) + (blockIdx.x >> 3);
+    m0 = (tile % m_tiles) * BM;
+    n0 = (tile / m_tiles) * BN;
+    lane = threadIdx.x & (kWave - 1);
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    wm = wave % WM;
+    wn = wave / WM;
+    return tile < tiles;
+  }
+  static __device__ __forceinline__ int turn(int r) { return TK == 64 ? (r >> 1) & 3 : r & 7; }
+  // piece q of this wavefront: the row its lane brings, and which bytes of it
+  __device__ __forceinline__ int row_of(int q, int pieces) const {
+    return (wave * pieces + q) * PR + lane / CH;
+  }
+  __device__ __forceinline__ int byte_of(int r) const { return ((lane % CH) ^ turn(r)) * 16; }
+  static __device__ __forceinline__ int channel_of(int r) {
+    const int i = r & 15, t = (r % (16 * NT)) / 16;
+    return r / (16 * NT) * (16 * NT) + (i >> 2) * (4 * NT) + t * 4 + (i & 3);
+  }
+  // byte offsets of the pieces from the tile's first row; rows past the last
+  // one repeat it (their sums are not stored)
+  template <class T>
+  __device__ __forceinline__ void offsets(const Int8Args& a, T* xo, T* wo) const {
+#pragma unroll
+    for (int q = 0; q < XI; ++q) {
+      const int r = row_of(q, XI);
+      xo[q] = (T)min(r, a.rows - 1 - m0) * (T)a.x_stride + (T)byte_of(r);
+    }
+#pragma unroll
+    for (int q = 0; q < WI; ++q) {
+      const int r = row_of(q, WI);
+      wo[q] = (T)min(channel_of(r), a.vocab - 1 - n0) * (T)a.w_stride + (T)byte_of(r);
+    }
+  }
+  // a partial stage from byte k of the rows on, zero behind their end
+  template <class T>
+  __device__ __forceinline__ void fetch_partial(const Int8Args& a, const int8_t* xb,
+                                                const int8_t* wb, const T* xo, const T* wo, int k,
+                                                int8_t* xs, int8_t* ws) const {
+    uint4 v[XI + WI];
+#pragma unroll
+    for (int q = 0; q < XI; ++q) {
+      const int c = byte_of(row_of(q, XI));
+      v[q] = load_bytes_zero(xb + (xo[q] - (T)c), k + c, a.width);
+    }
+#pragma unroll
+    for (int q = 0; q < WI; ++q) {
+      const int c = byte_of(row_of(q, WI));
+      v[XI + q] = load_bytes_zero(wb + (wo[q] - (T)c), k + c, a.width);
+    }
+    place_pieces(v, v + XI, xs, ws);
+  }
+  __device__ __forceinline__ void place_pieces(const uint4* x, const uint4* w, int8_t* xs,
+                                               int8_t* ws) const {
+#pragma unroll
+    for (int q = 0; q < XI; ++q)
+      *reinterpret_cast<uint4*>(xs + (wave * XI + q) * 1024 + lane * 16) = x[q];
+#pragma unroll
+    for (int q = 0; q < WI; ++q)
+      *reinterpret_cast<uint4*>(ws + (wave * WI + q) * 1024 + lane * 16) = w[q];
+  }
+  // operand q of the NT + MT that product h of a stage takes
+  __device__ __forceinline__ void read(int q, const int8_t* xs, const int8_t* ws, int h, v4i* w,
+                                       v4i* x) const {
+    const int i = lane & 15;
+    const int at = i * TK + (((h * 4 + (lane >> 4)) ^ turn(i)) * 16);
+    if (q < NT)
+      w[q < NT ? q : 0] = *reinterpret_cast<const v4i*>(ws + (wn * NT + q) * 16 * TK + at);
+    else
+      x[q < NT ? 0 : q - NT] =
+          *reinterpret_cast<const v4i*>(xs + (wm * MT + q - NT) * 16 * TK + at);
+  }
+  static __device__ __forceinline__ void clear(v4i (*acc)[MT]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int u = 0; u < MT; ++u) acc[t][u] = v4i{0, 0, 0, 0};
+  }
+  static __device__ __forceinline__ void multiply_row(v4i (*acc)[MT], int u, const v4i* w,
+                                                      const v4i* x) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      acc[t][u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[t], x[u], acc[t][u], 0, 0, 0);
+  }
+  __device__ __forceinline__ void multiply_stage(v4i (*acc)[MT], const int8_t* xs,
+                                                 const int8_t* ws) const {
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      v4i w[NT], x[MT];
+#pragma unroll
+      for (int q = 0; q < NT + MT; ++q) read(q, xs, ws, h, w, x);
+#pragma unroll
+      for (int u = 0; u < MT; ++u) multiply_row(acc, u, w, x);
+      sched_fence();
+    }
+  }
+  // The sum rounded to float32, times the row's scale, then times the channel's
+  // and plus the bias in one rounding; float32 holds far more than the codes do.
+  template <int DT>
+  __device__ __forceinline__ void store(const Int8Args& a, const v4i (*acc)[MT]) const {
+    const int c0 = n0 + wn * (16 * NT) + (lane >> 4) * (4 * NT);
+    float ws[4 * NT], bs[4 * NT];
+#pragma unroll
+    for (int e = 0; e < 4 * NT; ++e) {
+      const int c = min(c0 + e, a.vocab - 1);
+      ws[e] = a.w_scale[c];
+      bs[e] = a.bias ? a.bias[c] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < MT; ++u) {
+      const int r = m0 + (wm * MT + u) * 16 + (lane & 15);
+      if (r >= a.rows) continue;
+      const float xs = a.x_scale[r];
+      float v[4 * NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[t * 4 + e] = fmaf((float)acc[t][u][e] * xs, ws[t * 4 + e], bs[t * 4 + e]);
+      store_row<DT, 4 * NT>(a.out + (long long)r * a.out_stride_bytes, c0, a.vocab, v);
+    }
+  }
+};
+
+// Operands whose rows start at 4-byte words: loads go straight to LDS, RING
+// stages deep. The loads for later lie between the products, so that
+// a wavefront's matrix pipe does not wait while they are issued.
+template <int DT, int BM, int BN, int WM, int WN, int TK, int RING, bool ONCE>
+__global__ __launch_bounds__(WM* WN* kWave, 1) void int8_ring_kernel(Int8Args a, int m_tiles,
+                                                                     int tiles) {
+  using T = Tile<BM, BN, WM, WN, TK>;
+  constexpr int MT = T::MT, NT = T::NT, XI = T::XI, WI = T::WI, H = T::H, DMAS = XI + WI;
+  static_assert(RING >= 2 && RING <= 4 && (RING * H) % 2 == 0, "ring");
+  // one object per operand and stage: only so are loads into one stage known
+  // not to meet reads of another
+  constexpr int XB = BM * TK, WB = BN * TK, X2 = RING > 2 ? XB : 16, W2 = RING > 2 ? WB : 16,
+                X3 = RING > 3 ? XB : 16, W3 = RING > 3 ? WB : 16;
+  __shared__ __attribute__((aligned(1024))) int8_t x0[XB];
+  __shared__ __attribute__((aligned(1024))) int8_t w0[WB];
+  __shared__ __attribute__((aligned(1024))) int8_t x1[XB];
+  __shared__ __attribute__((aligned(1024))) int8_t w1[WB];
+  __shared__ __attribute__((aligned(1024))) int8_t x2[X2];
+  __shared__ __attribute__((aligned(1024))) int8_t w2[W2];
+  __shared__ __attribute__((aligned(1024))) int8_t x3[X3];
+  __shared__ __attribute__((aligned(1024))) int8_t w3[W3];
+  T t;
+  if (!t.place(m_tiles, tiles)) return;
+  const int8_t* xb = a.x + (long long)t.m0 * a.x_stride;
+  const int8_t* wb = a.w + (long long)t.n0 * a.w_stride;
+  // the tile's bytes end with the last byte of its last row
+  const uint32_t xn = (uint32_t)(min(BM, a.rows - t.m0) - 1) * (uint32_t)a.x_stride + a.width;
+  const uint32_t wn = (uint32_t)(min(BN, a.vocab - t.n0) - 1) * (uint32_t)a.w_stride + a.width;
+  uint32_t xo[XI], wo[WI];
+  t.offsets(a, xo, wo);
+  v4i acc[NT][MT];
+  T::clear(acc);
+
+  const int stages = a.width / TK;
+  // piece q of stage b; past the last stage it reads nothing, and is counted
+  // by the waits all the same
+  auto fetch_piece = [&](int q, int b, int8_t* xs, int8_t* ws) {
+    const bool in = b < stages;
+    if (q < XI)
+      to_lds<false>(buffer_of(xb, in ? xn : 0), xs + (t.wave * XI + q) * 1024,
+                    xo[q < XI ? q : 0], in ? b * TK : 0);
+    else
+      to_lds<ONCE>(buffer_of(wb, in ? wn : 0), ws + (t.wave * WI + q - XI) * 1024,
+                   wo[q < XI ? 0 : q - XI], in ? b * TK : 0);
+  };
+  auto fetch = [&](int b, int8_t* xs, int8_t* ws) {
+#pragma unroll
+    for (int q = 0; q < DMAS; ++q) fetch_piece(q, b, xs, ws);
+  };
+  fetch(0, x0, w0);
+  if constexpr (RING > 2) fetch(1, x1, w1);
+  if constexpr (RING > 3) fetch(2, x2, w2);
+  int8_t* const xl = RING == 2 ? x1 : RING == 3 ? x2 : x3;
+  int8_t* const wl = RING == 2 ? w1 : RING == 3 ? w2 : w3;
+  if (stages * TK < a.width) {
+    // a partial stage goes through registers, beside the first whole ones' loads
+    t.fetch_partial(a, xb, wb, xo, wo, stages * TK, xl, wl);
+    __syncthreads();
+    t.multiply_stage(acc, xl, wl);
+    __syncthreads();
+  }
+  if (stages > 0) {
+    fetch(RING - 1, xl, wl);
+    wait_loads<DMAS*(RING - 1)>();
+    __builtin_amdgcn_s_barrier();
+    sched_fence();
+    v4i wv[2][NT], xv[2][MT];
+#pragma unroll
+    for (int q = 0; q < NT + MT; ++q) t.read(q, x0, w0, 0, wv[0], xv[0]);
+    // Stage b = J of a turn of the ring. Its last product meets the next stage,
+    // which has landed for every wavefront behind the barrier; so has
+    // everyone's reading of this one, whose place takes stage b + RING.
+    auto stage = [&](auto j, auto more, int b, int8_t* xs, int8_t* ws, int8_t* xnext,
+                     int8_t* wnext) {
+      constexpr int J = decltype(j)::value, F = J * H;
+      constexpr bool MORE = decltype(more)::value;
+      constexpr bool LAST = !MORE && J + 1 == RING;   // no stage follows
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const bool to_next = h + 1 == H;
+        if (to_next && !LAST) {
+          wait_loads<DMAS*(MORE ? RING - 2 : J + 2 < RING ? RING - 2 - J : 0)>();
+          __builtin_amdgcn_s_barrier();
+          sched_fence();
+        }
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {
+          if (!to_next || !LAST) {
+#pragma unroll
+            for (int q = u * (NT + MT) / MT; q < (u + 1) * (NT + MT) / MT; ++q) {
+              if (to_next)
+                t.read(q, xnext, wnext, 0, wv[(F + h + 1) & 1], xv[(F + h + 1) & 1]);
+              else
+                t.read(q, xs, ws, h + 1, wv[(F + h + 1) & 1], xv[(F + h + 1) & 1]);
+            }
+          }
+          if (MORE && to_next) {
+#pragma unroll
+            for (int q = u * DMAS / MT; q < (u + 1) * DMAS / MT; ++q)
+              fetch_piece(q, b + RING, xs, ws);
+          }
+          T::multiply_row(acc, u, wv[(F + h) & 1], xv[(F + h) & 1]);
+          sched_fence();
+        }
+      }
+    };
+    constexpr std::integral_constant<int, 0> j0{};
+    constexpr std::integral_constant<int, 1> j1{};
+    constexpr std::integral_constant<int, 2> j2{};
+    constexpr std::integral_constant<int, 3> j3{};
+    int b = 0;
+    for (; b + RING < stages; b += RING) {
+      stage(j0, std::true_type{}, b, x0, w0, x1, w1);
+      stage(j1, std::true_type{}, b + 1, x1, w1, RING > 2 ? x2 : x0, RING > 2 ? w2 : w0);
+      if constexpr (RING > 2)
+        stage(j2, std::true_type{}, b + 2, x2, w2, RING > 3 ? x3 : x0, RING > 3 ? w3 : w0);
+      if constexpr (RING > 3) stage(j3, std::true_type{}, b + 3, x3, w3, x0, w0);
+    }
+    // the last turn, of 1 to RING stages
+    stage(j0, std::false_type{}, b, x0, w0, x1, w1);
+    if (b + 1 < stages) {
+      stage(j1, std::false_type{}, b + 1, x1, w1, RING > 2 ? x2 : x0, RING > 2 ? w2 : w0);
+      if constexpr (RING > 2) {
+        if (b + 2 < stages) {
+          stage(j2, std::false_type{}, b + 2, x2, w2, RING > 3 ? x3 : x0, RING > 3 ? w3 : w0);
+          if constexpr (RING > 3) {
+            if (b + 3 < stages) stage(j3, std::false_type{}, b + 3, x3, w3, x0, w0);
+          }
+        }
+      }
+    }
+  }
+  wait_loads<0>();   // none writes LDS that another workgroup has by then
+  t.template store<DT>(a, acc);
+}
+
+// Operands at any byte: loads into registers, put into LDS once the stage
+// before them is multiplied. A 16-byte load that does not start at a 4-byte word
+// runs at a third of the rate (2.0 against 5.0 TB/s from the caches), so a lane
+// loads the four words from the one that holds its first byte on, takes the
+// fifth from the next lane (the last lane of a row loads it), and shifts.
+template <int DT, int BM, int BN, int WM, int WN, int TK>
+__global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(Int8Args a, int m_tiles,
+                                                                  int tiles) {
+  using T = Tile<BM, BN, WM, WN, TK>;
+  constexpr int XI = T::XI, WI = T::WI, N = XI + WI;
+  __shared__ __attribute__((aligned(1024))) int8_t x0[BM * TK];
+  __shared__ __attribute__((aligned(1024))) int8_t x1[BM * TK];
+  __shared__ __attribute__((aligned(1024))) int8_t w0[BN * TK];
+  __shared__ __attribute__((aligned(1024))) int8_t w1[BN * TK];
+  T t;
+  if (!t.place(m_tiles, tiles)) return;
+  const int8_t* xb = a.x + (long long)t.m0 * a.x_stride;
+  const int8_t* wb = a.w + (long long)t.n0 * a.w_stride;
+  uint32_t off[N];
+  t.offsets(a, off, off + XI);
+  v4i acc[T::NT][T::MT];
+  T::clear(acc);
+  const int stages = a.width / TK;
+  if (stages * TK < a.width) {   // a partial stage first
+    t.fetch_partial(a, xb, wb, off, off + XI, stages * TK, x1, w1);
+    __syncthreads();
+    t.multiply_stage(acc, x1, w1);
+  }
+
+  // from here on lane c of a row's lanes brings chunk c
+  const int c = t.lane % T::CH;
+  const bool last = c == T::CH - 1;
+  int at[N];       // where it goes in LDS
+  uint32_t skew = 0;   // bytes of the first word before the chunk, 2 bits a piece
+  static_assert(N <= 16, "pieces");
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const int r = q < XI ? t.row_of(q, XI) : t.row_of(q - XI, WI);
+    off[q] = off[q] - t.byte_of(r) + c * 16;
+    at[q] = r * TK + (c ^ T::turn(r)) * 16;
+    const uint32_t s = ((uint32_t)(uintptr_t)(q < XI ? xb : wb) + off[q]) & 3;
+    skew |= s << (2 * q);
+  }
+  uint4 v[N];
+  uint32_t fifth[N];
+  auto fetch = [&](int b) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const uint32_t s = (skew >> (2 * q)) & 3;
+      const int8_t* p = (q < XI ? xb : wb) + (long long)b * TK + ((long long)off[q] - s);
+      const Words4 w = *reinterpret_cast<const Words4*>(p);
+      v[q] = make_uint4(w.x, w.y, w.z, w.w);
+      fifth[q] = 0;
+      if (last && s != 0) fifth[q] = *reinterpret_cast<const uint32_t*>(p + 16);
+    }
+  };
+  auto put = [&](int8_t* xs, int8_t* ws) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const uint32_t s = (skew >> (2 * q)) & 3;
+      const uint32_t next = dpp_u32<0x101 /* row_shl:1: the next lane's */>(v[q].x);
+      const uint32_t e = last ? fifth[q] : next;
+      *reinterpret_cast<uint4*>((q < XI ? xs : ws) + at[q]) =
+          make_uint4(__builtin_amdgcn_alignbyte(v[q].y, v[q].x, s),
+                     __builtin_amdgcn_alignbyte(v[q].z, v[q].y, s),
+                     __builtin_amdgcn_alignbyte(v[q].w, v[q].z, s),
+                     __builtin_amdgcn_alignbyte(e, v[q].w, s));
+    }
+  };
+  if (stages > 0) {
+    fetch(0);
+    put(x0, w0);
+    __syncthreads();
+    int b = 0;
+    for (; b + 2 < stages; b += 2) {
+      fetch(b + 1);
+      t.multiply_stage(acc, x0, w0);
+      put(x1, w1);
+      __syncthreads();
+      fetch(b + 2);
+      t.multiply_stage(acc, x1, w1);
+      put(x0, w0);
+      __syncthreads();
+    }
+    const bool two = b + 1 < stages;
+    if (two) fetch(b + 1);
+    t.multiply_stage(acc, x0, w0);
+    if (two) {
+      put(x1, w1);
+      __syncthreads();
+      t.multiply_stage(acc, x1, w1);
+    }
+  }
+  t.template store<DT>(a, acc);
+}
+
+template <int BM, int BN>
+void tiles_of(const Int8Args& a, int* m_tiles, int* tiles) {
+  *m_tiles = (a.rows + BM - 1) / BM;
+  *tiles = *m_tiles * ((a.vocab + BN - 1) / BN);
+}
+
+template <int DT, int BM, int BN, int WM, int WN, int TK, int RING, bool ONCE>
+hipError_t launch_ring(const Int8Args& a, hipStream_t s) {
+  int m_tiles, tiles;
+  tiles_of<BM, BN>(a, &m_tiles, &tiles);
+  hipLaunchKernelGGL((int8_ring_kernel<DT, BM, BN, WM, WN, TK, RING, ONCE>),
+                     dim3((tiles + 7) / 8 * 8), dim3(WM * WN * kWave), 0, s, a, m_tiles, tiles);
+  return hipGetLastError();
+}
+
+template <int DT, int BM, int BN, int WM, int WN, int TK>
+hipError_t launch_tile(const Int8Args& a, hipStream_t s) {
+  int m_tiles, tiles;
+  tiles_of<BM, BN>(a, &m_tiles, &tiles);
+  hipLaunchKernelGGL((int8_tile_kernel<DT, BM, BN, WM, WN, TK>), dim3((tiles + 7) / 8 * 8),
+                     dim3(WM * WN * kWave), 0, s, a, m_tiles, tiles);
+  return hipGetLastError();
+}
+
+// Tile shapes for more than 64 rows: how many run at once (one or two to a
+// compute unit) and how long one round of them takes, in us at width 4096.
+struct TileCost {
+  int bm, bn, at_once, us;
+};
+constexpr TileCost kTileCost[] = {{256, 256, 256, 57}, {192, 256, 256, 47}, {128, 256, 256, 33},
+                                  {160, 128, 512, 39}, {128, 128, 512, 37}};
+
+// The shape with the least rounds' time. A last round that leaves every second
+// place empty takes 0.6 of a full one. Measured at width 4096 (us): 256 x 32000
+// 128x256 40, 128x128 46, 160x128 48, 256x256 66; 320 x 32000 160x128 53, 192x256
+// 55, 256x256 60; 384 x 32000 192x256 57, 256x256 61; 128 x 32000 128x128 36,
+// 128x256 39; 128 x 128256 128x256 117, 128x128 131; 1024 x 151936 256x256 566,
+// 128x256 622, 160x128 659, 128x128 698.
+inline int pick_tile(int rows, int vocab) {
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < 5; ++i) {
+    const TileCost& c = kTileCost[i];
+    const long long tiles =
+        (long long)((rows + c.bm - 1) / c.bm) * ((vocab + c.bn - 1) / c.bn);
+    const long long rest = tiles % c.at_once;
+    const double rounds = (double)(tiles / c.at_once) +
+                          (rest == 0 ? 0.0 : c.at_once == 512 && rest <= 256 ? 0.6 : 1.0);
+    if (i == 0 || rounds * c.us < least) {
+      best = i;
+      least = rounds * c.us;
+    }
+  }
+  return best;
+}
+
+// ONCE where the rows' lines are whole (a line that two loads share would be
+// read twice): 1 x 128256 x 4096 78 us against 84, with rows 4100 apart 92
+// against 84.
+template <int DT, bool LINES>
+hipError_t launch_direct(const Int8Args& a, hipStream_t s) {
+  if (a.rows <= 16) return launch_ring<DT, 16, 64, 1, 4, 256, 4, LINES>(a, s);
+  if (a.rows <= 32) return launch_ring<DT, 32, 64, 1, 4, 256, 2, LINES>(a, s);
+  if (a.rows <= 64) return launch_ring<DT, 64, 128, 1, 4, 128, 3, LINES>(a, s);
+  switch (pick_tile(a.rows, a.vocab)) {
+    case 0: return launch_ring<DT, 256, 256, 2, 4, 128, 2, false>(a, s);
+    case 1: return launch_ring<DT, 192, 256, 2, 4, 128, 2, false>(a, s);
+    case 2: return launch_ring<DT, 128, 256, 2, 4, 128, 3, LINES>(a, s);
+    case 3: return launch_ring<DT, 160, 128, 2, 2, 128, 2, false>(a, s);
+    default: return launch_ring<DT, 128, 128, 2, 2, 128, 2, LINES>(a, s);
+  }
+}
+
+template <int DT>
+hipError_t launch_int8_dt(const Int8Args& a, hipStream_t s) {
+  auto multiple = [&](int n) {
+    return a.x_stride % n == 0 && a.w_stride % n == 0 && (uintptr_t)a.x % n == 0 &&
+           (uintptr_t)a.w % n == 0;
+  };
+  if (multiple(128)) return launch_direct<DT, true>(a, s);
+  if (multiple(4)) return launch_direct<DT, false>(a, s);
+  // measured at width 4095 (us): 1 x 128256 93 (64 rows a tile 109), 30 x 128256 115
+  // (123, 128x128 127), 64 x 128256 138 (128x128 141), 700 x 50001 263 (256x128 279)
+  if (a.rows <= 16) return launch_tile<DT, 16, 64, 1, 4, 256>(a, s);
+  if (a.rows <= 32) return launch_tile<DT, 32, 64, 1, 4, 256>(a, s);
+  if (a.rows <= 64) return launch_tile<DT, 64, 64, 1, 4, 256>(a, s);
+  return launch_tile<DT, 128, 128, 2, 2, 128>(a, s);
+}
+
+}  // namespace tsr

@@ -1,4 +1,5 @@
-// The sample_rows and verify front doors (element type dispatch) and the Philox test hook.
+// The sample_rows, verify and int8_logits front doors (element type dispatch) and the Philox
+// test hook.
 #include "dispatch.hpp"
 
 namespace tsr {
@@ -102,6 +103,13 @@ hipError_t launch_sample(const void* logits, int dtype, int rows, int V, long lo
   const unsigned char* p = static_cast<const unsigned char*>(logits);
   return dtype == 0 ? launch_sample_dt0(p, rows, V, stride_bytes, ragged, kp, out, dg, s)
                     : launch_sample_dt1(p, rows, V, stride_bytes, ragged, kp, out, dg, s);
+}
+
+hipError_t launch_int8_dt0(const Int8Args& a, hipStream_t s);
+hipError_t launch_int8_dt1(const Int8Args& a, hipStream_t s);
+
+hipError_t launch_int8(const Int8Args& a, int dtype, hipStream_t s) {
+  return dtype == 0 ? launch_int8_dt0(a, s) : launch_int8_dt1(a, s);
 }
 
 hipError_t launch_philox(const uint32_t* ctr, int n, uint32_t k0, uint32_t k1, uint32_t* out,

@@ -15,6 +15,9 @@ __device__ __forceinline__ uint4 load16(const void* p) {
   return make_uint4(b.w[0], b.w[1], b.w[2], b.w[3]);
 }
 
+// Four words at a word boundary.
+typedef uint32_t Words4 __attribute__((ext_vector_type(4), aligned(4)));
+
 template <int N>
 __device__ __forceinline__ void store_words(void* p, const uint32_t* w) {
   static_assert(N == 1 || N == 2 || N == 4, "words");
@@ -47,35 +50,32 @@ __device__ __forceinline__ uint4 load_chunk_zero(const unsigned char* row, long 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Bytes [k, k + 16) of a row of n bytes; those at or past n read as 0. Where
-// the row ends inside them: the row's last 16 bytes, shifted down.
+// Bytes [k, k + 16) of a row of n bytes; those at or past n read as 0. Without
+// a branch where n >= 16: the last 16 bytes of the row at most, shifted down by
+// those before k.
 __device__ __forceinline__ uint4 load_bytes_zero(const int8_t* row, int k, int n) {
-  if (k + 16 <= n) return load16(row + k);
-  uint64_t lo = 0, hi = 0;
-  if (k < n) {
-    if (n >= 16) {
-      const uint4 v = load16(row + n - 16);
-      lo = v.x | (uint64_t)v.y << 32;
-      hi = v.z | (uint64_t)v.w << 32;
-      const int s = (k + 16 - n) * 8;   // 8 .. 120 bits
-      if (s >= 64) {
-        lo = hi >> (s - 64);
-        hi = 0;
-      } else {
-        lo = lo >> s | hi << (64 - s);
-        hi >>= s;
-      }
-    } else {   // k is 0
+  if (n < 16) {
+    uint64_t lo = 0, hi = 0;
 #pragma unroll 1
-      for (int e = 0; e < n; ++e) {
-        const uint64_t byte = (uint8_t)row[e];
-        if (e < 8)
-          lo |= byte << (8 * e);
-        else
-          hi |= byte << (8 * (e - 8));
-      }
+    for (int e = k; e < n; ++e) {
+      const uint64_t byte = (uint8_t)row[e];
+      if (e - k < 8)
+        lo |= byte << (8 * (e - k));
+      else
+        hi |= byte << (8 * (e - k - 8));
     }
+    return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
   }
+  const int at = min(k, n - 16);
+  const uint4 v = load16(row + at);
+  const int s = min(k - at, 16) * 8;   // 0 .. 128 bits
+  uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+  lo = s >= 64 ? hi : lo;
+  hi = s >= 64 ? 0 : hi;
+  const int r = s & 63;
+  lo = r ? lo >> r | hi << (64 - r) : lo;
+  hi >>= r;
+  if (s >= 128) lo = 0;
   return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
 }
 
