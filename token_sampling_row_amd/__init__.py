@@ -179,27 +179,37 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
 
+_torch = None
+_current_raw = None   # the C getter of a device's current stream, where torch has it
+
+
+def _t():
+    """torch, imported at the first call that needs it."""
+    global _torch, _current_raw
+    if _torch is None:
+        import torch
+        _torch = torch
+        _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return _torch
+
+
 def _stream_on(device, stream):
     """A raw stream handle: `stream`, or the current stream of `device` (which
     need not be the current device)."""
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    getter = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return getter(device) if getter is not None else torch.cuda.current_stream(device).cuda_stream
+    if _current_raw is not None:
+        return _current_raw(device)
+    return _t().cuda.current_stream(device).cuda_stream
 
 
-def _made_on(stream):
-    """The context in which a call allocates what it returns: on the stream that
-    writes it, so that memory freed on the current stream is not taken early."""
-    import contextlib
-    import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _new(stream, device, dtype, *shape):
+    """A tensor that a call returns, allocated on the stream that writes it, so
+    that memory freed on the current stream is not taken early."""
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 def pack_row_params(params_list):
@@ -416,80 +426,79 @@ class Sampler:
 
     # 8-bit projection and verification from probabilities. Tensors of other
     # shapes, types or devices than the kernels take raise ValueError (TypeError
-    # for a type of logits, hidden states or probabilities).
+    # for a type of logits, hidden states or probabilities). The checks are
+    # written out where they are made: small batches are bound by host time.
+    def _rows(self, t, rows, width, what):
+        """Row stride of t, a [rows, width] matrix of contiguous rows that do not
+        overlap, on the handle's GPU."""
+        if t.shape != (rows, width) or t.get_device() != self.device or width < 1:
+            raise ValueError(f"{what}: not [{rows}, {width}] on the handle's GPU")
+        stride = t.stride(0)
+        if (width > 1 and t.stride(1) != 1) or (rows > 1 and stride < width):
+            raise ValueError(f"{what}: rows not contiguous, or overlapping")
+        return stride if stride > width else width
+
+    def _vector(self, t, dtype, what, *shape):
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or \
+                t.get_device() != self.device:
+            raise ValueError(f"{what}: not a contiguous {list(shape)} {dtype} on the handle's GPU")
+        return t.data_ptr()
+
+    def _codes(self, codes, scale, rows, width, what):
+        if codes.dtype is not _torch.int8:
+            raise ValueError(f"{what}: not int8")
+        self._vector(scale, _torch.float32, what, rows)
+        return self._rows(codes, rows, width, what)
+
     def quantize_rows(self, x, out=None, scale=None, stream=None):
         """x [rows, W] float32 or bfloat16 (rows contiguous, any row stride) ->
         (codes [rows, W] int8, scale [rows] float32): absmax codes per row."""
-        import torch
+        torch = _t()
         dt = _dtype_code(x)
-        _need(x.dim() == 2 and x.shape[1] > 0 and x.stride(1) == 1 and
-              (x.shape[0] < 2 or x.stride(0) >= x.shape[1]) and x.get_device() == self.device,
-              "x: [rows, width] rows on the handle's GPU, none overlapping")
+        if x.dim() != 2:
+            raise ValueError("x: not a matrix")
         rows, width = x.shape
-        if out is None or scale is None:
-            with _made_on(stream):
-                out = torch.empty(rows, width, dtype=torch.int8, device=x.device) \
-                    if out is None else out
-                scale = torch.empty(rows, dtype=torch.float32, device=x.device) \
-                    if scale is None else scale
-        self._check_codes(out, scale, rows, width, "out")
-        if rows == 0:
-            return out, scale
-        _check(load_library().quantize_rows(
-            self._h, x.data_ptr(), dt, rows, width, max(x.stride(0), width), out.data_ptr(),
-            max(out.stride(0), width), scale.data_ptr(), _stream_on(self.device, stream)),
-            "quantize_rows")
+        xs = self._rows(x, rows, width, "x")
+        if out is None:
+            out = _new(stream, x.device, torch.int8, rows, width)
+        if scale is None:
+            scale = _new(stream, x.device, torch.float32, rows)
+        stride = self._codes(out, scale, rows, width, "out")
+        if rows:
+            _check(load_library().quantize_rows(
+                self._h, x.data_ptr(), dt, rows, width, xs, out.data_ptr(), stride,
+                scale.data_ptr(), _stream_on(self.device, stream)), "quantize_rows")
         return out, scale
 
-    def _check_codes(self, codes, scale, rows, width, what):
-        import torch
-        _need(codes.dtype is torch.int8 and codes.dim() == 2 and codes.shape[0] == rows and
-              codes.shape[1] == width and codes.stride(1) == 1 and
-              (rows < 2 or codes.stride(0) >= width) and codes.get_device() == self.device,
-              f"{what}: [{rows}, {width}] int8 rows on the handle's GPU")
-        _need(scale.dtype is torch.float32 and scale.dim() == 1 and scale.shape[0] == rows and
-              scale.is_contiguous() and scale.get_device() == self.device,
-              f"{what}'s scale: [{rows}] float32 on the handle's GPU")
-
     def _head(self, weight, w_scale, bias):
-        import torch
-        _need(weight.dim() == 2 and weight.shape[0] > 0 and weight.shape[1] > 0,
-              "weight: [vocab, width]")
+        if weight.dim() != 2:
+            raise ValueError("weight: not [vocab, width]")
         vocab, width = weight.shape
-        self._check_codes(weight, w_scale, vocab, width, "weight")
-        if bias is not None:
-            _need(bias.dtype is torch.float32 and bias.dim() == 1 and bias.shape[0] == vocab and
-                  bias.is_contiguous() and bias.get_device() == self.device,
-                  f"bias: [{vocab}] float32 on the handle's GPU")
-        return _Head(weight.data_ptr(), max(weight.stride(0), width), w_scale.data_ptr(),
-                     None if bias is None else bias.data_ptr(), vocab, width)
-
-    def _logits_out(self, out, rows, vocab, dtype, like, stream):
-        import torch
-        if out is None:
-            with _made_on(stream):
-                return torch.empty(rows, vocab, dtype=dtype, device=like.device)
-        _need(out.dim() == 2 and out.shape[0] == rows and out.shape[1] == vocab and
-              out.stride(1) == 1 and (rows < 2 or out.stride(0) >= vocab) and
-              out.get_device() == self.device, f"out: [{rows}, {vocab}] rows on the handle's GPU")
-        return out
+        stride = self._codes(weight, w_scale, vocab, width, "weight")
+        if vocab < 1:
+            raise ValueError("weight: no channel")
+        b = None if bias is None else self._vector(bias, _torch.float32, "bias", vocab)
+        return _Head(weight.data_ptr(), stride, w_scale.data_ptr(), b, vocab, width)
 
     def int8_logits(self, codes, scale, weight, w_scale, bias=None, dtype=None, out=None,
                     stream=None):
         """codes [rows, W] and weight [V, W] int8 with their scales (see
         quantize_rows), bias [V] float32 or None -> logits [rows, V], of `dtype`
         (float32 or bfloat16, the default) or in `out`."""
-        import torch
+        torch = _t()
         head = self._head(weight, w_scale, bias)
-        rows = codes.shape[0]
-        self._check_codes(codes, scale, rows, head.width, "codes")
-        out = self._logits_out(out, rows, head.vocab, dtype or torch.bfloat16, codes, stream)
-        if rows == 0:
-            return out
-        _check(load_library().int8_logits(
-            self._h, codes.data_ptr(), max(codes.stride(0), head.width), scale.data_ptr(), rows,
-            ctypes.byref(head), out.data_ptr(), _dtype_code(out), max(out.stride(0), head.vocab),
-            _stream_on(self.device, stream)), "int8_logits")
+        rows, vocab = codes.shape[0], head.vocab
+        stride = self._codes(codes, scale, rows, head.width, "codes")
+        if out is None:
+            out = _new(stream, codes.device, dtype or torch.bfloat16, rows, vocab)
+            out_stride = vocab
+        else:
+            out_stride = self._rows(out, rows, vocab, "out")
+        dt = _dtype_code(out)
+        if rows:
+            _check(load_library().int8_logits(
+                self._h, codes.data_ptr(), stride, scale.data_ptr(), rows, ctypes.byref(head),
+                out.data_ptr(), dt, out_stride, _stream_on(self.device, stream)), "int8_logits")
         return out
 
     def sample_hidden(self, hidden, weight, w_scale, params, step: int, bias=None, dtype=None,
@@ -498,45 +507,36 @@ class Sampler:
         int8_logits and sample_rows in one call. ``logits``: a preallocated
         contiguous [rows, V] tensor for the logits, or None (then of `dtype`,
         bfloat16 by default); ``diag`` as in sample_rows."""
-        import torch
+        torch = _t()
         hdt = _dtype_code(hidden)
         head = self._head(weight, w_scale, bias)
-        rows, dev = hidden.shape[0], hidden.device
-        _need(hidden.dim() == 2 and hidden.shape[1] == head.width and hidden.stride(1) == 1 and
-              (hidden.shape[0] < 2 or hidden.stride(0) >= head.width) and
-              hidden.get_device() == self.device,
-              f"hidden: [rows, {head.width}] rows on the handle's GPU")
-        logits = self._logits_out(logits, rows, head.vocab, dtype or torch.bfloat16, hidden, stream)
-        _need(logits.is_contiguous(), "logits: contiguous")
-        with _made_on(stream):
-            codes = torch.empty(rows, head.width, dtype=torch.int8, device=dev)
-            scale = torch.empty(rows, dtype=torch.float32, device=dev)
-            out = torch.empty(rows, dtype=torch.int32, device=dev) if out is None else out
-        self._check_ints(out, (rows,), "out")
+        if hidden.dim() != 2:
+            raise ValueError("hidden: not a matrix")
+        rows, dev, vocab = hidden.shape[0], hidden.device, head.vocab
+        stride = self._rows(hidden, rows, head.width, "hidden")
+        if logits is None:
+            logits = _new(stream, dev, dtype or torch.bfloat16, rows, vocab)
+        elif self._rows(logits, rows, vocab, "logits") != vocab:
+            raise ValueError("logits: not contiguous")
+        ldt = _dtype_code(logits)
+        codes = _new(stream, dev, torch.int8, rows, head.width)
+        scale = _new(stream, dev, torch.float32, rows)
+        if out is None:
+            out = _new(stream, dev, torch.int32, rows)
+        else:
+            self._vector(out, torch.int32, "out", rows)
         cp = Params.of(params)._c()
         d = None
         if diag is not None:
             d = _Diag(*(ctypes.c_void_p(diag[k].data_ptr()) if diag.get(k) is not None else None
                         for k in ("status", "kept_count", "threshold", "kept_mass", "probs")))
-        if rows == 0:
-            return out
-        _check(load_library().sample_hidden(
-            self._h, hidden.data_ptr(), hdt, rows, max(hidden.stride(0), head.width),
-            ctypes.byref(head), codes.data_ptr(), scale.data_ptr(), logits.data_ptr(),
-            _dtype_code(logits), ctypes.byref(cp), int(step), out.data_ptr(),
-            ctypes.byref(d) if d is not None else None, _stream_on(self.device, stream)),
-            "sample_hidden")
+        if rows:
+            _check(load_library().sample_hidden(
+                self._h, hidden.data_ptr(), hdt, rows, stride, ctypes.byref(head),
+                codes.data_ptr(), scale.data_ptr(), logits.data_ptr(), ldt, ctypes.byref(cp),
+                int(step), out.data_ptr(), ctypes.byref(d) if d is not None else None,
+                _stream_on(self.device, stream)), "sample_hidden")
         return out
-
-    def _check_ints(self, t, shape, what):
-        import torch
-        _need(t.dtype is torch.int32 and t.shape == shape and t.is_contiguous() and
-              t.get_device() == self.device, f"{what}: {list(shape)} int32 on the handle's GPU")
-
-    def _check_floats(self, t, shape, what):
-        import torch
-        _need(t.dtype is torch.float32 and t.shape == shape and t.is_contiguous() and
-              t.get_device() == self.device, f"{what}: {list(shape)} float32 on the handle's GPU")
 
     def verify_probs(self, target, draft, draft_tokens, accept_u, draw_u, draft_lens=None,
                      out_tokens=None, out_accepted=None, out_status=None, stream=None):
@@ -545,42 +545,42 @@ class Sampler:
         proposed with certainty) float32 or bfloat16, draft_tokens [rows, K] and
         draft_lens [rows] (None: K each) int32, accept_u [rows, K] and draw_u
         [rows] float32 in [0, 1) -> (tokens [rows, K+1], accepted [rows])."""
-        import torch
+        torch = _t()
+        i32, f32, dev = torch.int32, torch.float32, self.device
         dt = _dtype_code(target)
-        _need(target.dim() == 3 and target.stride(2) == 1 and target.shape[1] > 1 and
-              target.get_device() == self.device,
-              "target: [rows, K + 1, vocab] rows on the handle's GPU")
+        if target.dim() != 3 or target.get_device() != dev:
+            raise ValueError("target: not [rows, K + 1, vocab] on the handle's GPU")
         rows, k1, vocab = target.shape
+        t_seq, t_row, one = target.stride()
+        if k1 < 2 or vocab < 1 or (one != 1 and vocab > 1):
+            raise ValueError("target: not rows of contiguous probabilities, two at least")
         K = k1 - 1
+        d_ptr, d_seq, d_row = None, 0, 0
         if draft is not None:
-            _need(draft.dtype is target.dtype and draft.shape == (rows, K, vocab) and
-                  draft.stride(2) == 1 and draft.get_device() == self.device,
-                  f"draft: [{rows}, {K}, {vocab}] of the target's type on the handle's GPU")
-        self._check_ints(draft_tokens, (rows, K), "draft_tokens")
-        self._check_floats(accept_u, (rows, K), "accept_u")
-        self._check_floats(draw_u, (rows,), "draw_u")
-        if draft_lens is not None:
-            self._check_ints(draft_lens, (rows,), "draft_lens")
-        if out_tokens is None or out_accepted is None:
-            with _made_on(stream):
-                out_tokens = torch.empty(rows, k1, dtype=torch.int32, device=target.device) \
-                    if out_tokens is None else out_tokens
-                out_accepted = torch.empty(rows, dtype=torch.int32, device=target.device) \
-                    if out_accepted is None else out_accepted
-        self._check_ints(out_tokens, (rows, k1), "out_tokens")
-        self._check_ints(out_accepted, (rows,), "out_accepted")
-        if out_status is not None:
-            self._check_ints(out_status, (rows,), "out_status")
-        if rows == 0:
-            return out_tokens, out_accepted
-        _check(load_library().verify_probs(
-            self._h, target.data_ptr(), target.stride(0), target.stride(1),
-            None if draft is None else draft.data_ptr(), 0 if draft is None else draft.stride(0),
-            0 if draft is None else draft.stride(1), dt, draft_tokens.data_ptr(),
-            None if draft_lens is None else draft_lens.data_ptr(), accept_u.data_ptr(),
-            draw_u.data_ptr(), rows, K, vocab, out_tokens.data_ptr(), out_accepted.data_ptr(),
-            None if out_status is None else out_status.data_ptr(),
-            _stream_on(self.device, stream)), "verify_probs")
+            d_seq, d_row, one = draft.stride() if draft.dim() == 3 else (0, 0, 0)
+            if draft.shape != (rows, K, vocab) or draft.dtype is not target.dtype or \
+                    (one != 1 and vocab > 1) or draft.get_device() != dev:
+                raise ValueError(f"draft: not [{rows}, {K}, {vocab}] rows of the target's type "
+                                 "on the handle's GPU")
+            d_ptr = draft.data_ptr()
+        x_ptr = self._vector(draft_tokens, i32, "draft_tokens", rows, K)
+        u_ptr = self._vector(accept_u, f32, "accept_u", rows, K)
+        v_ptr = self._vector(draw_u, f32, "draw_u", rows)
+        n_ptr = None if draft_lens is None else self._vector(draft_lens, i32, "draft_lens", rows)
+        s_ptr = None if out_status is None else self._vector(out_status, i32, "out_status", rows)
+        if out_tokens is None:
+            out_tokens = _new(stream, target.device, i32, rows, k1)
+        else:
+            self._vector(out_tokens, i32, "out_tokens", rows, k1)
+        if out_accepted is None:
+            out_accepted = _new(stream, target.device, i32, rows)
+        else:
+            self._vector(out_accepted, i32, "out_accepted", rows)
+        if rows:
+            _check(load_library().verify_probs(
+                self._h, target.data_ptr(), t_seq, t_row, d_ptr, d_seq, d_row, dt, x_ptr, n_ptr,
+                u_ptr, v_ptr, rows, K, vocab, out_tokens.data_ptr(), out_accepted.data_ptr(),
+                s_ptr, _stream_on(dev, stream)), "verify_probs")
         return out_tokens, out_accepted
 
     def philox(self, counters, stream=None):

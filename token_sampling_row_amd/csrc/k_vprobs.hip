@@ -6,9 +6,19 @@
 namespace tsr {
 namespace {
 
-constexpr int kVpWaves = 16;
-constexpr int kVpBlock = kVpWaves * kWave;
-constexpr int kVpSteps = 1024;   // most steps a row is cut into
+// Wavefronts of the one-launch kernel: sixteen where a span's registers allow.
+template <int DT> constexpr int kVpWaves = DT == 0 ? 16 : 8;
+constexpr int kVpSliceWaves = 4;
+constexpr int kVpSliceBlock = kVpSliceWaves * kWave;
+constexpr int kVpGroup = 4;   // spans of a group; a wavefront has two groups' loads on their way
+
+// How many workgroups share a row's sums (1: the one-launch kernel).
+int vp_slices(int rows, int groups, int ws_rows) {
+  if (rows > ws_rows || groups <= 32) return 1;
+  const int want = (1024 + rows - 1) / rows;
+  const int most = (groups + 2 * kVpSliceWaves - 1) / (2 * kVpSliceWaves);
+  return want < most ? want : most;
+}
 
 // What the K tests of one sequence decide.
 struct VpCut {
@@ -17,6 +27,7 @@ struct VpCut {
   int refused;   // whether draft `kept` was refused (else all were kept)
   int token;     // that draft's token
   int x;         // this lane's draft token
+  float v;       // the uniform of the draw
 };
 
 // The tests of sequence b, lane j < 32 taking draft j: kept iff u q(x) < p(x)
@@ -29,11 +40,12 @@ __device__ __forceinline__ VpCut vp_cut(const VprobsArgs& a, int b, int lane) {
   const bool mine = lane < len && lane < a.K;
   c.x = mine ? a.tokens[(long long)b * a.K + lane] : 0;
   const bool out = mine && (c.x < 0 || c.x >= a.V);
-  float p = 0.0f, q = 1.0f, u = 0.0f;
+  const float u = mine ? a.accept_u[(long long)b * a.K + lane] : 0.0f;
+  c.v = a.draw_u[b];
+  float p = 0.0f, q = 1.0f;
   if (mine && !out) {
     p = load_elem<DT>(a.target + b * a.t_seq + lane * a.t_row, c.x);
     if (a.draft) q = load_elem<DT>(a.draft + b * a.d_seq + lane * a.d_row, c.x);
-    u = a.accept_u[(long long)b * a.K + lane];
   }
   const bool keep = mine && !out && (double)u * (double)q < (double)p;
   const unsigned long long refuse = __ballot(mine && !keep);
@@ -43,117 +55,224 @@ __device__ __forceinline__ VpCut vp_cut(const VprobsArgs& a, int b, int lane) {
   const bool seen = mine && lane <= c.kept;
   const unsigned long long bad_p =
       __ballot(seen && !(p >= 0.0f && p <= kFltMax && q >= 0.0f && q <= kFltMax));
-  const float v = a.draw_u[b];
   const unsigned long long bad_u =
-      __ballot((seen && !(u >= 0.0f && u < 1.0f)) || !(v >= 0.0f && v < 1.0f));
+      __ballot((seen && !(u >= 0.0f && u < 1.0f)) || !(c.v >= 0.0f && c.v < 1.0f));
   c.token = (int)readlane_u32((uint32_t)c.x, c.kept & 31);
   c.status = (len < 0 || len > a.K) ? 4 : bad_x ? 3 : bad_p ? 1 : bad_u ? 4 : 0;
   return c;
 }
 
-// Weights of one chunk of the row that is drawn from, in 64 bits: the target's
-// probabilities, less the draft's (SUB 1) or less the certain draft `x` (SUB
-// 2). Returns their sum; NaN where a value read is no probability.
+// The row that is drawn from, cut into spans of 64 chunks (one a lane) and
+// groups of kVpGroup x rep spans.
+struct VpRow {
+  const unsigned char* p;   // the target's row
+  const unsigned char* q;   // the draft's, where it is taken off (SUB 1)
+  int V;
+  int x;                    // the token whose certain draft is taken off (SUB 2)
+  int rep, groups;
+};
+template <int DT>
+__device__ __forceinline__ VpRow vp_row(const VprobsArgs& a, int b, int kept, int x, int rep,
+                                        int groups) {
+  return VpRow{a.target + b * a.t_seq + kept * a.t_row,
+               a.draft ? a.draft + b * a.d_seq + kept * a.d_row : nullptr, a.V, x, rep, groups};
+}
+
+// Weights of one chunk in 64 bits: the target's probabilities, less the draft's
+// (SUB 1) or less the certain draft x (SUB 2). Returns their sum; NaN where a
+// value read is no probability. The bits of a float in [0, largest] are at
+// most 0x7F7FFFFF as an integer; a larger maximum is looked at again (it may be
+// a negative zero).
 template <int DT, int SUB>
 __device__ __forceinline__ double vp_weights(uint4 pr, uint4 qr, int e0, int x, double* w) {
   constexpr int EPC = Fmt<DT>::EPC;
   float p[EPC], q[EPC];
   unpack<DT>(pr, p);
   if constexpr (SUB == 1) unpack<DT>(qr, q);
-  bool ok = true;
+  uint32_t top = 0;
   double sum = 0.0;
 #pragma unroll
   for (int e = 0; e < EPC; ++e) {
-    ok = ok && p[e] >= 0.0f && p[e] <= kFltMax;
+    top = max(top, __float_as_uint(p[e]));
     double d = (double)p[e];
     if constexpr (SUB == 1) {
-      ok = ok && q[e] >= 0.0f && q[e] <= kFltMax;
+      top = max(top, __float_as_uint(q[e]));
       d = fmax(d - (double)q[e], 0.0);
     }
     if constexpr (SUB == 2) d = e0 + e == x ? fmax(d - 1.0, 0.0) : d;
     w[e] = d;
     sum += d;
   }
-  return ok ? sum : __builtin_nan("");
+  if (top > 0x7F7FFFFFu) {
+#pragma unroll
+    for (int e = 0; e < EPC; ++e) {
+      const bool ok = p[e] >= 0.0f && p[e] <= kFltMax &&
+                      (SUB != 1 || (q[e] >= 0.0f && q[e] <= kFltMax));
+      if (!ok) sum = __builtin_nan("");
+    }
+  }
+  return sum;
 }
 
-// Sums of the steps wave, wave + waves, ... of a row into `sums`; a step is
-// `rep` times 64 chunks.
+// kVpGroup spans from span s0 on: the chunks this lane has of them. All loads
+// are on their way together; spans past the row's whole ones repeat the last
+// of those (`in` tells), the partial one is loaded by itself.
 template <int DT, int SUB>
-__device__ __forceinline__ void vp_sums(const unsigned char* prow, const unsigned char* qrow, int V,
-                                        int x, int first, int stride, int steps, int rep,
-                                        int lane, double* sums) {
-  constexpr int EPC = Fmt<DT>::EPC;
-  for (int s = first; s < steps; s += stride) {
-    double sum = 0.0;
-    for (int k = 0; k < rep; ++k) {
-      const int e0 = ((s * rep + k) * kWave + lane) * EPC;
-      const uint4 pr = load_chunk_zero<DT>(prow, e0, V);
-      uint4 qr{};
-      if constexpr (SUB == 1) qr = load_chunk_zero<DT>(qrow, e0, V);
-      double w[EPC];
-      sum += vp_weights<DT, SUB>(pr, qr, e0, x, w);
+struct VpGroup {
+  uint4 p[kVpGroup], q[SUB == 1 ? kVpGroup : 1];
+  __device__ __forceinline__ void load(const VpRow& r, int s0, int lane) {
+    constexpr int EPC = Fmt<DT>::EPC, ESZ = Fmt<DT>::ESZ, SPAN = kWave * EPC;
+    const int whole = r.V / SPAN;
+    if (whole > 0) {
+#pragma unroll
+      for (int i = 0; i < kVpGroup; ++i) {
+        const long long at = (long long)min(s0 + i, whole - 1) * (SPAN * ESZ);   // the same in all lanes
+        p[i] = load16(r.p + at + lane * 16);
+        if constexpr (SUB == 1) q[i] = load16(r.q + at + lane * 16);
+      }
     }
-    sum = wave_sum(sum);
-    if (lane == 0) sums[s] = sum;
+    if (s0 + kVpGroup > whole) {   // the partial span, and nothing past it
+      uint4 pe = make_uint4(0, 0, 0, 0), qe = pe;
+      if (s0 <= whole) {
+        pe = load_chunk_zero<DT>(r.p, whole * SPAN + lane * EPC, r.V);
+        if constexpr (SUB == 1) qe = load_chunk_zero<DT>(r.q, whole * SPAN + lane * EPC, r.V);
+      }
+#pragma unroll
+      for (int i = 0; i < kVpGroup; ++i) {
+        if (s0 + i < whole) continue;
+        const uint32_t keep = s0 + i == whole ? 0xFFFFFFFFu : 0u;
+        p[i] = make_uint4(pe.x & keep, pe.y & keep, pe.z & keep, pe.w & keep);
+        if constexpr (SUB == 1)
+          q[i] = make_uint4(qe.x & keep, qe.y & keep, qe.z & keep, qe.w & keep);
+      }
+    }
+  }
+  __device__ __forceinline__ double weights(const VpRow& r, int s0, int i, int lane,
+                                            double* w) const {
+    constexpr int EPC = Fmt<DT>::EPC;
+    return vp_weights<DT, SUB>(p[i], q[SUB == 1 ? i : 0], ((s0 + i) * kWave + lane) * EPC, r.x, w);
+  }
+};
+
+// Sums of the groups first, first + stride, ... below `end` into `sums`.
+template <int DT, int SUB>
+__device__ __forceinline__ void vp_sums(const VpRow& r, int first, int stride, int end, int lane,
+                                        double* sums) {
+  for (int g = first; g < end; g += 2 * stride) {
+    const bool two = g + stride < end;
+    double sum[2] = {0.0, 0.0};
+    for (int k = 0; k < r.rep; ++k) {
+      const int s0 = (g * r.rep + k) * kVpGroup;
+      const int s1 = ((g + stride) * r.rep + k) * kVpGroup;
+      VpGroup<DT, SUB> v0, v1;
+      v0.load(r, s0, lane);
+      if (two) v1.load(r, s1, lane);
+      double w[Fmt<DT>::EPC];
+#pragma unroll
+      for (int i = 0; i < kVpGroup; ++i) {
+        sum[0] += v0.weights(r, s0, i, lane, w);
+        sched_fence();   // one span's doubles at a time
+      }
+      if (two) {
+#pragma unroll
+        for (int i = 0; i < kVpGroup; ++i) {
+          sum[1] += v1.weights(r, s1, i, lane, w);
+          sched_fence();
+        }
+      }
+    }
+    const double a = wave_sum(sum[0]), b = wave_sum(sum[1]);
+    if (lane == 0) {
+      sums[g] = a;
+      if (two) sums[g + stride] = b;
+    }
   }
 }
+template <int DT>
+__device__ __forceinline__ void vp_sums_of(const VpRow& r, int sub, int first, int stride, int end,
+                                           int lane, double* sums) {
+  if (sub == 0)
+    vp_sums<DT, 0>(r, first, stride, end, lane, sums);
+  else if (sub == 1)
+    vp_sums<DT, 1>(r, first, stride, end, lane, sums);
+  else
+    vp_sums<DT, 2>(r, first, stride, end, lane, sums);
+}
 
-// The step that holds aim = v * total: lane l holds steps 16 l .. 16 l + 15.
+// The group that holds aim = v * total: lane l looks at `per` neighbouring ones.
 struct VpOwner {
   double total;
-  int step;      // -1: the weights sum to nothing
-  double base;   // total of the steps before it
+  int group;     // -1: the weights sum to nothing, or not to a number
+  double base;   // total of the groups before it
 };
-__device__ __forceinline__ VpOwner vp_owner(const double* sums, int steps, float v, int lane) {
-  constexpr int PER = kVpSteps / kWave;
+__device__ __forceinline__ VpOwner vp_owner(const double* sums, int groups, float v, int lane) {
+  const int per = (groups + kWave - 1) / kWave;
   double mine = 0.0;
-  for (int k = 0; k < PER; ++k) {
-    const int s = lane * PER + k;
-    if (s < steps) mine += sums[s];
+  for (int k = 0; k < per; ++k) {
+    const int g = lane * per + k;
+    if (g < groups) mine += sums[g];
   }
   const double incl = wave_incl_scan(mine);
   VpOwner o;
   o.total = readlane_f64(incl, kWave - 1);
   const double aim = (double)v * o.total;
   const unsigned long long over = __ballot(incl > aim);
-  o.step = -1;
+  o.group = -1;
   o.base = 0.0;
   if (!over) return o;   // total 0 or NaN
   const int l = __ffsll((long long)over) - 1;
   double c = l > 0 ? readlane_f64(incl, l - 1) : 0.0;
-  for (int k = 0; k < PER; ++k) {
-    const int s = l * PER + k;
-    if (s >= steps) break;
-    const double w = sums[s];
-    if (w > 0.0) {   // the last such step where rounding leaves none above aim
-      o.step = s;
+  for (int k = 0; k < per; ++k) {
+    const int g = l * per + k;
+    if (g >= groups) break;
+    const double w = sums[g];
+    if (w > 0.0) {   // the last such group where rounding leaves none above aim
+      o.group = g;
       o.base = c;
       if (c + w > aim) break;
     }
     c += w;
   }
+  o.group = __builtin_amdgcn_readfirstlane(o.group);
+  o.base = readlane_f64(o.base, 0);
   return o;
 }
 
-// The first id of the step whose running total exceeds aim; the last one with
+// The first id of the group whose running total exceeds aim; the last one with
 // a weight where rounding leaves none.
 template <int DT, int SUB>
-__device__ __forceinline__ int vp_pick(const unsigned char* prow, const unsigned char* qrow, int V,
-                                       int x, int step, int rep, double base, double aim,
-                                       int lane) {
+__device__ __forceinline__ int vp_pick(const VpRow& r, const VpOwner& o, double aim, int lane) {
   constexpr int EPC = Fmt<DT>::EPC;
-  int last = -1;
-  for (int k = 0; k < rep; ++k) {
-    const int e0 = ((step * rep + k) * kWave + lane) * EPC;
-    const uint4 pr = load_chunk_zero<DT>(prow, e0, V);
-    uint4 qr{};
-    if constexpr (SUB == 1) qr = load_chunk_zero<DT>(qrow, e0, V);
+  double base = o.base;
+  int found = -1;   // last id with a weight so far
+  for (int k = 0; k < r.rep; ++k) {
+    const int s0 = (o.group * r.rep + k) * kVpGroup;
+    VpGroup<DT, SUB> v;
+    v.load(r, s0, lane);
+    // the first span that passes aim, else the last with a weight
+    int span = -1;
+    double before = base;
+    uint4 pr{}, qr{};
+#pragma unroll
+    for (int i = 0; i < kVpGroup; ++i) {
+      double w[EPC];
+      const double sum = wave_sum(v.weights(r, s0, i, lane, w));
+      const bool done = span >= 0 && base > aim;   // an earlier span passed it
+      if (sum > 0.0 && !done) {
+        span = s0 + i;
+        before = base;
+        pr = v.p[i];
+        qr = v.q[SUB == 1 ? i : 0];
+      }
+      base = done ? base : base + sum;
+      sched_fence();
+    }
+    if (span < 0) continue;
+    const int e0 = (span * kWave + lane) * EPC;
     double w[EPC];
-    const double sum = vp_weights<DT, SUB>(pr, qr, e0, x, w);
+    const double sum = vp_weights<DT, SUB>(pr, qr, e0, r.x, w);
     const double incl = wave_incl_scan(sum);
-    const double before = dpp_f64<kDppWaveShr1>(incl);   // lane 0: 0
-    double c = base + before;
+    double c = before + dpp_f64<kDppWaveShr1>(incl);   // lane 0: nothing before it
     int hit = -1, pos = -1;
 #pragma unroll
     for (int e = 0; e < EPC; ++e) {
@@ -165,76 +284,144 @@ __device__ __forceinline__ int vp_pick(const unsigned char* prow, const unsigned
     }
     const unsigned long long hits = __ballot(hit >= 0);
     if (hits) return (int)readlane_u32((uint32_t)hit, __ffsll((long long)hits) - 1);
-    last = max(last, wave_max(pos));
-    base += readlane_f64(incl, kWave - 1);
+    found = max(found, wave_max(pos));
+    if (base > aim) break;   // by the spans' sums it was here
   }
-  return last;
+  return found;
 }
 
-// One workgroup per sequence.
+// The draw once the group sums are known (one wavefront). Returns the token,
+// or -1 with a status.
 template <int DT>
-__global__ __launch_bounds__(kVpBlock) void vprobs_kernel(VprobsArgs a, int steps, int rep) {
-  __shared__ double sums[kVpSteps];
-  const int b = blockIdx.x, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+__device__ __forceinline__ int vp_draw(const VpRow& r, int sub, const VpOwner& o, float v, int lane,
+                                       int* status) {
+  if (!(o.total >= 0.0)) {
+    *status = 1;
+    return -1;
+  }
+  if (o.group < 0) {
+    *status = 2;
+    return -1;
+  }
+  const double aim = (double)v * o.total;
+  return sub == 0   ? vp_pick<DT, 0>(r, o, aim, lane)
+         : sub == 1 ? vp_pick<DT, 1>(r, o, aim, lane)
+                    : vp_pick<DT, 2>(r, o, aim, lane);
+}
+
+__device__ __forceinline__ void vp_write(const VprobsArgs& a, int b, int status, int kept, int x,
+                                         int token, int lane) {
+  if (lane <= a.K)
+    a.out_tokens[(long long)b * (a.K + 1) + lane] =
+        status ? -1 : lane < kept ? x : lane == kept ? token : -1;
+  if (lane == 0) {
+    a.out_accepted[b] = status ? 0 : kept;
+    if (a.out_status) a.out_status[b] = status;
+  }
+}
+
+// One workgroup per sequence: tests, group sums in LDS, draw.
+template <int DT>
+__global__ __launch_bounds__(kVpWaves<DT> * kWave) void vprobs_kernel(VprobsArgs a, int groups, int rep) {
+  __shared__ double sums[kVpGroups];
+  const int b = blockIdx.x, lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const VpCut c = vp_cut<DT>(a, b, lane);
   int status = c.status, token = -1;
   if (status == 0) {
-    const unsigned char* prow = a.target + b * a.t_seq + c.kept * a.t_row;
-    const unsigned char* qrow = a.draft ? a.draft + b * a.d_seq + c.kept * a.d_row : nullptr;
-    const float v = a.draw_u[b];
+    const VpRow r = vp_row<DT>(a, b, c.kept, c.token, rep, groups);
     int sub = !c.refused ? 0 : a.draft ? 1 : 2;
     VpOwner o;
     for (;;) {
-      if (sub == 0)
-        vp_sums<DT, 0>(prow, qrow, a.V, c.token, wave, kVpWaves, steps, rep, lane, sums);
-      else if (sub == 1)
-        vp_sums<DT, 1>(prow, qrow, a.V, c.token, wave, kVpWaves, steps, rep, lane, sums);
-      else
-        vp_sums<DT, 2>(prow, qrow, a.V, c.token, wave, kVpWaves, steps, rep, lane, sums);
+      vp_sums_of<DT>(r, sub, wave, kVpWaves<DT>, groups, lane, sums);
       __syncthreads();
-      o = vp_owner(sums, steps, v, lane);
+      o = vp_owner(sums, groups, c.v, lane);
       if (sub == 0 || o.total != 0.0) break;
       sub = 0;           // nothing is left of the target: drawn from the target itself
       __syncthreads();   // every wavefront has read the sums
     }
     if (wave > 0) return;
-    if (!(o.total >= 0.0)) {
-      status = 1;
-    } else if (o.step < 0) {
-      status = 2;
-    } else {
-      const double aim = (double)v * o.total;
-      token = sub == 0 ? vp_pick<DT, 0>(prow, qrow, a.V, c.token, o.step, rep, o.base, aim, lane)
-              : sub == 1
-                  ? vp_pick<DT, 1>(prow, qrow, a.V, c.token, o.step, rep, o.base, aim, lane)
-                  : vp_pick<DT, 2>(prow, qrow, a.V, c.token, o.step, rep, o.base, aim, lane);
-    }
+    token = vp_draw<DT>(r, sub, o, c.v, lane, &status);
   }
   if (wave > 0) return;
-  if (lane <= a.K) {
-    a.out_tokens[(long long)b * (a.K + 1) + lane] =
-        status ? -1 : lane < c.kept ? c.x : lane == c.kept ? token : -1;
-  }
-  if (lane == 0) {
-    a.out_accepted[b] = status ? 0 : c.kept;
-    if (a.out_status) a.out_status[b] = status;
-  }
+  vp_write(a, b, status, c.kept, c.x, token, lane);
+}
+
+// The same in two launches, for few rows of many ids: `slices` workgroups to a
+// sequence write group sums, then one workgroup draws. Each slice makes the
+// tests for itself (two dependent loads); the first leaves what they decided
+// for the draw.
+template <int DT>
+__global__ __launch_bounds__(kVpSliceBlock) void vprobs_slices_kernel(VprobsArgs a, int groups,
+                                                                      int rep, int slices,
+                                                                      VprobsWs ws) {
+  const int b = blockIdx.y, slice = blockIdx.x, lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const VpCut c = vp_cut<DT>(a, b, lane);
+  if (slice == 0 && threadIdx.x == 0)
+    ws.cut[b] = make_int4(c.status, c.kept, c.refused, c.token);
+  if (c.status != 0) return;
+  const VpRow r = vp_row<DT>(a, b, c.kept, c.token, rep, groups);
+  vp_sums_of<DT>(r, !c.refused ? 0 : a.draft ? 1 : 2, slice * kVpSliceWaves + wave,
+                 slices * kVpSliceWaves, groups, lane, ws.sums + (long long)b * kVpGroups);
 }
 
 template <int DT>
-hipError_t launch_vprobs_dt(const VprobsArgs& a, hipStream_t s) {
-  constexpr int SPAN = kWave * Fmt<DT>::EPC;
-  const int spans = (a.V + SPAN - 1) / SPAN;
-  const int rep = (spans + kVpSteps - 1) / kVpSteps;
-  const int steps = (spans + rep - 1) / rep;
-  hipLaunchKernelGGL((vprobs_kernel<DT>), dim3(a.rows), dim3(kVpBlock), 0, s, a, steps, rep);
+__global__ __launch_bounds__(kVpSliceBlock) void vprobs_draw_kernel(VprobsArgs a, int groups,
+                                                                    int rep, VprobsWs ws) {
+  __shared__ double sums[kVpGroups];
+  const int b = blockIdx.x, lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int4 cut = ws.cut[b];
+  int status = cut.x, token = -1;
+  const int x = lane < a.K ? a.tokens[(long long)b * a.K + lane] : 0;
+  const float v = a.draw_u[b];
+  for (int g = threadIdx.x; g < groups; g += kVpSliceBlock)
+    sums[g] = ws.sums[(long long)b * kVpGroups + g];
+  __syncthreads();
+  if (status == 0) {
+    const VpRow r = vp_row<DT>(a, b, cut.y, cut.w, rep, groups);
+    int sub = !cut.z ? 0 : a.draft ? 1 : 2;
+    VpOwner o = vp_owner(sums, groups, v, lane);
+    if (sub != 0 && o.total == 0.0) {
+      sub = 0;
+      __syncthreads();
+      vp_sums_of<DT>(r, 0, wave, kVpSliceWaves, groups, lane, sums);
+      __syncthreads();
+      o = vp_owner(sums, groups, v, lane);
+    }
+    if (wave > 0) return;
+    token = vp_draw<DT>(r, sub, o, v, lane, &status);
+  }
+  if (wave > 0) return;
+  vp_write(a, b, status, cut.y, x, token, lane);
+}
+
+template <int DT>
+hipError_t launch_vprobs_dt(const VprobsArgs& a, const VprobsWs& ws, hipStream_t s) {
+  constexpr int UNIT = kWave * Fmt<DT>::EPC * kVpGroup;   // ids of a group at rep 1
+  const int units = (a.V + UNIT - 1) / UNIT;
+  const int rep = (units + kVpGroups - 1) / kVpGroups;
+  const int groups = (units + rep - 1) / rep;
+  const int slices = vp_slices(a.rows, groups, ws.rows);
+  if (slices > 1) {
+    hipLaunchKernelGGL((vprobs_slices_kernel<DT>), dim3(slices, a.rows), dim3(kVpSliceBlock), 0, s,
+                       a, groups, rep, slices, ws);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((vprobs_draw_kernel<DT>), dim3(a.rows), dim3(kVpSliceBlock), 0, s, a, groups,
+                       rep, ws);
+  } else {
+    hipLaunchKernelGGL((vprobs_kernel<DT>), dim3(a.rows), dim3(kVpWaves<DT> * kWave), 0, s, a,
+                       groups, rep);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_vprobs(const VprobsArgs& a, int dtype, hipStream_t s) {
-  return dtype == 0 ? launch_vprobs_dt<0>(a, s) : launch_vprobs_dt<1>(a, s);
+hipError_t launch_vprobs(const VprobsArgs& a, int dtype, const VprobsWs& ws, hipStream_t s) {
+  return dtype == 0 ? launch_vprobs_dt<0>(a, ws, s) : launch_vprobs_dt<1>(a, ws, s);
 }
 
 }  // namespace tsr

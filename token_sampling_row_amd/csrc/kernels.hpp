@@ -168,7 +168,16 @@ struct VprobsArgs {
   int32_t* out_accepted;
   int32_t* out_status;
 };
-hipError_t launch_vprobs(const VprobsArgs& a, int dtype, hipStream_t s);
+// Its workspace: per sequence (of up to `rows`) kVpGroups sums and what the tests
+// decided (status, drafts kept, whether one was refused, its token).
+constexpr int kVpGroups = 1024;   // most groups a row is cut into
+constexpr int kVpWsRows = 512;
+struct VprobsWs {
+  double* sums;
+  int4* cut;
+  int rows;
+};
+hipError_t launch_vprobs(const VprobsArgs& a, int dtype, const VprobsWs& ws, hipStream_t s);
 
 hipError_t launch_philox(const uint32_t* ctr, int n, uint32_t k0, uint32_t k1, uint32_t* out,
                          hipStream_t s);
