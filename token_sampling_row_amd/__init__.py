@@ -461,9 +461,15 @@ class Sampler:
         xs = self._rows(x, rows, width, "x")
         if out is None:
             out = _new(stream, x.device, torch.int8, rows, width)
+            stride = width
+        elif out.dtype is not torch.int8:
+            raise ValueError("out: not int8")
+        else:
+            stride = self._rows(out, rows, width, "out")
         if scale is None:
             scale = _new(stream, x.device, torch.float32, rows)
-        stride = self._codes(out, scale, rows, width, "out")
+        else:
+            self._vector(scale, torch.float32, "scale", rows)
         if rows:
             _check(load_library().quantize_rows(
                 self._h, x.data_ptr(), dt, rows, width, xs, out.data_ptr(), stride,
@@ -563,9 +569,15 @@ class Sampler:
                 raise ValueError(f"draft: not [{rows}, {K}, {vocab}] rows of the target's type "
                                  "on the handle's GPU")
             d_ptr = draft.data_ptr()
-        x_ptr = self._vector(draft_tokens, i32, "draft_tokens", rows, K)
-        u_ptr = self._vector(accept_u, f32, "accept_u", rows, K)
-        v_ptr = self._vector(draw_u, f32, "draw_u", rows)
+        if draft_tokens.dtype is not i32 or draft_tokens.shape != (rows, K) or \
+                draft_tokens.get_device() != dev or not draft_tokens.is_contiguous():
+            self._vector(draft_tokens, i32, "draft_tokens", rows, K)
+        if accept_u.dtype is not f32 or accept_u.shape != (rows, K) or \
+                accept_u.get_device() != dev or not accept_u.is_contiguous():
+            self._vector(accept_u, f32, "accept_u", rows, K)
+        if draw_u.dtype is not f32 or draw_u.shape != (rows,) or draw_u.get_device() != dev or \
+                not draw_u.is_contiguous():
+            self._vector(draw_u, f32, "draw_u", rows)
         n_ptr = None if draft_lens is None else self._vector(draft_lens, i32, "draft_lens", rows)
         s_ptr = None if out_status is None else self._vector(out_status, i32, "out_status", rows)
         if out_tokens is None:
@@ -578,8 +590,8 @@ class Sampler:
             self._vector(out_accepted, i32, "out_accepted", rows)
         if rows:
             _check(load_library().verify_probs(
-                self._h, target.data_ptr(), t_seq, t_row, d_ptr, d_seq, d_row, dt, x_ptr, n_ptr,
-                u_ptr, v_ptr, rows, K, vocab, out_tokens.data_ptr(), out_accepted.data_ptr(),
+                self._h, target.data_ptr(), t_seq, t_row, d_ptr, d_seq, d_row, dt,
+                draft_tokens.data_ptr(), n_ptr, accept_u.data_ptr(), draw_u.data_ptr(), rows, K, vocab, out_tokens.data_ptr(), out_accepted.data_ptr(),
                 s_ptr, _stream_on(dev, stream)), "verify_probs")
         return out_tokens, out_accepted
 
