@@ -369,15 +369,16 @@ int int8_logits(tsr_handle h, const int8_t* codes, int64_t codes_stride, const f
  * enqueued one after the other.
  *  hidden [rows][head->width] of type hidden_dtype, hidden_stride elements
  *      apart.
- *  codes [rows][width], code_scale [rows] and logits [rows][vocab] (of type
- *      dtype) are workspace of the caller's and hold the codes, the scales
- *      and the logits afterwards.
+ *  codes [rows][width] (codes_stride bytes apart), code_scale [rows] and logits
+ *      [rows][vocab] (of type dtype) are workspace of the caller's and hold the
+ *      codes, the scales and the logits afterwards.
  * params, step, out_tokens and diag are sample_rows'; so are the limits on
  * vocab. */
 int sample_hidden(tsr_handle h, const void* hidden, int hidden_dtype, int rows,
-                  int64_t hidden_stride, const tsr_head* head, int8_t* codes, float* code_scale,
-                  void* logits, int dtype, const tsr_params* params, uint64_t step,
-                  int32_t* out_tokens, const tsr_diag* diag, void* hip_stream);
+                  int64_t hidden_stride, const tsr_head* head, int8_t* codes,
+                  int64_t codes_stride, float* code_scale, void* logits, int dtype,
+                  const tsr_params* params, uint64_t step, int32_t* out_tokens,
+                  const tsr_diag* diag, void* hip_stream);
 
 /* The verify step from probabilities and the caller's random numbers
  * [P2 39.4, Listing 39.4; P3 "The Algorithm", "Batching Speculation"], for

@@ -12,7 +12,7 @@ def test_null_handles(lib):  # noqa: F811
     prm = tsr._Params(1.0, 0, 1.0, 0.0, 0)
     assert lib.quantize_rows(None, None, 0, 1, 1, 1, None, 1, None, None) == 1
     assert lib.int8_logits(None, None, 1, None, 1, ctypes.byref(head), None, 0, 1, None) == 1
-    assert lib.sample_hidden(None, None, 0, 1, 1, ctypes.byref(head), None, None, None, 0,
+    assert lib.sample_hidden(None, None, 0, 1, 1, ctypes.byref(head), None, 1, None, None, 0,
                              ctypes.byref(prm), 0, None, None, None) == 1
     assert lib.verify_probs(None, None, 0, 0, None, 0, 0, 0, None, None, None, None, 1, 1, 1,
                             None, None, None, None) == 1

@@ -102,7 +102,7 @@ def load_library():
     lib.beam_step.argtypes = [vp, vp, i32, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp]
     lib.quantize_rows.argtypes = [vp, vp, i32, i32, i32, i64, vp, i64, vp, vp]
     lib.int8_logits.argtypes = [vp, vp, i64, vp, i32, ctypes.POINTER(_Head), vp, i32, i64, vp]
-    lib.sample_hidden.argtypes = [vp, vp, i32, i32, i64, ctypes.POINTER(_Head), vp, vp, vp, i32,
+    lib.sample_hidden.argtypes = [vp, vp, i32, i32, i64, ctypes.POINTER(_Head), vp, i64, vp, vp, i32,
                                   ctypes.POINTER(_Params), u64, vp, ctypes.POINTER(_Diag), vp]
     lib.verify_probs.argtypes = [vp, vp, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, i32, i32,
                                  i32, vp, vp, vp, vp]
@@ -450,18 +450,29 @@ class Sampler:
         self._vector(scale, _torch.float32, what, rows)
         return self._rows(codes, rows, width, what)
 
+    def _new_codes(self, stream, device, rows, width):
+        """[rows, width] int8 whose rows start at multiples of 128 bytes, as
+        int8_logits reads them fastest."""
+        if stream is None:
+            return _torch.empty_strided((rows, width), (width + -width % 128, 1),
+                                        dtype=_torch.int8, device=device)
+        with _torch.cuda.stream(stream):
+            return self._new_codes(None, device, rows, width)
+
     def quantize_rows(self, x, out=None, scale=None, stream=None):
         """x [rows, W] float32 or bfloat16 (rows contiguous, any row stride) ->
-        (codes [rows, W] int8, scale [rows] float32): absmax codes per row."""
+        (codes [rows, W] int8, scale [rows] float32): absmax codes per row. New
+        codes are rows a multiple of 128 bytes apart: not contiguous where W is
+        no such multiple."""
         torch = _t()
-        dt = _dtype_code(x)
+        dt = 1 if x.dtype is torch.bfloat16 else _dtype_code(x)
         if x.dim() != 2:
             raise ValueError("x: not a matrix")
         rows, width = x.shape
         xs = self._rows(x, rows, width, "x")
         if out is None:
-            out = _new(stream, x.device, torch.int8, rows, width)
-            stride = width
+            out = self._new_codes(stream, x.device, rows, width)
+            stride = width + -width % 128
         elif out.dtype is not torch.int8:
             raise ValueError("out: not int8")
         else:
@@ -525,7 +536,7 @@ class Sampler:
         elif self._rows(logits, rows, vocab, "logits") != vocab:
             raise ValueError("logits: not contiguous")
         ldt = _dtype_code(logits)
-        codes = _new(stream, dev, torch.int8, rows, head.width)
+        codes = self._new_codes(stream, dev, rows, head.width)
         scale = _new(stream, dev, torch.float32, rows)
         if out is None:
             out = _new(stream, dev, torch.int32, rows)
@@ -539,9 +550,10 @@ class Sampler:
         if rows:
             _check(load_library().sample_hidden(
                 self._h, hidden.data_ptr(), hdt, rows, stride, ctypes.byref(head),
-                codes.data_ptr(), scale.data_ptr(), logits.data_ptr(), ldt, ctypes.byref(cp),
-                int(step), out.data_ptr(), ctypes.byref(d) if d is not None else None,
-                _stream_on(self.device, stream)), "sample_hidden")
+                codes.data_ptr(), head.width + -head.width % 128, scale.data_ptr(),
+                logits.data_ptr(), ldt, ctypes.byref(cp), int(step), out.data_ptr(),
+                ctypes.byref(d) if d is not None else None, _stream_on(self.device, stream)),
+                "sample_hidden")
         return out
 
     def verify_probs(self, target, draft, draft_tokens, accept_u, draw_u, draft_lens=None,
@@ -553,7 +565,7 @@ class Sampler:
         [rows] float32 in [0, 1) -> (tokens [rows, K+1], accepted [rows])."""
         torch = _t()
         i32, f32, dev = torch.int32, torch.float32, self.device
-        dt = _dtype_code(target)
+        dt = F32 if target.dtype is f32 else _dtype_code(target)
         if target.dim() != 3 or target.get_device() != dev:
             raise ValueError("target: not [rows, K + 1, vocab] on the handle's GPU")
         rows, k1, vocab = target.shape
@@ -591,8 +603,8 @@ class Sampler:
         if rows:
             _check(load_library().verify_probs(
                 self._h, target.data_ptr(), t_seq, t_row, d_ptr, d_seq, d_row, dt,
-                draft_tokens.data_ptr(), n_ptr, accept_u.data_ptr(), draw_u.data_ptr(), rows, K, vocab, out_tokens.data_ptr(), out_accepted.data_ptr(),
-                s_ptr, _stream_on(dev, stream)), "verify_probs")
+                draft_tokens.data_ptr(), n_ptr, accept_u.data_ptr(), draw_u.data_ptr(), rows, K,
+                vocab, out_tokens.data_ptr(), out_accepted.data_ptr(), s_ptr, _stream_on(dev, stream)), "verify_probs")
         return out_tokens, out_accepted
 
     def philox(self, counters, stream=None):

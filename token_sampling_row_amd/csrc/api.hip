@@ -558,22 +558,23 @@ int int8_logits(tsr_handle h, const int8_t* codes, int64_t codes_stride, const f
 }
 
 int sample_hidden(tsr_handle h, const void* hidden, int hidden_dtype, int rows,
-                  int64_t hidden_stride, const tsr_head* head, int8_t* codes, float* code_scale,
-                  void* logits, int dtype, const tsr_params* params, uint64_t step,
-                  int32_t* out_tokens, const tsr_diag* diag, void* hip_stream) {
+                  int64_t hidden_stride, const tsr_head* head, int8_t* codes,
+                  int64_t codes_stride, float* code_scale, void* logits, int dtype,
+                  const tsr_params* params, uint64_t step, int32_t* out_tokens,
+                  const tsr_diag* diag, void* hip_stream) {
   // every argument of the three steps first: an error leaves nothing enqueued
   if (!h || !head || !out_tokens) return TSR_EINVAL;
   int rc = check_quantize(hidden, hidden_dtype, rows, head->width, hidden_stride, codes,
-                          head->width, code_scale);
+                          codes_stride, code_scale);
   if (rc == TSR_OK)
-    rc = check_int8(h, codes, head->width, code_scale, rows, head, logits, dtype, head->vocab);
+    rc = check_int8(h, codes, codes_stride, code_scale, rows, head, logits, dtype, head->vocab);
   if (rc == TSR_OK) rc = check_params(params);
   if (rc == TSR_OK && head->vocab > tsr::max_vocab_sample(dtype)) rc = TSR_EUNSUPPORTED;
   if (rc != TSR_OK || rows == 0) return rc;
   rc = quantize_rows(h, hidden, hidden_dtype, rows, head->width, hidden_stride, codes,
-                     head->width, code_scale, hip_stream);
+                     codes_stride, code_scale, hip_stream);
   if (rc == TSR_OK)
-    rc = int8_logits(h, codes, head->width, code_scale, rows, head, logits, dtype, head->vocab,
+    rc = int8_logits(h, codes, codes_stride, code_scale, rows, head, logits, dtype, head->vocab,
                      hip_stream);
   if (rc == TSR_OK)
     rc = sample_rows(h, logits, dtype, rows, head->vocab, head->vocab, params, step, out_tokens,

@@ -37,6 +37,16 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
 }
 
+// Every wavefront of the workgroup, its LDS accesses done; stores and loads stay
+// on their way.
+__device__ __forceinline__ void meet() {
+  wait_loads<63>();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  sched_fence();
+}
+
 // Tiles of BM hidden rows by BN channels. WM x WN wavefronts each hold MT x NT
 // blocks of 16 x 16 sums.
 //
@@ -162,30 +172,109 @@ struct Tile {
       sched_fence();
     }
   }
-  // The sum rounded to float32, times the row's scale, then times the channel's
-  // and plus the bias in one rounding; float32 holds far more than the codes do.
-  template <int DT>
-  __device__ __forceinline__ void store(const Int8Args& a, const v4i (*acc)[MT]) const {
+  // What the sums of this lane are multiplied with and added to. Read before the
+  // products where registers allow, for a tile's end waits for it otherwise.
+  static constexpr bool EARLY = MT * NT <= 24;
+  struct Scales {
+    float w[4 * NT], b[4 * NT], x[MT];
+  };
+  __device__ __forceinline__ void load_scales(const Int8Args& a, Scales* s) const {
     const int c0 = n0 + wn * (16 * NT) + (lane >> 4) * (4 * NT);
-    float ws[4 * NT], bs[4 * NT];
 #pragma unroll
     for (int e = 0; e < 4 * NT; ++e) {
       const int c = min(c0 + e, a.vocab - 1);
-      ws[e] = a.w_scale[c];
-      bs[e] = a.bias ? a.bias[c] : 0.0f;
+      s->w[e] = a.w_scale[c];
+      s->b[e] = a.bias ? a.bias[c] : 0.0f;
     }
 #pragma unroll
-    for (int u = 0; u < MT; ++u) {
-      const int r = m0 + (wm * MT + u) * 16 + (lane & 15);
-      if (r >= a.rows) continue;
-      const float xs = a.x_scale[r];
-      float v[4 * NT];
+    for (int u = 0; u < MT; ++u)
+      s->x[u] = a.x_scale[min(m0 + (wm * MT + u) * 16 + (lane & 15), a.rows - 1)];
+  }
+  // The sum rounded to float32, times the row's scale, then times the channel's
+  // and plus the bias in one rounding; float32 holds far more than the codes do.
+  //
+  // The results pass through LDS (`even` and `odd` in turn, each as large as a
+  // stage of the weight), so that a row's run of channels leaves in whole lines:
+  // written from the sums' own lanes, in pieces of 16 to 64 bytes, 64 rows of
+  // 128256 bfloat16 logits took 17 us of 105. Chunk c of LDS row r lies at place
+  // c ^ (r & 7).
+  template <int DT>
+  __device__ __forceinline__ void store(const Int8Args& a, const v4i (*acc)[MT], Scales& s,
+                                        int8_t* even, int8_t* odd) const {
+    constexpr int ESZ = Fmt<DT>::ESZ, EPC = Fmt<DT>::EPC, ROW = BN * ESZ, CB = ROW / 16;
+    constexpr int FIT = BN * TK / (16 * WM * ROW);
+    constexpr int UP = FIT < MT ? FIT : MT;   // blocks of rows a pass
+    constexpr int RP = 16 * WM * UP;          // rows a pass
+    static_assert(UP >= 1 && CB >= 8, "a pass fits a stage");
+    const int i = lane & 15, cw = wn * (16 * NT) + (lane >> 4) * (4 * NT);
+    if constexpr (!EARLY) load_scales(a, &s);
+    const bool whole_lines =
+        (((uintptr_t)a.out | (uintptr_t)a.out_stride_bytes) & 127) == 0;
+    meet();   // every wavefront has read its last stage
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+    for (int p = 0; p < MT; p += UP) {
+      int8_t* buf = (p / UP) % 2 ? odd : even;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[t * 4 + e] = fmaf((float)acc[t][u][e] * xs, ws[t * 4 + e], bs[t * 4 + e]);
-      store_row<DT, 4 * NT>(a.out + (long long)r * a.out_stride_bytes, c0, a.vocab, v);
+      for (int u = 0; u < UP && p + u < MT; ++u) {
+        const int lr = (wm * UP + u) * 16 + i;
+        uint32_t w[4 * NT * ESZ / 4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = fmaf((float)acc[t][p + u][e] * s.x[p + u], s.w[t * 4 + e], s.b[t * 4 + e]);
+          if constexpr (DT == 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[t * 4 + e] = __float_as_uint(v[e]);
+          } else {
+            w[t * 2] = bf16_pair(v[0], v[1]);
+            w[t * 2 + 1] = bf16_pair(v[2], v[3]);
+          }
+        }
+        constexpr int N = 4 * NT * ESZ < 16 ? 2 : 4;   // words a write
+#pragma unroll
+        for (int k = 0; k < 4 * NT * ESZ / 4; k += N) {
+          const int at = cw * ESZ + k * 4;
+          int8_t* o = buf + lr * ROW + ((at / 16) ^ (lr & 7)) * 16 + at % 16;
+          if constexpr (N == 4)
+            *reinterpret_cast<uint4*>(o) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+          else
+            *reinterpret_cast<uint2*>(o) = make_uint2(w[k], w[k + 1]);
+        }
+      }
+      meet();
+#pragma unroll
+      for (int q = 0; q < (RP * CB + THREADS - 1) / THREADS; ++q) {
+        const int n = q * THREADS + threadIdx.x;
+        if (RP * CB % THREADS != 0 && n >= RP * CB) break;
+        const int lr = n / CB, c = n % CB;
+        const int u = p + lr / 16 % UP;
+        const int r = m0 + (lr / (16 * UP) * MT + u) * 16 + lr % 16;
+        if (u >= MT || r >= a.rows) continue;
+        const uint4 v = *reinterpret_cast<const uint4*>(buf + lr * ROW + (c ^ (lr & 7)) * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const int e0 = n0 + c * EPC;
+        unsigned char* o = a.out + (long long)r * a.out_stride_bytes + (long long)e0 * ESZ;
+        if (e0 + EPC <= a.vocab) {
+          // whole lines of many rows' logits leave the caches before they are read:
+          // 256 x 128256 160 us kept in them, 150 not (24 rows 85 and 87; lines
+          // that two tiles share, 256 x 50001: 122 and 180)
+          if (BM >= 128 && whole_lines)
+            store16_once(o, v);
+          else
+            store_words<4>(o, w);
+        } else {
+#pragma unroll
+          for (int e = 0; e < EPC; ++e) {
+            if (e0 + e >= a.vocab) break;
+            if constexpr (DT == 0)
+              reinterpret_cast<uint32_t*>(o)[e] = w[e];
+            else
+              reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+          }
+        }
+      }
     }
   }
 };
@@ -213,6 +302,8 @@ __global__ __launch_bounds__(WM* WN* kWave, 1) void int8_ring_kernel(Int8Args a,
   __shared__ __attribute__((aligned(1024))) int8_t w3[W3];
   T t;
   if (!t.place(m_tiles, tiles)) return;
+  typename T::Scales scales;
+  if constexpr (T::EARLY) t.load_scales(a, &scales);
   const int8_t* xb = a.x + (long long)t.m0 * a.x_stride;
   const int8_t* wb = a.w + (long long)t.n0 * a.w_stride;
   // the tile's bytes end with the last byte of its last row
@@ -322,8 +413,8 @@ __global__ __launch_bounds__(WM* WN* kWave, 1) void int8_ring_kernel(Int8Args a,
       }
     }
   }
-  wait_loads<0>();   // none writes LDS that another workgroup has by then
-  t.template store<DT>(a, acc);
+  wait_loads<0>();   // LDS takes no more loads: the results pass through it
+  t.template store<DT>(a, acc, scales, w0, w1);
 }
 
 // Operands at any byte: loads into registers, put into LDS once the stage
@@ -342,6 +433,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(Int8Args a, in
   __shared__ __attribute__((aligned(1024))) int8_t w1[BN * TK];
   T t;
   if (!t.place(m_tiles, tiles)) return;
+  typename T::Scales scales;
+  if constexpr (T::EARLY) t.load_scales(a, &scales);
   const int8_t* xb = a.x + (long long)t.m0 * a.x_stride;
   const int8_t* wb = a.w + (long long)t.n0 * a.w_stride;
   uint32_t off[N];
@@ -419,7 +512,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(Int8Args a, in
       t.multiply_stage(acc, x1, w1);
     }
   }
-  t.template store<DT>(a, acc);
+  t.template store<DT>(a, acc, scales, w0, w1);
 }
 
 template <int BM, int BN>
@@ -484,7 +577,7 @@ inline int pick_tile(int rows, int vocab) {
 template <int DT, bool LINES>
 hipError_t launch_direct(const Int8Args& a, hipStream_t s) {
   if (a.rows <= 16) return launch_ring<DT, 16, 64, 1, 4, 256, 4, LINES>(a, s);
-  if (a.rows <= 32) return launch_ring<DT, 32, 64, 1, 4, 256, 2, LINES>(a, s);
+  if (a.rows <= 32) return launch_ring<DT, 32, 64, 1, 4, 128, 4, LINES>(a, s);
   if (a.rows <= 64) return launch_ring<DT, 64, 128, 1, 4, 128, 3, LINES>(a, s);
   switch (pick_tile(a.rows, a.vocab)) {
     case 0: return launch_ring<DT, 256, 256, 2, 4, 128, 2, false>(a, s);
@@ -504,11 +597,12 @@ hipError_t launch_int8_dt(const Int8Args& a, hipStream_t s) {
   if (multiple(128)) return launch_direct<DT, true>(a, s);
   if (multiple(4)) return launch_direct<DT, false>(a, s);
   // measured at width 4095 (us): 1 x 128256 93 (64 rows a tile 109), 30 x 128256 115
-  // (123, 128x128 127), 64 x 128256 138 (128x128 141), 700 x 50001 263 (256x128 279)
+  // (123, 128x128 127), 64 x 128256 136 (128x128 141), 256 x 50001 118 (256x128 127,
+  // 128x256 134, 256x256 217)
   if (a.rows <= 16) return launch_tile<DT, 16, 64, 1, 4, 256>(a, s);
   if (a.rows <= 32) return launch_tile<DT, 32, 64, 1, 4, 256>(a, s);
   if (a.rows <= 64) return launch_tile<DT, 64, 64, 1, 4, 256>(a, s);
-  return launch_tile<DT, 128, 128, 2, 2, 128>(a, s);
+  return launch_tile<DT, 128, 128, 1, 4, 128>(a, s);
 }
 
 }  // namespace tsr

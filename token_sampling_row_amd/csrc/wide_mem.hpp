@@ -30,6 +30,13 @@ __device__ __forceinline__ void store_words(void* p, const uint32_t* w) {
   }
 }
 
+// 16 bytes, at any byte, that are not kept in the caches.
+__device__ __forceinline__ void store16_once(void* p, uint4 v) {
+  typedef uint32_t Any4 __attribute__((ext_vector_type(4), aligned(1)));
+  const Any4 w = {v.x, v.y, v.z, v.w};
+  __builtin_nontemporal_store(w, static_cast<Any4*>(p));
+}
+
 // Elements [e0, e0 + EPC) of a row of n elements; those at or past n read as 0.
 template <int DT>
 __device__ __forceinline__ uint4 load_chunk_zero(const unsigned char* row, long long e0,
@@ -79,46 +86,10 @@ __device__ __forceinline__ uint4 load_bytes_zero(const int8_t* row, int k, int n
   return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
 }
 
-__device__ __forceinline__ uint16_t bf16_bits(float v) {
-  return __builtin_bit_cast(uint16_t, (__bf16)v);   // to nearest even
-}
-
-// N consecutive float results (n0 and up of a row of `n` elements) in the
-// output's type.
-template <int DT, int N>
-__device__ __forceinline__ void store_row(unsigned char* row, int n0, int n, const float* v) {
-  if constexpr (DT == 0) {
-    float* o = reinterpret_cast<float*>(row) + n0;
-    if (n0 + N <= n) {
-#pragma unroll
-      for (int e = 0; e < N; e += 4) {
-        const uint32_t w[4] = {__float_as_uint(v[e]), __float_as_uint(v[e + 1]),
-                               __float_as_uint(v[e + 2]), __float_as_uint(v[e + 3])};
-        store_words<4>(o + e, w);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (n0 + e < n) o[e] = v[e];
-    }
-  } else {
-    uint16_t* o = reinterpret_cast<uint16_t*>(row) + n0;
-    if (n0 + N <= n) {
-      constexpr int S = N >= 8 ? 8 : 4;
-#pragma unroll
-      for (int e = 0; e < N; e += S) {
-        uint32_t w[S / 2];
-#pragma unroll
-        for (int k = 0; k < S / 2; ++k)
-          w[k] = (uint32_t)bf16_bits(v[e + 2 * k]) | ((uint32_t)bf16_bits(v[e + 2 * k + 1]) << 16);
-        store_words<S / 2>(o + e, w);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (n0 + e < n) o[e] = bf16_bits(v[e]);
-    }
-  }
+// Two floats as bfloat16, each to nearest even; the first in the low half.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) |
+         ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16);
 }
 
 }  // namespace tsr
