@@ -540,32 +540,33 @@ hipError_t launch_tile(const Int8Args& a, hipStream_t s) {
 }
 
 // Tile shapes for more than 64 rows: how many run at once (one or two to a
-// compute unit) and how long one round of them takes, in us at width 4096.
+// compute unit) and how long a round of them takes, in us at width 4096. A round
+// that fills only part of the places of a shape that runs in pairs takes 0.6 of
+// a full one at least.
 struct TileCost {
   int bm, bn, at_once, us;
 };
-constexpr TileCost kTileCost[] = {{256, 256, 256, 57}, {192, 256, 256, 47}, {128, 256, 256, 33},
-                                  {160, 128, 512, 39}, {128, 128, 512, 37}};
+constexpr TileCost kTileCost[] = {{256, 256, 256, 57}, {192, 256, 256, 52}, {128, 256, 256, 38},
+                                  {160, 128, 512, 50}, {128, 128, 512, 42}, {64, 64, 512, 17}};
 
-// The shape with the least rounds' time. A last round that leaves every second
-// place empty takes 0.6 of a full one. Measured at width 4096 (us): 256 x 32000
-// 128x256 40, 128x128 46, 160x128 48, 256x256 66; 320 x 32000 160x128 53, 192x256
-// 55, 256x256 60; 384 x 32000 192x256 57, 256x256 61; 128 x 32000 128x128 36,
-// 128x256 39; 128 x 128256 128x256 117, 128x128 131; 1024 x 151936 256x256 566,
-// 128x256 622, 160x128 659, 128x128 698.
+// The shape with the least rounds' time. Measured at width 4096 (us): 128 x 32000
+// 128x128 36, 128x256 39, 64x128 40; 128 x 128256 128x256 117, 128x128 131; 200 x 8960
+// 64x64 26, 128x128 31; 256 x 32000 128x256 40, 128x128 46, 160x128 48, 256x256 66;
+// 320 x 32000 160x128 53, 192x256 55, 256x256 60; 384 x 32000 192x256 57, 256x256 61;
+// 1024 x 151936 256x256 566, 128x256 622, 160x128 659, 128x128 698, 64x64 1213.
 inline int pick_tile(int rows, int vocab) {
   int best = 0;
   double least = 0.0;
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < 6; ++i) {
     const TileCost& c = kTileCost[i];
     const long long tiles =
         (long long)((rows + c.bm - 1) / c.bm) * ((vocab + c.bn - 1) / c.bn);
     const long long rest = tiles % c.at_once;
-    const double rounds = (double)(tiles / c.at_once) +
-                          (rest == 0 ? 0.0 : c.at_once == 512 && rest <= 256 ? 0.6 : 1.0);
-    if (i == 0 || rounds * c.us < least) {
+    const double part = rest == 0 ? 0.0 : c.at_once == 512 ? 0.6 + 0.4 * rest / 512 : 1.0;
+    const double time = ((double)(tiles / c.at_once) + part) * c.us;
+    if (i == 0 || time < least) {
       best = i;
-      least = rounds * c.us;
+      least = time;
     }
   }
   return best;
@@ -584,7 +585,8 @@ hipError_t launch_direct(const Int8Args& a, hipStream_t s) {
     case 1: return launch_ring<DT, 192, 256, 2, 4, 128, 2, false>(a, s);
     case 2: return launch_ring<DT, 128, 256, 2, 4, 128, 3, LINES>(a, s);
     case 3: return launch_ring<DT, 160, 128, 2, 2, 128, 2, false>(a, s);
-    default: return launch_ring<DT, 128, 128, 2, 2, 128, 2, LINES>(a, s);
+    case 4: return launch_ring<DT, 128, 128, 2, 2, 128, 2, LINES>(a, s);
+    default: return launch_ring<DT, 64, 64, 2, 2, 128, 4, LINES>(a, s);
   }
 }
 
@@ -602,6 +604,10 @@ hipError_t launch_int8_dt(const Int8Args& a, hipStream_t s) {
   if (a.rows <= 16) return launch_tile<DT, 16, 64, 1, 4, 256>(a, s);
   if (a.rows <= 32) return launch_tile<DT, 32, 64, 1, 4, 256>(a, s);
   if (a.rows <= 64) return launch_tile<DT, 64, 64, 1, 4, 256>(a, s);
+  // under two tiles of 128 x 128 to a compute unit: 87 x 19685 x 3234 34 us in 64 x 64,
+  // 41 in 128 x 128; 128 x 128256 157 in 128 x 128, 193 in 128 x 64
+  if ((long long)((a.rows + 127) / 128) * ((a.vocab + 127) / 128) <= 256)
+    return launch_tile<DT, 64, 64, 1, 4, 128>(a, s);
   return launch_tile<DT, 128, 128, 1, 4, 128>(a, s);
 }
 
