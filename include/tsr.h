@@ -328,8 +328,8 @@ int beam_step(tsr_handle h, const void* logits, int dtype, int groups, int beam,
  * infinity gets scale NaN and codes 0, so its logits are NaN and the sampler
  * reports it as TSR_ROW_NONFINITE. Bytes of out_codes between width and
  * codes_stride are left as they are.
- * rows is not bound by the handle's max_rows (a weight has vocab rows); width
- * <= 2^30 (TSR_EUNSUPPORTED beyond). Uses no workspace. */
+ * rows is not bound by the handle's max_rows (a weight has vocab rows); rows <
+ * 2^24 and width <= 2^30 (TSR_EUNSUPPORTED beyond). Uses no workspace. */
 int quantize_rows(tsr_handle h, const void* x, int dtype, int rows, int width, int64_t row_stride,
                   int8_t* out_codes, int64_t codes_stride, float* out_scale, void* hip_stream);
 
@@ -356,8 +356,8 @@ typedef struct {
  *  codes [rows][width] int8, codes_stride bytes apart (any alignment).
  *  out_logits [rows][vocab] of type dtype, out_stride elements apart; what
  *      lies between vocab and out_stride is left as it is.
- * width <= 131071 (the sum fits 32 bits) and both operands' strides < 2^23
- * (TSR_EUNSUPPORTED beyond). Rows that start at 4-byte words are read fastest,
+ * width <= 131071 (the sum fits 32 bits), vocab <= 2^30 and both operands'
+ * strides < 2^23 (TSR_EUNSUPPORTED beyond). Rows that start at 4-byte words are read fastest,
  * those at multiples of 128 bytes most of all; other rows are read in whole
  * 4-byte words, so up to three bytes on either side of a row, in words that
  * also hold bytes of it. Uses no workspace. */
@@ -410,8 +410,11 @@ int sample_hidden(tsr_handle h, const void* hidden, int hidden_dtype, int rows,
  *      tested draft, or draw_u, outside [0, 1)), TSR_ROW_NONFINITE (such a
  *      value in the rows drawn from), TSR_ROW_EMPTY (they are all zero).
  *      Rows and positions that the step does not come to are not checked.
- * 1 <= K <= max_k and K <= 32; vocab <= 2^30 (TSR_EUNSUPPORTED beyond).
- * Strides are not negative; rows may overlap or repeat (stride 0). */
+ * 1 <= K <= max_k and K <= 32; vocab <= 2^30 and rows < 2^22
+ * (TSR_EUNSUPPORTED beyond). Strides are not negative; rows may overlap or
+ * repeat (stride 0). Up to 512 sequences of many ids are summed by several
+ * workgroups each, through per-handle workspace of its own: not concurrent
+ * with another verify_probs on the handle. */
 int verify_probs(tsr_handle h, const void* target_probs, int64_t target_seq_stride,
                  int64_t target_row_stride, const void* draft_probs, int64_t draft_seq_stride,
                  int64_t draft_row_stride, int dtype, const int32_t* draft_tokens,

@@ -108,10 +108,12 @@ bool elem_aligned(const void* p, int dtype) {
 bool word_aligned(const void* p) { return ((uintptr_t)p % 4) == 0; }
 
 constexpr int kMaxQuantWidth = 1 << 30;
+constexpr int kMaxQuantRows = (1 << 24) - 1;   // 256 threads a row: fewer than 2^32 in a launch
 // sums of products of 8-bit integers fit 32 bits: 2^17 - 1 times (-128)^2
 constexpr int kMaxInt8Width = (1 << 17) - 1;
 constexpr int64_t kMaxInt8Stride = 1 << 23;   // a tile's 256 rows within 2^31 bytes
-constexpr int kMaxVprobsVocab = 1 << 30;
+constexpr int kMaxWideVocab = 1 << 30;          // ids past the last one stay whole numbers
+constexpr int kMaxVprobsRows = (1 << 22) - 1;   // 1024 threads a sequence: fewer than 2^32
 
 int check_quantize(const void* x, int dtype, int rows, int width, int64_t row_stride,
                    const int8_t* out_codes, int64_t codes_stride, const float* out_scale) {
@@ -119,7 +121,7 @@ int check_quantize(const void* x, int dtype, int rows, int width, int64_t row_st
   if (dtype != TSR_F32 && dtype != TSR_BF16) return TSR_EINVAL;
   if (rows < 0 || width < 1 || row_stride < width || codes_stride < width) return TSR_EINVAL;
   if (!elem_aligned(x, dtype) || !word_aligned(out_scale)) return TSR_EINVAL;
-  if (width > kMaxQuantWidth) return TSR_EUNSUPPORTED;
+  if (width > kMaxQuantWidth || rows > kMaxQuantRows) return TSR_EUNSUPPORTED;
   return TSR_OK;
 }
 
@@ -137,7 +139,7 @@ int check_int8(tsr_handle h, const int8_t* codes, int64_t codes_stride, const fl
   if (!word_aligned(code_scale) || !word_aligned(head->scale) || !word_aligned(head->bias) ||
       !elem_aligned(out_logits, dtype))
     return TSR_EINVAL;
-  if (head->width > kMaxInt8Width || codes_stride >= kMaxInt8Stride ||
+  if (head->width > kMaxInt8Width || head->vocab > kMaxWideVocab || codes_stride >= kMaxInt8Stride ||
       head->weight_stride >= kMaxInt8Stride)
     return TSR_EUNSUPPORTED;
   return TSR_OK;
@@ -601,7 +603,7 @@ int verify_probs(tsr_handle h, const void* target_probs, int64_t target_seq_stri
       !word_aligned(draw_u) || !word_aligned(out_tokens) || !word_aligned(out_accepted) ||
       !word_aligned(out_status))
     return TSR_EINVAL;
-  if (vocab > kMaxVprobsVocab) return TSR_EUNSUPPORTED;
+  if (vocab > kMaxWideVocab || rows > kMaxVprobsRows) return TSR_EUNSUPPORTED;
   if (rows == 0) return TSR_OK;
   const long long es = esize(dtype);
   tsr::VprobsArgs a{};
