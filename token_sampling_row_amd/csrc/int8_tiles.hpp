@@ -540,47 +540,76 @@ hipError_t launch_tile(const Int8Args& a, hipStream_t s) {
 }
 
 // Tile shapes for more than 64 rows: how many run at once (one or two to a
-// compute unit) and how long a round of them takes, in us at width 4096. A round
-// that fills only part of the places of a shape that runs in pairs takes 0.6 of
-// a full one at least.
+// compute unit), how long a full round of them takes in us at width 4096, and
+// which share of that a round of few takes. Shapes that run in pairs keep that
+// share up to half the places. Measured in rounds of 0.1, 0.5, 1 and 2 (us):
+// 256x256 40 44 55 114, 192x256 38 35 42 97, 128x256 32 31 34 66, 160x128 26 26 38
+// 95, 128x128 30 31 41 85, 64x64 12 11 19 35.
 struct TileCost {
-  int bm, bn, at_once, us;
+  int bm, bn, at_once;
+  double us, least;
 };
-constexpr TileCost kTileCost[] = {{256, 256, 256, 57}, {192, 256, 256, 52}, {128, 256, 256, 38},
-                                  {160, 128, 512, 50}, {128, 128, 512, 42}, {64, 64, 512, 17}};
+constexpr TileCost kTileCost[] = {{256, 256, 256, 57.0, 0.65}, {192, 256, 256, 49.0, 0.68},
+                                  {128, 256, 256, 34.0, 0.88}, {160, 128, 512, 48.0, 0.62},
+                                  {128, 128, 512, 42.0, 0.68}, {64, 64, 512, 17.5, 0.62}};
 
+inline long long tiles_in(const TileCost& c, int rows, int vocab) {
+  return (long long)((rows + c.bm - 1) / c.bm) * ((vocab + c.bn - 1) / c.bn);
+}
+inline double rounds_us(const TileCost& c, int rows, int vocab) {
+  const long long tiles = tiles_in(c, rows, vocab), rest = tiles % c.at_once;
+  double part = 0.0;
+  if (rest > 0) {
+    double more = (double)rest / c.at_once;
+    if (c.at_once == 512) more = more > 0.5 ? 2.0 * more - 1.0 : 0.0;
+    part = c.least + (1.0 - c.least) * more;
+  }
+  return ((double)(tiles / c.at_once) + part) * c.us;
+}
 // The shape with the least rounds' time. Measured at width 4096 (us): 128 x 32000
 // 128x128 36, 128x256 39, 64x128 40; 128 x 128256 128x256 117, 128x128 131; 200 x 8960
 // 64x64 26, 128x128 31; 256 x 32000 128x256 40, 128x128 46, 160x128 48, 256x256 66;
 // 320 x 32000 160x128 53, 192x256 55, 256x256 60; 384 x 32000 192x256 57, 256x256 61;
 // 1024 x 151936 256x256 566, 128x256 622, 160x128 659, 128x128 698, 64x64 1213.
+constexpr int kTileShapes = sizeof(kTileCost) / sizeof(kTileCost[0]);
 inline int pick_tile(int rows, int vocab) {
   int best = 0;
-  double least = 0.0;
-  for (int i = 0; i < 6; ++i) {
+  for (int i = 1; i < kTileShapes; ++i)
+    if (rounds_us(kTileCost[i], rows, vocab) < rounds_us(kTileCost[best], rows, vocab)) best = i;
+  return best;
+}
+// The whole batch in one launch, or the channels that fill whole rounds of a
+// large shape first and the others in the shape that suits them, where that
+// saves more than a launch's 3 us (1000 x 50001: 225 us in one launch, 193 in two).
+// `first`: the channels of the first launch.
+struct TilePlan {
+  int shape, first;
+};
+inline TilePlan plan_tiles(int rows, int vocab, int width) {
+  TilePlan p{pick_tile(rows, vocab), vocab};
+  double least = rounds_us(kTileCost[p.shape], rows, vocab);
+  for (int i = 0; i < kTileShapes; ++i) {
     const TileCost& c = kTileCost[i];
-    const long long tiles =
-        (long long)((rows + c.bm - 1) / c.bm) * ((vocab + c.bn - 1) / c.bn);
-    const long long rest = tiles % c.at_once;
-    const double part = rest == 0 ? 0.0 : c.at_once == 512 ? 0.6 + 0.4 * rest / 512 : 1.0;
-    const double time = ((double)(tiles / c.at_once) + part) * c.us;
-    if (i == 0 || time < least) {
-      best = i;
-      least = time;
+    const long long full = tiles_in(c, rows, vocab) / c.at_once;
+    const long long first = full * c.at_once / ((rows + c.bm - 1) / c.bm) * c.bn;
+    if (first <= 0 || first >= vocab) continue;
+    const int rest = vocab - (int)first;
+    const double us = full * c.us + rounds_us(kTileCost[pick_tile(rows, rest)], rows, rest) +
+                      3.0 * 4096.0 / width;
+    if (us < least) {
+      p = TilePlan{i, (int)first};
+      least = us;
     }
   }
-  return best;
+  return p;
 }
 
 // ONCE where the rows' lines are whole (a line that two loads share would be
 // read twice): 1 x 128256 x 4096 78 us against 84, with rows 4100 apart 92
 // against 84.
 template <int DT, bool LINES>
-hipError_t launch_direct(const Int8Args& a, hipStream_t s) {
-  if (a.rows <= 16) return launch_ring<DT, 16, 64, 1, 4, 256, 4, LINES>(a, s);
-  if (a.rows <= 32) return launch_ring<DT, 32, 64, 1, 4, 128, 4, LINES>(a, s);
-  if (a.rows <= 64) return launch_ring<DT, 64, 128, 1, 4, 128, 3, LINES>(a, s);
-  switch (pick_tile(a.rows, a.vocab)) {
+hipError_t launch_shape(const Int8Args& a, int shape, hipStream_t s) {
+  switch (shape) {
     case 0: return launch_ring<DT, 256, 256, 2, 4, 128, 2, false>(a, s);
     case 1: return launch_ring<DT, 192, 256, 2, 4, 128, 2, false>(a, s);
     case 2: return launch_ring<DT, 128, 256, 2, 4, 128, 3, LINES>(a, s);
@@ -588,6 +617,23 @@ hipError_t launch_direct(const Int8Args& a, hipStream_t s) {
     case 4: return launch_ring<DT, 128, 128, 2, 2, 128, 2, LINES>(a, s);
     default: return launch_ring<DT, 64, 64, 2, 2, 128, 4, LINES>(a, s);
   }
+}
+template <int DT, bool LINES>
+hipError_t launch_direct(const Int8Args& a, hipStream_t s) {
+  if (a.rows <= 16) return launch_ring<DT, 16, 64, 1, 4, 256, 4, LINES>(a, s);
+  if (a.rows <= 32) return launch_ring<DT, 32, 64, 1, 4, 128, 4, LINES>(a, s);
+  if (a.rows <= 64) return launch_ring<DT, 64, 128, 1, 4, 128, 3, LINES>(a, s);
+  const TilePlan p = plan_tiles(a.rows, a.vocab, a.width);
+  Int8Args part = a;
+  part.vocab = p.first;
+  const hipError_t e = launch_shape<DT, LINES>(part, p.shape, s);
+  if (e != hipSuccess || p.first == a.vocab) return e;
+  part.vocab = a.vocab - p.first;
+  part.w += (long long)p.first * a.w_stride;
+  part.w_scale += p.first;
+  if (a.bias) part.bias += p.first;
+  part.out += (long long)p.first * Fmt<DT>::ESZ;
+  return launch_shape<DT, LINES>(part, pick_tile(a.rows, part.vocab), s);
 }
 
 template <int DT>
