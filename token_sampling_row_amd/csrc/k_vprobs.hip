@@ -10,13 +10,22 @@ namespace {
 template <int DT> constexpr int kVpWaves = DT == 0 ? 16 : 8;
 constexpr int kVpSliceWaves = 4;
 constexpr int kVpSliceBlock = kVpSliceWaves * kWave;
+// Batches of more bytes of target rows than this are read past the caches:
+// 256 x 128256 fp32 39 us against 44, but 64 x 32000, which stays in them between
+// the model and this call, 12 us against 10.
+constexpr long long kVpOnceBytes = 48ll << 20;
 constexpr int kVpGroup = 4;   // spans of a group; a wavefront has two groups' loads on their way
 
-// How many workgroups share a row's sums (1: the one-launch kernel).
+// How many workgroups share a row's sums (1: the one-launch kernel, as fast up
+// to 32 groups: 64 x 32000 fp32 9.8 us). A wavefront takes two groups at a time,
+// or one where that leaves places empty (33 x 151935 bf16 11.4 us against 11.9,
+// but 64 x 128256 bf16 15.7 against 14.5); 256 x 128256 fp32 with eight
+// workgroups to a row 37 us, with four 39.
 int vp_slices(int rows, int groups, int ws_rows) {
   if (rows > ws_rows || groups <= 32) return 1;
-  const int want = (1024 + rows - 1) / rows;
-  const int most = (groups + 2 * kVpSliceWaves - 1) / (2 * kVpSliceWaves);
+  const int one = (groups + kVpSliceWaves - 1) / kVpSliceWaves;
+  const int most = rows * one <= 768 ? one : (one + 1) / 2;
+  const int want = (2048 + rows - 1) / rows;
   return want < most ? want : most;
 }
 
@@ -70,12 +79,14 @@ struct VpRow {
   int V;
   int x;                    // the token whose certain draft is taken off (SUB 2)
   int rep, groups;
+  bool once;                // the rows of the batch outgrow the caches
 };
 template <int DT>
 __device__ __forceinline__ VpRow vp_row(const VprobsArgs& a, int b, int kept, int x, int rep,
                                         int groups) {
   return VpRow{a.target + b * a.t_seq + kept * a.t_row,
-               a.draft ? a.draft + b * a.d_seq + kept * a.d_row : nullptr, a.V, x, rep, groups};
+               a.draft ? a.draft + b * a.d_seq + kept * a.d_row : nullptr, a.V, x, rep, groups,
+               (long long)a.rows * a.V * Fmt<DT>::ESZ >= kVpOnceBytes};
 }
 
 // Weights of one chunk in 64 bits: the target's probabilities, less the draft's
@@ -123,7 +134,14 @@ struct VpGroup {
   __device__ __forceinline__ void load(const VpRow& r, int s0, int lane) {
     constexpr int EPC = Fmt<DT>::EPC, ESZ = Fmt<DT>::ESZ, SPAN = kWave * EPC;
     const int whole = r.V / SPAN;
-    if (whole > 0) {
+    if (whole > 0 && r.once) {
+#pragma unroll
+      for (int i = 0; i < kVpGroup; ++i) {
+        const long long at = (long long)min(s0 + i, whole - 1) * (SPAN * ESZ);
+        p[i] = load16_once(r.p + at + lane * 16);
+        if constexpr (SUB == 1) q[i] = load16_once(r.q + at + lane * 16);
+      }
+    } else if (whole > 0) {
 #pragma unroll
       for (int i = 0; i < kVpGroup; ++i) {
         const long long at = (long long)min(s0 + i, whole - 1) * (SPAN * ESZ);   // the same in all lanes
@@ -383,7 +401,7 @@ __global__ __launch_bounds__(kVpSliceBlock) void vprobs_draw_kernel(VprobsArgs a
     const VpRow r = vp_row<DT>(a, b, cut.y, cut.w, rep, groups);
     int sub = !cut.z ? 0 : a.draft ? 1 : 2;
     VpOwner o = vp_owner(sums, groups, v, lane);
-    if (sub != 0 && o.total == 0.0) {
+    if (sub != 0 && o.total == 0.0) {   // nothing is left of the target
       sub = 0;
       __syncthreads();
       vp_sums_of<DT>(r, 0, wave, kVpSliceWaves, groups, lane, sums);

@@ -31,8 +31,12 @@ __device__ __forceinline__ void store_words(void* p, const uint32_t* w) {
 }
 
 // 16 bytes, at any byte, that are not kept in the caches.
+typedef uint32_t Any4 __attribute__((ext_vector_type(4), aligned(1)));
+__device__ __forceinline__ uint4 load16_once(const void* p) {
+  const Any4 v = __builtin_nontemporal_load(static_cast<const Any4*>(p));
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
 __device__ __forceinline__ void store16_once(void* p, uint4 v) {
-  typedef uint32_t Any4 __attribute__((ext_vector_type(4), aligned(1)));
   const Any4 w = {v.x, v.y, v.z, v.w};
   __builtin_nontemporal_store(w, static_cast<Any4*>(p));
 }
