@@ -350,3 +350,20 @@ def test_refusals(s):
             few.verify_probs(p, q, x, u, v)
         assert e.value.code == 1
     assert s.verify_probs(p[:0], q[:0], x[:0], u[:0], v[:0])[0].shape == (0, K + 1)
+
+
+@pytest.mark.parametrize("groups,last", [(32, 31), (40, 32)])
+def test_draw_where_sums_of_two_orders_straddle_the_aim(s, groups, last):
+    """Weights 1, 2^-53, 2^-53, 1 in the first, second, fourth and last of runs of
+    1024 ids: their running total is 1 in one order of addition and 1 + 2^-52 in
+    another, and half of the total is 1. Runs without a weight lie where the
+    orders part; the draw takes a token with a weight all the same."""
+    ids = [0, 1024, 3 * 1024, last * 1024]
+    p = np.zeros((1, 2, groups * 1024), np.float32)
+    p[0, 0, ids] = [1.0, 2.0 ** -53, 2.0 ** -53, 1.0]
+    status = torch.full((1,), -1, dtype=torch.int32, device=device())
+    tokens, accepted = s.verify_probs(
+        dev(p), None, dev(np.zeros((1, 1), np.int32)), dev(np.zeros((1, 1), np.float32)),
+        dev(np.array([0.5], np.float32)), draft_lens=dev(np.zeros(1, np.int32)), out_status=status)
+    assert int(status[0]) == 0 and int(accepted[0]) == 0
+    assert int(tokens[0, 0]) in ids[2:] and int(tokens[0, 1]) == -1

@@ -234,11 +234,14 @@ __device__ __forceinline__ VpOwner vp_owner(const double* sums, int groups, floa
   VpOwner o;
   o.total = readlane_f64(incl, kWave - 1);
   const double aim = (double)v * o.total;
-  const unsigned long long over = __ballot(incl > aim);
+  // the totals of different lanes are added in different orders, so one may pass
+  // aim at a lane that adds nothing: only lanes with a weight are looked at
+  const unsigned long long any = __ballot(mine > 0.0);
+  const unsigned long long over = __ballot(mine > 0.0 && incl > aim);
   o.group = -1;
   o.base = 0.0;
-  if (!over) return o;   // total 0 or NaN
-  const int l = __ffsll((long long)over) - 1;
+  if (!any) return o;   // total 0 or NaN
+  const int l = over ? __ffsll((long long)over) - 1 : 63 - __clzll((long long)any);
   double c = l > 0 ? readlane_f64(incl, l - 1) : 0.0;
   for (int k = 0; k < per; ++k) {
     const int g = l * per + k;
