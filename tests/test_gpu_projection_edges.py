@@ -197,6 +197,13 @@ def test_refusals_through_the_c_interface(s):
     for bad in (dict(width=131072, cst=131072, wst=131072), dict(cst=1 << 23), dict(wst=1 << 23)):
         assert logits(**bad) == 4, bad
 
+    # more channels than a launch takes, on a handle that allows them
+    with tsr.Sampler(0, max_rows=1, max_vocab=1 << 30, max_k=1, seed=0) as big:
+        n = (1 << 29) + 1
+        hd = tsr._Head(vp(b), 64, vp(sc), None, n, 64)
+        assert lib.int8_logits(big._h, vp(b), 64, vp(sc), 1, ctypes.byref(hd), vp(out), 0, n,
+                               None) == 4
+
     prm = tsr._Params(1.0, 0, 1.0, 0.0, 0)
 
     def hidden(x=vp(f), dt=0, rows=4, stride=64, q=vp(b), qs=64, scale=vp(sc), lg=vp(out),

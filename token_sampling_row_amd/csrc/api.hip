@@ -112,6 +112,7 @@ constexpr int kMaxQuantRows = (1 << 24) - 1;   // 256 threads a row: fewer than 
 // sums of products of 8-bit integers fit 32 bits: 2^17 - 1 times (-128)^2
 constexpr int kMaxInt8Width = (1 << 17) - 1;
 constexpr int64_t kMaxInt8Stride = 1 << 23;   // a tile's 256 rows within 2^31 bytes
+constexpr int kMaxInt8Vocab = 1 << 29;        // 256 threads to 64 channels: fewer than 2^32
 constexpr int kMaxWideVocab = 1 << 30;          // ids past the last one stay whole numbers
 constexpr int kMaxVprobsRows = (1 << 22) - 1;   // 1024 threads a sequence: fewer than 2^32
 
@@ -139,8 +140,8 @@ int check_int8(tsr_handle h, const int8_t* codes, int64_t codes_stride, const fl
   if (!word_aligned(code_scale) || !word_aligned(head->scale) || !word_aligned(head->bias) ||
       !elem_aligned(out_logits, dtype))
     return TSR_EINVAL;
-  if (head->width > kMaxInt8Width || head->vocab > kMaxWideVocab || codes_stride >= kMaxInt8Stride ||
-      head->weight_stride >= kMaxInt8Stride)
+  if (head->width > kMaxInt8Width || head->vocab > kMaxInt8Vocab ||
+      codes_stride >= kMaxInt8Stride || head->weight_stride >= kMaxInt8Stride)
     return TSR_EUNSUPPORTED;
   return TSR_OK;
 }
