@@ -276,6 +276,8 @@ def test_refusals(s):
             lambda: s.quantize_rows(h, out=c, scale=cs[:3]),
             lambda: s.int8_logits(c, cs[:3], w, ws),
             lambda: s.int8_logits(c[:, :63], cs, w, ws),
+            lambda: s.int8_logits(c[0], cs, w, ws),
+            lambda: s.int8_logits(c[0, 0], cs, w, ws),
             lambda: s.int8_logits(c, cs, w.t(), ws),
             lambda: s.int8_logits(c, cs, w, ws[:31]),
             lambda: s.int8_logits(c, cs, w, ws.double()),

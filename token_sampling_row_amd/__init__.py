@@ -504,6 +504,8 @@ class Sampler:
         (float32 or bfloat16, the default) or in `out`."""
         torch = _t()
         head = self._head(weight, w_scale, bias)
+        if codes.dim() != 2:
+            raise ValueError("codes: not [rows, width]")
         rows, vocab = codes.shape[0], head.vocab
         stride = self._codes(codes, scale, rows, head.width, "codes")
         if out is None:
@@ -604,7 +606,8 @@ class Sampler:
             _check(load_library().verify_probs(
                 self._h, target.data_ptr(), t_seq, t_row, d_ptr, d_seq, d_row, dt,
                 draft_tokens.data_ptr(), n_ptr, accept_u.data_ptr(), draw_u.data_ptr(), rows, K,
-                vocab, out_tokens.data_ptr(), out_accepted.data_ptr(), s_ptr, _stream_on(dev, stream)), "verify_probs")
+                vocab, out_tokens.data_ptr(), out_accepted.data_ptr(), s_ptr,
+                _stream_on(dev, stream)), "verify_probs")
         return out_tokens, out_accepted
 
     def philox(self, counters, stream=None):
