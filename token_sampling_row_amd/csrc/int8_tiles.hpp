@@ -85,7 +85,9 @@ struct Tile {
     wn = wave / WM;
     return tile < tiles;
   }
-  static __device__ __forceinline__ int turn(int r) { return TK == 64 ? (r >> 1) & 3 : r & 7; }
+  static __device__ __forceinline__ int turn(int r) {
+    return TK == 64 ? (r >> 1) & 3 : TK == 128 ? r & 7 : r & 15;
+  }
   // piece q of this wavefront: the row its lane brings, and which bytes of it
   __device__ __forceinline__ int row_of(int q, int pieces) const {
     return (wave * pieces + q) * PR + lane / CH;
