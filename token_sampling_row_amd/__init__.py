@@ -444,11 +444,19 @@ class Sampler:
             raise ValueError(f"{what}: not a contiguous {list(shape)} {dtype} on the handle's GPU")
         return t.data_ptr()
 
-    def _codes(self, codes, scale, rows, width, what):
-        if codes.dtype is not _torch.int8:
-            raise ValueError(f"{what}: not int8")
-        self._vector(scale, _torch.float32, what, rows)
-        return self._rows(codes, rows, width, what)
+    def _codes(self, codes, scale, what):
+        """Rows, width and row stride of codes [rows, width] with a scale per row."""
+        dev = self.device
+        if codes.dtype is not _torch.int8 or codes.dim() != 2 or codes.get_device() != dev:
+            raise ValueError(f"{what}: not an int8 matrix on the handle's GPU")
+        rows, width = codes.shape
+        stride, one = codes.stride()
+        if width < 1 or (width > 1 and one != 1) or (rows > 1 and stride < width):
+            raise ValueError(f"{what}: rows empty, not contiguous, or overlapping")
+        if scale.dtype is not _torch.float32 or scale.shape != (rows,) or \
+                scale.get_device() != dev or not scale.is_contiguous():
+            self._vector(scale, _torch.float32, f"scale of the {what}", rows)
+        return rows, width, stride if stride > width else width
 
     def _new_codes(self, stream, device, rows, width):
         """[rows, width] int8 whose rows start at multiples of 128 bytes, as
@@ -488,14 +496,11 @@ class Sampler:
         return out, scale
 
     def _head(self, weight, w_scale, bias):
-        if weight.dim() != 2:
-            raise ValueError("weight: not [vocab, width]")
-        vocab, width = weight.shape
-        stride = self._codes(weight, w_scale, vocab, width, "weight")
+        vocab, width, stride = self._codes(weight, w_scale, "weight")
         if vocab < 1:
             raise ValueError("weight: no channel")
         b = None if bias is None else self._vector(bias, _torch.float32, "bias", vocab)
-        return _Head(weight.data_ptr(), stride, w_scale.data_ptr(), b, vocab, width)
+        return vocab, width, _Head(weight.data_ptr(), stride, w_scale.data_ptr(), b, vocab, width)
 
     def int8_logits(self, codes, scale, weight, w_scale, bias=None, dtype=None, out=None,
                     stream=None):
@@ -503,11 +508,10 @@ class Sampler:
         quantize_rows), bias [V] float32 or None -> logits [rows, V], of `dtype`
         (float32 or bfloat16, the default) or in `out`."""
         torch = _t()
-        head = self._head(weight, w_scale, bias)
-        if codes.dim() != 2:
-            raise ValueError("codes: not [rows, width]")
-        rows, vocab = codes.shape[0], head.vocab
-        stride = self._codes(codes, scale, rows, head.width, "codes")
+        vocab, width, head = self._head(weight, w_scale, bias)
+        rows, w, stride = self._codes(codes, scale, "codes")
+        if w != width:
+            raise ValueError(f"codes: not [{rows}, {width}]")
         if out is None:
             out = _new(stream, codes.device, dtype or torch.bfloat16, rows, vocab)
             out_stride = vocab
@@ -528,17 +532,17 @@ class Sampler:
         bfloat16 by default); ``diag`` as in sample_rows."""
         torch = _t()
         hdt = _dtype_code(hidden)
-        head = self._head(weight, w_scale, bias)
+        vocab, width, head = self._head(weight, w_scale, bias)
         if hidden.dim() != 2:
             raise ValueError("hidden: not a matrix")
-        rows, dev, vocab = hidden.shape[0], hidden.device, head.vocab
-        stride = self._rows(hidden, rows, head.width, "hidden")
+        rows, dev = hidden.shape[0], hidden.device
+        stride = self._rows(hidden, rows, width, "hidden")
         if logits is None:
             logits = _new(stream, dev, dtype or torch.bfloat16, rows, vocab)
         elif self._rows(logits, rows, vocab, "logits") != vocab:
             raise ValueError("logits: not contiguous")
         ldt = _dtype_code(logits)
-        codes = self._new_codes(stream, dev, rows, head.width)
+        codes = self._new_codes(stream, dev, rows, width)
         scale = _new(stream, dev, torch.float32, rows)
         if out is None:
             out = _new(stream, dev, torch.int32, rows)
@@ -552,7 +556,7 @@ class Sampler:
         if rows:
             _check(load_library().sample_hidden(
                 self._h, hidden.data_ptr(), hdt, rows, stride, ctypes.byref(head),
-                codes.data_ptr(), head.width + -head.width % 128, scale.data_ptr(),
+                codes.data_ptr(), width + -width % 128, scale.data_ptr(),
                 logits.data_ptr(), ldt, ctypes.byref(cp), int(step), out.data_ptr(),
                 ctypes.byref(d) if d is not None else None, _stream_on(self.device, stream)),
                 "sample_hidden")
