@@ -51,6 +51,43 @@ def test_codes_match(s, dtype, rows, width):
     check_codes(s.quantize_rows(x), v)
 
 
+@pytest.mark.parametrize("dtype,epc", [("f32", 4), ("bf16", 8)])
+@pytest.mark.parametrize("rows", [4095, 4097])
+@pytest.mark.parametrize("chunks", [1, 64, 65, 128, 129, 192, 193, 256, 257, 384, 385, 512])
+def test_codes_of_many_rows(s, dtype, epc, rows, chunks):
+    """Rows of one, two and four wavefronts, on either side of each limit; a row
+    number that does not fill the last workgroup; a partial chunk behind."""
+    width = chunks * epc + chunks % 3 % epc
+    g = torch.Generator(device()).manual_seed(chunks)
+    x = torch.randn(rows, width, device=device(), generator=g)
+    x = (x * torch.exp(torch.randn(rows, 1, device=device(), generator=g)))
+    x[7, width - 1], x[rows - 1, 0], x[rows - 2] = float("nan"), 1e30, 0.0
+    x = x.to({"f32": torch.float32, "bf16": torch.bfloat16}[dtype])
+    codes, scale = s.quantize_rows(x)
+    some = [0, 1, 7, rows // 2, rows - 3, rows - 2, rows - 1]
+    check_codes((codes[some], scale[some]), x[some].float().cpu().numpy())
+    for r0 in range(0, rows, 1000):   # the same rows, fewer at a time
+        c, sc = s.quantize_rows(x[r0:r0 + 1000])
+        assert torch.equal(c, codes[r0:r0 + 1000])
+        assert torch.equal(sc.view(torch.int32), scale[r0:r0 + 1000].view(torch.int32))
+
+
+@pytest.mark.parametrize("dtype,rows,width", [("bf16", 100001, 1007), ("bf16", 63001, 1601),
+                                              ("bf16", 24581, 4097), ("f32", 9001, 5603),
+                                              ("f32", 6301, 8000), ("f32", 66003, 763),
+                                              ("f32", 36003, 1400)])
+def test_codes_of_large_inputs(s, dtype, rows, width):
+    """Inputs that outgrow the caches, against the same rows in small batches."""
+    td = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    x = torch.empty(rows, width, dtype=td, device=device()).normal_(
+        generator=torch.Generator(device()).manual_seed(rows))
+    codes, scale = s.quantize_rows(x)
+    check_codes((codes[-3:], scale[-3:]), x[-3:].float().cpu().numpy())
+    for r0 in range(0, rows, 4000):
+        c, sc = s.quantize_rows(x[r0:r0 + 4000])
+        assert torch.equal(c, codes[r0:r0 + 4000]) and torch.equal(sc, scale[r0:r0 + 4000])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_codes_of_special_rows(s, dtype):
     """Zeros, negative zeros, halves, one value, NaN, infinities at either end,

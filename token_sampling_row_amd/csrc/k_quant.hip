@@ -1,8 +1,10 @@
 // Per-row 8-bit codes of float rows (quantize_rows): weights per channel,
-// hidden states per token.
+// hidden states per token. s = max |x| / 127, q = x / s to the nearest.
 //
 // Bound by memory: a row is read once, held in registers between its largest
-// magnitude and its codes.
+// magnitude and its codes. 32000 x 4096 bf16 (393 MB) 62 us, 6.3 TB/s (a copy
+// runs at 5.1, reads alone at 6.9); 333 x 5003 fp32 4.7 us and 5 x 4096 bf16 2.8,
+// a launch, one trip to memory and back.
 #include "kernels.hpp"
 #include "wide_mem.hpp"
 
@@ -10,6 +12,10 @@ namespace tsr {
 namespace {
 
 constexpr int kQuantBlock = 256;
+// Inputs of more bytes than this are read past the caches, which could not keep
+// them: 32000 x 4096 bf16 62 us against 67. Smaller ones may be there still:
+// 16384 x 4096 bf16 31 us read from them, 34 past them.
+constexpr long long kQuantOnceBytes = 192ll << 20;
 
 // A row's scale from the bits of its largest magnitude (float bits order as the
 // values do, infinities and NaN above).
@@ -93,23 +99,24 @@ __device__ __forceinline__ void store_codes(int8_t* row, int i0, int width, cons
   }
 }
 
-// The largest of `m` over the WPR wavefronts of a row.
+// The largest of `m` over the WPR wavefronts of a row, neighbours in the workgroup.
 template <int WPR>
 __device__ __forceinline__ uint32_t row_top(uint32_t m) {
   m = wave_max_u32(m);
   if constexpr (WPR > 1) {
-    __shared__ uint32_t each[WPR];
+    __shared__ uint32_t each[kQuantBlock / kWave];
     if ((threadIdx.x & (kWave - 1)) == 0) each[threadIdx.x / kWave] = m;
     __syncthreads();
+    const int first = threadIdx.x / (WPR * kWave) * WPR;
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) m = max(m, each[w]);
+    for (int w = 0; w < WPR; ++w) m = max(m, each[first + w]);
   }
   return m;
 }
 
 // Rows of up to NC chunks a lane, in registers; WPR wavefronts to a row, four in
-// a workgroup.
-template <int DT, int WPR, int NC>
+// a workgroup. ONCE: read past the caches.
+template <int DT, int WPR, int NC, bool ONCE>
 __global__ __launch_bounds__(kQuantBlock) void quant_kernel(const unsigned char* x,
                                                             long long stride_bytes, int rows,
                                                             int width, int8_t* q,
@@ -118,13 +125,14 @@ __global__ __launch_bounds__(kQuantBlock) void quant_kernel(const unsigned char*
   const int part = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
   const int t = threadIdx.x % T;
   const long long r = (long long)blockIdx.x * RPB + part;
-  if (r >= rows) return;   // whole wavefronts of rows of their own (RPB > 1)
-  const unsigned char* row = x + r * stride_bytes;
+  const unsigned char* row = x + min(r, (long long)rows - 1) * stride_bytes;
   const int whole = width / EPC;   // at least one
   uint4 c[NC];
 #pragma unroll
-  for (int j = 0; j < NC; ++j)   // chunks past the last whole one repeat it
-    c[j] = load16(row + (long long)min(j * T + t, whole - 1) * 16);
+  for (int j = 0; j < NC; ++j) {   // chunks past the last whole one repeat it
+    const unsigned char* p = row + (long long)min(j * T + t, whole - 1) * 16;
+    c[j] = ONCE ? load16_once(p) : load16(p);
+  }
   uint4 rest{};
   const bool partial = whole * EPC < width && t == whole % T;
   if (partial) rest = load_chunk_zero<DT>(row, (long long)whole * EPC, width);
@@ -132,6 +140,7 @@ __global__ __launch_bounds__(kQuantBlock) void quant_kernel(const unsigned char*
 #pragma unroll
   for (int j = 0; j < NC; ++j) m = max(m, top_of<DT>(c[j]));
   const RowScale a(row_top<WPR>(m));
+  if (r >= rows) return;
   if (t == 0) scale[r] = a.out;
   int8_t* out = q + r * q_stride;
   uint32_t w[EPC / 4];
@@ -170,23 +179,49 @@ __global__ __launch_bounds__(kQuantBlock) void quant_wide_kernel(const unsigned 
   }
 }
 
-template <int DT, int WPR, int NC>
+template <int DT, int WPR, int NC, bool ONCE>
 hipError_t launch_nc(const unsigned char* x, int rows, int width, long long stride_bytes,
                      int8_t* q, long long q_stride, float* scale, hipStream_t s) {
   constexpr int RPB = kQuantBlock / (WPR * kWave);
-  hipLaunchKernelGGL((quant_kernel<DT, WPR, NC>), dim3((rows + RPB - 1) / RPB), dim3(kQuantBlock),
-                     0, s, x, stride_bytes, rows, width, q, q_stride, scale);
+  hipLaunchKernelGGL((quant_kernel<DT, WPR, NC, ONCE>), dim3((rows + RPB - 1) / RPB),
+                     dim3(kQuantBlock), 0, s, x, stride_bytes, rows, width, q, q_stride, scale);
   return hipGetLastError();
 }
 
-template <int DT, int WPR>
+template <int DT, int WPR, bool ONCE>
 hipError_t launch_wpr(const unsigned char* x, int rows, int width, long long stride_bytes,
                       int8_t* q, long long q_stride, float* scale, hipStream_t s) {
+  // the rule below leaves two wavefronts two chunks a lane at least, and four as
+  // many of a large input; fewer than four take three at most
+  constexpr bool ONE = WPR == 1 || (WPR == 4 && !ONCE);
   const int per = (width / Fmt<DT>::EPC + WPR * kWave - 1) / (WPR * kWave);
-  if (per <= 1) return launch_nc<DT, WPR, 1>(x, rows, width, stride_bytes, q, q_stride, scale, s);
-  if (per <= 2) return launch_nc<DT, WPR, 2>(x, rows, width, stride_bytes, q, q_stride, scale, s);
-  if (per <= 4) return launch_nc<DT, WPR, 4>(x, rows, width, stride_bytes, q, q_stride, scale, s);
-  return launch_nc<DT, WPR, 8>(x, rows, width, stride_bytes, q, q_stride, scale, s);
+  if constexpr (ONE)
+    if (per <= 1)
+      return launch_nc<DT, WPR, 1, ONCE>(x, rows, width, stride_bytes, q, q_stride, scale, s);
+  if (per <= 2)
+    return launch_nc<DT, WPR, 2, ONCE>(x, rows, width, stride_bytes, q, q_stride, scale, s);
+  if constexpr (WPR < 4)
+    return launch_nc<DT, WPR, 3, ONCE>(x, rows, width, stride_bytes, q, q_stride, scale, s);
+  if (per <= 4)
+    return launch_nc<DT, WPR, 4, ONCE>(x, rows, width, stride_bytes, q, q_stride, scale, s);
+  return launch_nc<DT, WPR, 8, ONCE>(x, rows, width, stride_bytes, q, q_stride, scale, s);
+}
+
+// Wavefronts to a row. Many rows fill the card however they are cut, and fewer
+// wavefronts to a row spend less on their largest value; past three chunks a
+// lane the registers leave too few rows on their way. In us with 1, 2 and 4:
+// bf16 126953 x 1024 66 79 118, 84635 x 1536 64 72 91, 16384 x 2048 21 21 23,
+// 50781 x 2560 68 65 75, 31738 x 4096 64 62 62. Few rows are bound by the time of
+// one: 2048 x 1024 4.4 4.3 4.6, 2048 x 2048 6.2 5.5 5.2, 300 x 4096 7.3 4.9 4.3.
+template <int DT, bool ONCE>
+hipError_t launch_once(const unsigned char* x, int rows, int width, long long stride_bytes,
+                       int8_t* q, long long q_stride, float* scale, hipStream_t s) {
+  const int whole = width / Fmt<DT>::EPC;
+  if (whole <= (rows >= 4096 ? 3 : 2) * kWave)
+    return launch_wpr<DT, 1, ONCE>(x, rows, width, stride_bytes, q, q_stride, scale, s);
+  if (rows >= 4096 && whole <= 6 * kWave)
+    return launch_wpr<DT, 2, ONCE>(x, rows, width, stride_bytes, q, q_stride, scale, s);
+  return launch_wpr<DT, 4, ONCE>(x, rows, width, stride_bytes, q, q_stride, scale, s);
 }
 
 template <int DT>
@@ -198,9 +233,9 @@ hipError_t launch_dt(const unsigned char* x, int rows, int width, long long stri
                        stride_bytes, width, q, q_stride, scale);
     return hipGetLastError();
   }
-  if (rows >= 2048 && whole <= 8 * kWave)
-    return launch_wpr<DT, 1>(x, rows, width, stride_bytes, q, q_stride, scale, s);
-  return launch_wpr<DT, 4>(x, rows, width, stride_bytes, q, q_stride, scale, s);
+  return (long long)rows * width * Fmt<DT>::ESZ > kQuantOnceBytes
+             ? launch_once<DT, true>(x, rows, width, stride_bytes, q, q_stride, scale, s)
+             : launch_once<DT, false>(x, rows, width, stride_bytes, q, q_stride, scale, s);
 }
 
 }  // namespace
