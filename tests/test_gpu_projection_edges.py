@@ -237,33 +237,63 @@ def test_refusals_through_the_c_interface(s):
     assert bool((out == -7).all()) and bool((tok == -7).all()) and not b.any()
 
 
+def large_batch(s, dtype, rows, vocab, width, stride):
+    """Logits of a batch that fills the card, held to the bound around float64
+    products of whole numbers below 2^53."""
+    from oracle import int8 as oi
+    g = torch.Generator(device()).manual_seed(rows)
+
+    def matrix(n):
+        m = torch.randint(-128, 128, (n, stride), dtype=torch.int8, device=device(), generator=g)
+        return m[:, :width]
+
+    c, w = matrix(rows), matrix(vocab)
+    cs = torch.rand(rows, device=device(), generator=g)
+    ws = torch.rand(vocab, device=device(), generator=g)
+    b = torch.randn(vocab, device=device(), generator=g) * 1000
+    got = s.int8_logits(c, cs, w, ws, bias=b,
+                        dtype={"f32": torch.float32, "bf16": torch.bfloat16}[dtype]).double()
+    product = (c.double() @ w.double().t()) * cs.double()[:, None] * ws.double()
+    want = product + b.double()
+    half = 2.0 ** -23 * product.abs() + 2.0 ** -24 * want.abs()
+    if dtype == "bf16":
+        half = half + 2.0 ** -8 * (want.abs() + half)
+    assert bool(((got - want).abs() <= half * (1 + 2.0 ** -20)).all())
+    # the same bound as the reference's
+    some = want[:2, :50].cpu().numpy(), product[:2, :50].abs().cpu().numpy()
+    assert np.allclose(oi.logits_bound(*some, dtype),
+                       (half * (1 + 2.0 ** -20))[:2, :50].cpu().numpy(), atol=1e-40)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,vocab", [(512, 32000), (384, 32003), (256, 32000), (320, 32001),
                                         (128, 32000), (200, 8960), (500, 31999), (1024, 33000)])
 def test_every_tile_shape(s, dtype, rows, vocab):
-    """Batches that fill the card, where each tile shape is the one taken, with
-    rows in whole lines, at words and at bytes, and with a partial stage; the
-    reference's sums are float64 products of whole numbers below 2^53."""
-    from oracle import int8 as oi
-    td = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
-    g = torch.Generator(device()).manual_seed(rows)
+    """Batches where each tile shape is the one taken, with rows in whole lines, at
+    words and at bytes, and with a partial stage."""
     for width in (384, 300, 641):
-        c = torch.randint(-128, 128, (rows, width), dtype=torch.int8, device=device(), generator=g)
-        w = torch.randint(-128, 128, (vocab, width), dtype=torch.int8, device=device(), generator=g)
-        cs = torch.rand(rows, device=device(), generator=g)
-        ws = torch.rand(vocab, device=device(), generator=g)
-        b = torch.randn(vocab, device=device(), generator=g) * 1000
-        got = s.int8_logits(c, cs, w, ws, bias=b, dtype=td).double()
-        product = (c.double() @ w.double().t()) * cs.double()[:, None] * ws.double()
-        want = product + b.double()
-        half = 2.0 ** -23 * product.abs() + 2.0 ** -24 * want.abs()
-        if dtype == "bf16":
-            half = half + 2.0 ** -8 * (want.abs() + half)
-        assert bool(((got - want).abs() <= half * (1 + 2.0 ** -20)).all())
-        # the same bound as the reference's
-        some = want[:2, :50].cpu().numpy(), product[:2, :50].abs().cpu().numpy()
-        assert np.allclose(oi.logits_bound(*some, dtype),
-                           (half * (1 + 2.0 ** -20))[:2, :50].cpu().numpy(), atol=1e-40)
+        large_batch(s, dtype, rows, vocab, width, width)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab,width,stride", [
+    (1000, 131072, 500, 512), (192, 131071, 500, 512), (320, 131072, 512, 512),
+    (128, 131073, 500, 512), (100, 40000, 1400, 1408), (700, 50001, 1100, 1152),
+    (90, 14000, 4000, 4096), (64, 40000, 1408, 1408), (30, 40001, 1400, 1408),
+    (9, 13000, 4100, 4224), (3, 13000, 4096, 4096)])
+def test_large_weights(s, dtype, rows, vocab, width, stride):
+    """Weights that outgrow the caches, in rows of whole lines; batches in one
+    launch and in two."""
+    large_batch(s, dtype, rows, vocab, width, stride)
+
+
+@pytest.mark.parametrize("rows", [512, 384, 320, 256])
+def test_stages_of_large_tiles(s, rows):
+    """One whole stage to more than two turns of the rings, without and with a
+    partial one behind."""
+    for stages in range(1, 15):
+        large_batch(s, "bf16", rows, 32000, 128 * stages, 128 * stages)
+        large_batch(s, "bf16", rows, 32000, 128 * stages + 60, 128 * stages + 64)
 
 
 @pytest.mark.parametrize("rows", [1, 5, 70])

@@ -6,6 +6,7 @@
 // row, or up to 256 of them, meets a run while it is in LDS.
 #pragma once
 
+#include <cmath>
 #include <type_traits>
 
 #include "kernels.hpp"
@@ -196,15 +197,15 @@ struct Tile {
   // and plus the bias in one rounding; float32 holds far more than the codes do.
   //
   // The results pass through LDS (`even` and `odd` in turn, each as large as a
-  // stage of the weight), so that a row's run of channels leaves in whole lines:
-  // written from the sums' own lanes, in pieces of 16 to 64 bytes, 64 rows of
-  // 128256 bfloat16 logits took 17 us of 105. Chunk c of LDS row r lies at place
-  // c ^ (r & 7).
+  // stage of the larger operand), so that a row's run of channels leaves in whole
+  // lines: from the sums' own lanes, in pieces of 16 to 64 bytes, 64 x 128256 took
+  // 110 us (105 so) and 1000 x 50001, whose rows end inside lines, 247 (221).
+  // Chunk c of LDS row r lies at place c ^ (r & 7).
   template <int DT>
   __device__ __forceinline__ void store(const Int8Args& a, const v4i (*acc)[MT], Scales& s,
                                         int8_t* even, int8_t* odd) const {
     constexpr int ESZ = Fmt<DT>::ESZ, EPC = Fmt<DT>::EPC, ROW = BN * ESZ, CB = ROW / 16;
-    constexpr int FIT = BN * TK / (16 * WM * ROW);
+    constexpr int FIT = (BM > BN ? BM : BN) * TK / (16 * WM * ROW);
     constexpr int UP = FIT < MT ? FIT : MT;   // blocks of rows a pass
     constexpr int RP = 16 * WM * UP;          // rows a pass
     static_assert(UP >= 1 && CB >= 8, "a pass fits a stage");
@@ -281,27 +282,33 @@ struct Tile {
   }
 };
 
-// Operands whose rows start at 4-byte words: loads go straight to LDS, RING
-// stages deep. The loads for later lie between the products, so that
-// a wavefront's matrix pipe does not wait while they are issued.
-template <int DT, int BM, int BN, int WM, int WN, int TK, int RING, bool ONCE>
+// Operands whose rows start at 4-byte words: loads go straight to LDS, XR stages
+// of the hidden rows and WR of the weight deep. The hidden rows are in the caches,
+// the weight comes from memory: where LDS does not hold three stages of both, it
+// holds two and three (1024 x 131072 x 4096 in 256 x 256: two and two 463 us, two
+// and three 432; with the weight in the caches 413, without loads 294). The loads
+// for later lie between the products, so that a wavefront's matrix pipe does not
+// wait while they are issued.
+template <int DT, int BM, int BN, int WM, int WN, int TK, int XR, int WR, bool ONCE>
 __global__ __launch_bounds__(WM* WN* kWave, 1) void int8_ring_kernel(Int8Args a, int m_tiles,
                                                                      int tiles) {
   using T = Tile<BM, BN, WM, WN, TK>;
   constexpr int MT = T::MT, NT = T::NT, XI = T::XI, WI = T::WI, H = T::H, DMAS = XI + WI;
-  static_assert(RING >= 2 && RING <= 4 && (RING * H) % 2 == 0, "ring");
+  constexpr int AHEAD = WR - XR, TURN = AHEAD == 0 ? XR : XR * WR;   // stages of a turn of both
+  static_assert(XR >= 2 && XR <= 4 && (AHEAD == 0 || (XR == 2 && WR == 3)), "ring");
+  static_assert((TURN * H) % 2 == 0, "ring");
   // one object per operand and stage: only so are loads into one stage known
   // not to meet reads of another
-  constexpr int XB = BM * TK, WB = BN * TK, X2 = RING > 2 ? XB : 16, W2 = RING > 2 ? WB : 16,
-                X3 = RING > 3 ? XB : 16, W3 = RING > 3 ? WB : 16;
-  __shared__ __attribute__((aligned(1024))) int8_t x0[XB];
-  __shared__ __attribute__((aligned(1024))) int8_t w0[WB];
-  __shared__ __attribute__((aligned(1024))) int8_t x1[XB];
-  __shared__ __attribute__((aligned(1024))) int8_t w1[WB];
-  __shared__ __attribute__((aligned(1024))) int8_t x2[X2];
-  __shared__ __attribute__((aligned(1024))) int8_t w2[W2];
-  __shared__ __attribute__((aligned(1024))) int8_t x3[X3];
-  __shared__ __attribute__((aligned(1024))) int8_t w3[W3];
+  __shared__ __attribute__((aligned(1024))) int8_t x0[BM * TK];
+  __shared__ __attribute__((aligned(1024))) int8_t w0[BN * TK];
+  __shared__ __attribute__((aligned(1024))) int8_t x1[BM * TK];
+  __shared__ __attribute__((aligned(1024))) int8_t w1[BN * TK];
+  __shared__ __attribute__((aligned(1024))) int8_t x2[XR > 2 ? BM * TK : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t w2[WR > 2 ? BN * TK : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t x3[XR > 3 ? BM * TK : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t w3[WR > 3 ? BN * TK : 16];
+  auto x_of = [&](int b) { return b % XR == 0 ? x0 : b % XR == 1 ? x1 : b % XR == 2 ? x2 : x3; };
+  auto w_of = [&](int b) { return b % WR == 0 ? w0 : b % WR == 1 ? w1 : b % WR == 2 ? w2 : w3; };
   T t;
   if (!t.place(m_tiles, tiles)) return;
   typename T::Scales scales;
@@ -317,26 +324,28 @@ __global__ __launch_bounds__(WM* WN* kWave, 1) void int8_ring_kernel(Int8Args a,
   T::clear(acc);
 
   const int stages = a.width / TK;
-  // piece q of stage b; past the last stage it reads nothing, and is counted
-  // by the waits all the same
+  // piece q of the hidden rows' stage b and of the weight's stage b + AHEAD; past
+  // the last stage it reads nothing, and is counted by the waits all the same
   auto fetch_piece = [&](int q, int b, int8_t* xs, int8_t* ws) {
-    const bool in = b < stages;
+    const int k = q < XI ? b : b + AHEAD;
+    const bool in = k < stages;
     if (q < XI)
       to_lds<false>(buffer_of(xb, in ? xn : 0), xs + (t.wave * XI + q) * 1024,
-                    xo[q < XI ? q : 0], in ? b * TK : 0);
+                    xo[q < XI ? q : 0], in ? k * TK : 0);
     else
       to_lds<ONCE>(buffer_of(wb, in ? wn : 0), ws + (t.wave * WI + q - XI) * 1024,
-                   wo[q < XI ? 0 : q - XI], in ? b * TK : 0);
+                   wo[q < XI ? 0 : q - XI], in ? k * TK : 0);
   };
-  auto fetch = [&](int b, int8_t* xs, int8_t* ws) {
+  auto fetch = [&](int q0, int b, int8_t* xs, int8_t* ws) {
 #pragma unroll
-    for (int q = 0; q < DMAS; ++q) fetch_piece(q, b, xs, ws);
+    for (int q = q0; q < DMAS; ++q) fetch_piece(q, b, xs, ws);
   };
-  fetch(0, x0, w0);
-  if constexpr (RING > 2) fetch(1, x1, w1);
-  if constexpr (RING > 3) fetch(2, x2, w2);
-  int8_t* const xl = RING == 2 ? x1 : RING == 3 ? x2 : x3;
-  int8_t* const wl = RING == 2 ? w1 : RING == 3 ? w2 : w3;
+  if constexpr (AHEAD > 0) fetch(XI, -1, nullptr, w0);   // the weight's first stage
+  fetch(0, 0, x0, w_of(AHEAD));
+  if constexpr (XR > 2) fetch(0, 1, x1, w1);
+  if constexpr (XR > 3) fetch(0, 2, x2, w2);
+  int8_t* const xl = x_of(XR - 1);
+  int8_t* const wl = w_of(WR - 1);
   if (stages * TK < a.width) {
     // a partial stage goes through registers, beside the first whole ones' loads
     t.fetch_partial(a, xb, wb, xo, wo, stages * TK, xl, wl);
@@ -345,26 +354,27 @@ __global__ __launch_bounds__(WM* WN* kWave, 1) void int8_ring_kernel(Int8Args a,
     __syncthreads();
   }
   if (stages > 0) {
-    fetch(RING - 1, xl, wl);
-    wait_loads<DMAS*(RING - 1)>();
+    fetch(0, XR - 1, xl, wl);
+    constexpr int LATER = AHEAD > 0 ? WI : 0;   // the weight's last pieces are for later
+    wait_loads<DMAS*(XR - 1) + LATER>();
     __builtin_amdgcn_s_barrier();
     sched_fence();
     v4i wv[2][NT], xv[2][MT];
 #pragma unroll
     for (int q = 0; q < NT + MT; ++q) t.read(q, x0, w0, 0, wv[0], xv[0]);
-    // Stage b = J of a turn of the ring. Its last product meets the next stage,
-    // which has landed for every wavefront behind the barrier; so has
-    // everyone's reading of this one, whose place takes stage b + RING.
-    auto stage = [&](auto j, auto more, int b, int8_t* xs, int8_t* ws, int8_t* xnext,
-                     int8_t* wnext) {
+    // Stage b = J of a turn of the rings. Its last product meets the next stage,
+    // which has landed for every wavefront behind the barrier; so has everyone's
+    // reading of this one, whose places take the stages b + XR and b + WR.
+    auto stage = [&](auto j, auto more, int b) {
       constexpr int J = decltype(j)::value, F = J * H;
       constexpr bool MORE = decltype(more)::value;
-      constexpr bool LAST = !MORE && J + 1 == RING;   // no stage follows
+      constexpr bool LAST = !MORE && J + 1 == XR;   // no stage follows
+      int8_t *xs = x_of(J), *ws = w_of(J), *xnext = x_of(J + 1), *wnext = w_of(J + 1);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         const bool to_next = h + 1 == H;
         if (to_next && !LAST) {
-          wait_loads<DMAS*(MORE ? RING - 2 : J + 2 < RING ? RING - 2 - J : 0)>();
+          wait_loads<DMAS*(MORE ? XR - 2 : J + 2 < XR ? XR - 2 - J : 0) + LATER>();
           __builtin_amdgcn_s_barrier();
           sched_fence();
         }
@@ -382,7 +392,7 @@ __global__ __launch_bounds__(WM* WN* kWave, 1) void int8_ring_kernel(Int8Args a,
           if (MORE && to_next) {
 #pragma unroll
             for (int q = u * DMAS / MT; q < (u + 1) * DMAS / MT; ++q)
-              fetch_piece(q, b + RING, xs, ws);
+              fetch_piece(q, b + XR, xs, ws);
           }
           T::multiply_row(acc, u, wv[(F + h) & 1], xv[(F + h) & 1]);
           sched_fence();
@@ -393,30 +403,49 @@ __global__ __launch_bounds__(WM* WN* kWave, 1) void int8_ring_kernel(Int8Args a,
     constexpr std::integral_constant<int, 1> j1{};
     constexpr std::integral_constant<int, 2> j2{};
     constexpr std::integral_constant<int, 3> j3{};
+    constexpr std::integral_constant<int, 4> j4{};
+    constexpr std::integral_constant<int, 5> j5{};
+    constexpr std::true_type more{};
+    constexpr std::false_type no_more{};
     int b = 0;
-    for (; b + RING < stages; b += RING) {
-      stage(j0, std::true_type{}, b, x0, w0, x1, w1);
-      stage(j1, std::true_type{}, b + 1, x1, w1, RING > 2 ? x2 : x0, RING > 2 ? w2 : w0);
-      if constexpr (RING > 2)
-        stage(j2, std::true_type{}, b + 2, x2, w2, RING > 3 ? x3 : x0, RING > 3 ? w3 : w0);
-      if constexpr (RING > 3) stage(j3, std::true_type{}, b + 3, x3, w3, x0, w0);
-    }
-    // the last turn, of 1 to RING stages
-    stage(j0, std::false_type{}, b, x0, w0, x1, w1);
-    if (b + 1 < stages) {
-      stage(j1, std::false_type{}, b + 1, x1, w1, RING > 2 ? x2 : x0, RING > 2 ? w2 : w0);
-      if constexpr (RING > 2) {
-        if (b + 2 < stages) {
-          stage(j2, std::false_type{}, b + 2, x2, w2, RING > 3 ? x3 : x0, RING > 3 ? w3 : w0);
-          if constexpr (RING > 3) {
-            if (b + 3 < stages) stage(j3, std::false_type{}, b + 3, x3, w3, x0, w0);
+    if constexpr (AHEAD > 0) {   // every stage as if more followed
+      for (; b + TURN <= stages; b += TURN) {
+        stage(j0, more, b);
+        stage(j1, more, b + 1);
+        stage(j2, more, b + 2);
+        stage(j3, more, b + 3);
+        stage(j4, more, b + 4);
+        stage(j5, more, b + 5);
+      }
+      if (b < stages) stage(j0, more, b);
+      if (b + 1 < stages) stage(j1, more, b + 1);
+      if (b + 2 < stages) stage(j2, more, b + 2);
+      if (b + 3 < stages) stage(j3, more, b + 3);
+      if (b + 4 < stages) stage(j4, more, b + 4);
+    } else {
+      for (; b + XR < stages; b += XR) {
+        stage(j0, more, b);
+        stage(j1, more, b + 1);
+        if constexpr (XR > 2) stage(j2, more, b + 2);
+        if constexpr (XR > 3) stage(j3, more, b + 3);
+      }
+      // the last turn, of 1 to XR stages
+      stage(j0, no_more, b);
+      if (b + 1 < stages) {
+        stage(j1, no_more, b + 1);
+        if constexpr (XR > 2) {
+          if (b + 2 < stages) {
+            stage(j2, no_more, b + 2);
+            if constexpr (XR > 3) {
+              if (b + 3 < stages) stage(j3, no_more, b + 3);
+            }
           }
         }
       }
     }
   }
   wait_loads<0>();   // LDS takes no more loads: the results pass through it
-  t.template store<DT>(a, acc, scales, w0, w1);
+  t.template store<DT>(a, acc, scales, BM > BN ? x0 : w0, BM > BN ? x1 : w1);
 }
 
 // Operands at any byte: loads into registers, put into LDS once the stage
@@ -514,7 +543,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void int8_tile_kernel(Int8Args a, in
       t.multiply_stage(acc, x1, w1);
     }
   }
-  t.template store<DT>(a, acc, scales, w0, w1);
+  t.template store<DT>(a, acc, scales, BM > BN ? x0 : w0, BM > BN ? x1 : w1);
 }
 
 template <int BM, int BN>
@@ -523,11 +552,11 @@ void tiles_of(const Int8Args& a, int* m_tiles, int* tiles) {
   *tiles = *m_tiles * ((a.vocab + BN - 1) / BN);
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int TK, int RING, bool ONCE>
+template <int DT, int BM, int BN, int WM, int WN, int TK, int XR, int WR, bool ONCE>
 hipError_t launch_ring(const Int8Args& a, hipStream_t s) {
   int m_tiles, tiles;
   tiles_of<BM, BN>(a, &m_tiles, &tiles);
-  hipLaunchKernelGGL((int8_ring_kernel<DT, BM, BN, WM, WN, TK, RING, ONCE>),
+  hipLaunchKernelGGL((int8_ring_kernel<DT, BM, BN, WM, WN, TK, XR, WR, ONCE>),
                      dim3((tiles + 7) / 8 * 8), dim3(WM * WN * kWave), 0, s, a, m_tiles, tiles);
   return hipGetLastError();
 }
@@ -542,23 +571,28 @@ hipError_t launch_tile(const Int8Args& a, hipStream_t s) {
 }
 
 // Tile shapes for more than 64 rows: how many run at once (one or two to a
-// compute unit), how long a full round of them takes in us at width 4096, and
-// which share of that a round of few takes. Shapes that run in pairs keep that
-// share up to half the places. Measured in rounds of 0.1, 0.5, 1 and 2 (us):
-// 256x256 40 44 55 114, 192x256 38 35 42 97, 128x256 32 31 34 66, 160x128 26 26 38
-// 95, 128x128 30 31 41 85, 64x64 12 11 19 35.
+// compute unit), how long a full round of them takes in us at width 4096 with the
+// weight in the caches, and which share of that a round of few takes. Shapes that
+// run in pairs keep that share up to half the places. Measured (us a round, many
+// rounds and one of few tiles): 256x256 54 38, 192x256 42 33, 320x128 38 31,
+// 128x256 34 26, 128x128 39 20, one to a compute unit 21 17, 64x64 16 10.
 struct TileCost {
   int bm, bn, at_once;
   double us, least;
 };
-constexpr TileCost kTileCost[] = {{256, 256, 256, 57.0, 0.65}, {192, 256, 256, 49.0, 0.68},
-                                  {128, 256, 256, 34.0, 0.88}, {160, 128, 512, 48.0, 0.62},
-                                  {128, 128, 512, 42.0, 0.68}, {64, 64, 512, 17.5, 0.62}};
+constexpr TileCost kTileCost[] = {{256, 256, 256, 54.0, 0.70}, {192, 256, 256, 42.5, 0.79},
+                                  {320, 128, 256, 38.0, 0.82}, {128, 256, 256, 34.0, 0.77},
+                                  {128, 128, 512, 39.0, 0.52}, {128, 128, 256, 21.5, 0.80},
+                                  {64, 64, 512, 16.2, 0.64}};
+constexpr int kTileShapes = sizeof(kTileCost) / sizeof(kTileCost[0]);
+constexpr double kWeightBytesPerUs = 4.8e6;   // as the tiles read it from memory
 
 inline long long tiles_in(const TileCost& c, int rows, int vocab) {
   return (long long)((rows + c.bm - 1) / c.bm) * ((vocab + c.bn - 1) / c.bn);
 }
-inline double rounds_us(const TileCost& c, int rows, int vocab) {
+// The rounds' time and the weight's, which hide each other but for where they
+// are alike (their fourth powers added).
+inline double tiles_us(const TileCost& c, int rows, int vocab, int width) {
   const long long tiles = tiles_in(c, rows, vocab), rest = tiles % c.at_once;
   double part = 0.0;
   if (rest > 0) {
@@ -566,38 +600,40 @@ inline double rounds_us(const TileCost& c, int rows, int vocab) {
     if (c.at_once == 512) more = more > 0.5 ? 2.0 * more - 1.0 : 0.0;
     part = c.least + (1.0 - c.least) * more;
   }
-  return ((double)(tiles / c.at_once) + part) * c.us;
+  const double r = ((double)(tiles / c.at_once) + part) * c.us * width / 4096.0;
+  const double m = (double)vocab * width / kWeightBytesPerUs;
+  return sqrt(sqrt(r * r * r * r + m * m * m * m));
 }
-// The shape with the least rounds' time. Measured at width 4096 (us): 128 x 32000
-// 128x128 36, 128x256 39, 64x128 40; 128 x 128256 128x256 117, 128x128 131; 200 x 8960
-// 64x64 26, 128x128 31; 256 x 32000 128x256 40, 128x128 46, 160x128 48, 256x256 66;
-// 320 x 32000 160x128 53, 192x256 55, 256x256 60; 384 x 32000 192x256 57, 256x256 61;
-// 1024 x 151936 256x256 566, 128x256 622, 160x128 659, 128x128 698, 64x64 1213.
-constexpr int kTileShapes = sizeof(kTileCost) / sizeof(kTileCost[0]);
-inline int pick_tile(int rows, int vocab) {
+// The shape with the least time. Measured at width 4096 (us), the shapes in the
+// table's order: 256 x 32000 49 46 43 39 49 51 71, 320 x 32000 53 47 44 65 65 60 82,
+// 384 x 32000 54 47 78 67 67 68 93, 128 x 128256 127 116 163 113 115 119 156,
+// 200 x 8960 41 35 34 28 22 19 22, 90 x 8192 38 33 31 26 20 17 11, 1024 x 131072
+// 431 509 602 542 624 702 1036.
+inline int pick_tile(int rows, int vocab, int width) {
   int best = 0;
   for (int i = 1; i < kTileShapes; ++i)
-    if (rounds_us(kTileCost[i], rows, vocab) < rounds_us(kTileCost[best], rows, vocab)) best = i;
+    if (tiles_us(kTileCost[i], rows, vocab, width) < tiles_us(kTileCost[best], rows, vocab, width))
+      best = i;
   return best;
 }
 // The whole batch in one launch, or the channels that fill whole rounds of a
 // large shape first and the others in the shape that suits them, where that
-// saves more than a launch's 3 us (1000 x 50001: 225 us in one launch, 193 in two).
-// `first`: the channels of the first launch.
+// saves more than a launch's 3 us. `first`: the channels of the first launch.
 struct TilePlan {
   int shape, first;
 };
 inline TilePlan plan_tiles(int rows, int vocab, int width) {
-  TilePlan p{pick_tile(rows, vocab), vocab};
-  double least = rounds_us(kTileCost[p.shape], rows, vocab);
+  TilePlan p{pick_tile(rows, vocab, width), vocab};
+  double least = tiles_us(kTileCost[p.shape], rows, vocab, width);
   for (int i = 0; i < kTileShapes; ++i) {
     const TileCost& c = kTileCost[i];
     const long long full = tiles_in(c, rows, vocab) / c.at_once;
     const long long first = full * c.at_once / ((rows + c.bm - 1) / c.bm) * c.bn;
     if (first <= 0 || first >= vocab) continue;
     const int rest = vocab - (int)first;
-    const double us = full * c.us + rounds_us(kTileCost[pick_tile(rows, rest)], rows, rest) +
-                      3.0 * 4096.0 / width;
+    const double us =
+        tiles_us(c, rows, (int)first, width) +
+        tiles_us(kTileCost[pick_tile(rows, rest, width)], rows, rest, width) + 3.0;
     if (us < least) {
       p = TilePlan{i, (int)first};
       least = us;
@@ -607,35 +643,43 @@ inline TilePlan plan_tiles(int rows, int vocab, int width) {
 }
 
 // ONCE where the rows' lines are whole (a line that two loads share would be
-// read twice): 1 x 128256 x 4096 78 us against 84, with rows 4100 apart 92
-// against 84.
-template <int DT, bool LINES>
+// read twice) and the weight is too large to be in the caches from the call
+// before: 1 x 128256 x 4096 78 us against 93, with rows 4100 apart 92 against 84,
+// 60 x 8192 x 4096 18 against 15. Small tiles that share a weight leave it in the
+// caches for each other (1024 x 131072 x 4096 in 128 x 128 656 us past them, 624
+// in them; in 256 x 256 431 and 453).
+constexpr long long kInt8OnceBytes = 48ll << 20;
+
+template <int DT, bool ONCE>
 hipError_t launch_shape(const Int8Args& a, int shape, hipStream_t s) {
   switch (shape) {
-    case 0: return launch_ring<DT, 256, 256, 2, 4, 128, 2, false>(a, s);
-    case 1: return launch_ring<DT, 192, 256, 2, 4, 128, 2, false>(a, s);
-    case 2: return launch_ring<DT, 128, 256, 2, 4, 128, 3, LINES>(a, s);
-    case 3: return launch_ring<DT, 160, 128, 2, 2, 128, 2, false>(a, s);
-    case 4: return launch_ring<DT, 128, 128, 2, 2, 128, 2, LINES>(a, s);
-    default: return launch_ring<DT, 64, 64, 2, 2, 128, 4, LINES>(a, s);
+    case 0: return launch_ring<DT, 256, 256, 2, 4, 128, 2, 3, ONCE>(a, s);
+    case 1: return launch_ring<DT, 192, 256, 2, 4, 128, 2, 3, ONCE>(a, s);
+    case 2: return launch_ring<DT, 320, 128, 4, 2, 128, 2, 3, ONCE>(a, s);
+    case 3: return launch_ring<DT, 128, 256, 2, 4, 128, 3, 3, ONCE>(a, s);
+    case 4:
+      if (ONCE && a.rows <= 128) return launch_ring<DT, 128, 128, 2, 2, 128, 2, 3, ONCE>(a, s);
+      return launch_ring<DT, 128, 128, 2, 2, 128, 2, 3, false>(a, s);
+    case 5: return launch_ring<DT, 128, 128, 2, 4, 128, 4, 4, false>(a, s);
+    default: return launch_ring<DT, 64, 64, 2, 2, 128, 4, 4, false>(a, s);
   }
 }
-template <int DT, bool LINES>
+template <int DT, bool ONCE>
 hipError_t launch_direct(const Int8Args& a, hipStream_t s) {
-  if (a.rows <= 16) return launch_ring<DT, 16, 64, 1, 4, 256, 4, LINES>(a, s);
-  if (a.rows <= 32) return launch_ring<DT, 32, 64, 1, 4, 128, 4, LINES>(a, s);
-  if (a.rows <= 64) return launch_ring<DT, 64, 128, 1, 4, 128, 3, LINES>(a, s);
+  if (a.rows <= 16) return launch_ring<DT, 16, 64, 1, 4, 256, 4, 4, ONCE>(a, s);
+  if (a.rows <= 32) return launch_ring<DT, 32, 64, 1, 4, 128, 4, 4, ONCE>(a, s);
+  if (a.rows <= 64) return launch_ring<DT, 64, 128, 1, 4, 128, 3, 3, ONCE>(a, s);
   const TilePlan p = plan_tiles(a.rows, a.vocab, a.width);
   Int8Args part = a;
   part.vocab = p.first;
-  const hipError_t e = launch_shape<DT, LINES>(part, p.shape, s);
+  const hipError_t e = launch_shape<DT, ONCE>(part, p.shape, s);
   if (e != hipSuccess || p.first == a.vocab) return e;
   part.vocab = a.vocab - p.first;
   part.w += (long long)p.first * a.w_stride;
   part.w_scale += p.first;
   if (a.bias) part.bias += p.first;
   part.out += (long long)p.first * Fmt<DT>::ESZ;
-  return launch_shape<DT, LINES>(part, pick_tile(a.rows, part.vocab), s);
+  return launch_shape<DT, ONCE>(part, pick_tile(a.rows, part.vocab, a.width), s);
 }
 
 template <int DT>
@@ -644,7 +688,8 @@ hipError_t launch_int8_dt(const Int8Args& a, hipStream_t s) {
     return a.x_stride % n == 0 && a.w_stride % n == 0 && (uintptr_t)a.x % n == 0 &&
            (uintptr_t)a.w % n == 0;
   };
-  if (multiple(128)) return launch_direct<DT, true>(a, s);
+  if (multiple(128) && (long long)a.vocab * a.width >= kInt8OnceBytes)
+    return launch_direct<DT, true>(a, s);
   if (multiple(4)) return launch_direct<DT, false>(a, s);
   // measured at width 4095 (us): 1 x 128256 93 (64 rows a tile 109), 30 x 128256 115
   // (123, 128x128 127), 64 x 128256 136 (128x128 141), 256 x 50001 118 (256x128 127,
