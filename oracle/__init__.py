@@ -15,6 +15,9 @@ philox   Philox4x32-10 counter-based generator (Salmon, Moraes, Dror, Shaw,
          "Parallel Random Numbers: As Easy as 1, 2, 3", SC'11), written from its
          published definition, and the counter layout the sampler uses.
 tree     The tree (multi-candidate) verify step.
+int8     Absmax codes of rows and the logits of an 8-bit projection, with the
+         bound that the kernels' roundings keep.
+vprobs   The verify step from probabilities and given random numbers.
 beam     One beam-search step (eq. 39.1, Listing 39.1) and the search built on it.
 sampler  The filter chain (temperature, softmax, top-k, top-p, min-p,
          renormalisation by eq. 39.2), the draw, greedy decoding, and the

@@ -1,9 +1,13 @@
 // The 8-bit output projection (int8_logits): out[r][n] = sum_k x[r][k] w[n][k]
 // in 32-bit integers, times the row's and the channel's scale.
 //
-// Few rows are bound by the weight's bytes, many by the matrix pipes. The
+// Few rows are bound by the weight's bytes: 1 x 128256 x 4096 78 us, 6.7 TB/s of
+// the 6.9 that reads reach here; 64 x 128256 104 us, 5.2 TB/s, its logits' 16 MB
+// among them. Many are bound by the matrix pipes and by what feeds them: 1024 x
+// 151936 x 4096 517 us, 2.46 P op/s, the pipes busy two thirds of it (products
+// of random codes alone reach 3.8, where the card's power holds its clock). The
 // weight is cut into runs of channels, each read from memory once: every hidden
-// row, or up to 256 of them, meets a run while it is in LDS.
+// row, or up to 320 of them, meets a run while it is in LDS.
 #pragma once
 
 #include <cmath>
