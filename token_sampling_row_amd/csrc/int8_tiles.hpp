@@ -701,9 +701,10 @@ hipError_t launch_int8_dt(const Int8Args& a, hipStream_t s) {
   if (a.rows <= 16) return launch_tile<DT, 16, 64, 1, 4, 256>(a, s);
   if (a.rows <= 32) return launch_tile<DT, 32, 64, 1, 4, 256>(a, s);
   if (a.rows <= 64) return launch_tile<DT, 64, 64, 1, 4, 256>(a, s);
-  // under two tiles of 128 x 128 to a compute unit: 87 x 19685 x 3234 34 us in 64 x 64,
-  // 41 in 128 x 128; 128 x 128256 157 in 128 x 128, 193 in 128 x 64
-  if ((long long)((a.rows + 127) / 128) * ((a.vocab + 127) / 128) <= 256)
+  // up to three tiles of 64 x 64 to a compute unit (us, 64 x 64 and 128 x 128):
+  // 90 x 24000 x 4095 45 48, 250 x 8000 31 41, 128 x 12000 36 47; past them 100 x
+  // 28000 63 51, 90 x 32000 61 51, 128 x 128256 238 156
+  if ((long long)((a.rows + 63) / 64) * ((a.vocab + 63) / 64) <= 768)
     return launch_tile<DT, 64, 64, 1, 4, 128>(a, s);
   return launch_tile<DT, 128, 128, 1, 4, 128>(a, s);
 }
