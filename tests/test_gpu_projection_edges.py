@@ -267,7 +267,8 @@ def large_batch(s, dtype, rows, vocab, width, stride):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,vocab", [(512, 32000), (384, 32003), (256, 32000), (320, 32001),
-                                        (128, 32000), (200, 8960), (500, 31999), (1024, 33000)])
+                                        (128, 32000), (200, 8960), (500, 31999), (1024, 33000),
+                                        (310, 32003), (190, 40003)])
 def test_every_tile_shape(s, dtype, rows, vocab):
     """Batches where each tile shape is the one taken, with rows in whole lines, at
     words and at bytes, and with a partial stage."""

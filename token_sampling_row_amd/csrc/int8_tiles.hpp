@@ -72,6 +72,7 @@ struct Tile {
   static constexpr int CH = TK / 16, PR = 64 / CH;   // chunks of a row, rows of a 1 KiB piece
   static constexpr int XI = BM / PR / WAVES, WI = BN / PR / WAVES;   // pieces per wavefront
   static constexpr int H = TK / 64;                                  // products along a stage
+  static_assert(TK == 128 || TK == 256, "turns");
   static_assert(XI * PR * WAVES == BM && WI * PR * WAVES == BN, "pieces");
   static_assert(MT * 16 * WM == BM && NT * 16 * WN == BN, "blocks");
 
@@ -90,9 +91,7 @@ struct Tile {
     wn = wave / WM;
     return tile < tiles;
   }
-  static __device__ __forceinline__ int turn(int r) {
-    return TK == 64 ? (r >> 1) & 3 : TK == 128 ? r & 7 : r & 15;
-  }
+  static __device__ __forceinline__ int turn(int r) { return r & (CH - 1); }
   // piece q of this wavefront: the row its lane brings, and which bytes of it
   __device__ __forceinline__ int row_of(int q, int pieces) const {
     return (wave * pieces + q) * PR + lane / CH;
@@ -265,8 +264,9 @@ struct Tile {
         unsigned char* o = a.out + (long long)r * a.out_stride_bytes + (long long)e0 * ESZ;
         if (e0 + EPC <= a.vocab) {
           // whole lines of many rows' logits leave the caches before they are read:
-          // 256 x 128256 160 us kept in them, 150 not (24 rows 85 and 87; lines
-          // that two tiles share, 256 x 50001: 122 and 180)
+          // 256 x 128256 150 us kept in them, 139 not, 1024 x 151936 519 and 511 (24
+          // rows 84 and 90; lines that two tiles share, 256 x 50001 x 4095: 122 and
+          // 180)
           if (BM >= 128 && whole_lines)
             store16_once(o, v);
           else
