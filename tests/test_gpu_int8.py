@@ -323,7 +323,8 @@ def test_refusals(s):
             lambda: s.int8_logits(c, cs, w, ws, out=torch.zeros(4, 31, device=d)),
             lambda: s.int8_logits(c, cs, w, ws, out=torch.zeros(1, 32, device=d).expand(4, 32)),
             lambda: s.sample_hidden(h[:, :63], w, ws, {}, 0),
-            lambda: s.sample_hidden(h, w, ws, {}, 0, out=torch.zeros(3, dtype=torch.int32, device=d)),
+            lambda: s.sample_hidden(h, w, ws, {}, 0,
+                                    out=torch.zeros(3, dtype=torch.int32, device=d)),
             lambda: s.sample_hidden(h, w, ws, {}, 0, logits=torch.zeros(4, 40, device=d)[:, :32])):
         with pytest.raises(ValueError):
             call()

@@ -44,7 +44,8 @@ def test_operands_of_unlike_alignment(s, rows, xs, ws):
 
 
 @pytest.mark.parametrize("rows", [1, 17, 33, 65, 300])
-@pytest.mark.parametrize("width", [127, 128, 129, 255, 256, 257, 383, 384, 512, 640, 768, 1024, 1279])
+@pytest.mark.parametrize("width", [127, 128, 129, 255, 256, 257, 383, 384, 512, 640, 768, 1024,
+                                   1279])
 def test_widths_about_the_stages(s, rows, width):
     """Every number of whole stages below a turn of the ring and above, with and
     without a partial one; rows a multiple of 128 bytes apart and not."""
@@ -268,7 +269,7 @@ def large_batch(s, dtype, rows, vocab, width, stride):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,vocab", [(512, 32000), (384, 32003), (256, 32000), (320, 32001),
                                         (128, 32000), (200, 8960), (500, 31999), (1024, 33000),
-                                        (310, 32003), (190, 40003)])
+                                        (310, 32003), (190, 40003), (60, 33001)])
 def test_every_tile_shape(s, dtype, rows, vocab):
     """Batches where each tile shape is the one taken, with rows in whole lines, at
     words and at bytes, and with a partial stage."""
@@ -280,7 +281,7 @@ def test_every_tile_shape(s, dtype, rows, vocab):
 @pytest.mark.parametrize("rows,vocab,width,stride", [
     (1000, 131072, 500, 512), (192, 131071, 500, 512), (320, 131072, 512, 512),
     (128, 131073, 500, 512), (100, 40000, 1400, 1408), (700, 50001, 1100, 1152),
-    (90, 14000, 4000, 4096), (64, 40000, 1408, 1408), (30, 40001, 1400, 1408),
+    (90, 14000, 4000, 4096), (64, 40000, 1408, 1408), (63, 32768, 1600, 1664), (30, 40001, 1400, 1408),
     (9, 13000, 4100, 4224), (3, 13000, 4096, 4096)])
 def test_large_weights(s, dtype, rows, vocab, width, stride):
     """Weights that outgrow the caches, in rows of whole lines; batches in one
@@ -288,13 +289,14 @@ def test_large_weights(s, dtype, rows, vocab, width, stride):
     large_batch(s, dtype, rows, vocab, width, stride)
 
 
-@pytest.mark.parametrize("rows", [512, 384, 320, 256])
-def test_stages_of_large_tiles(s, rows):
+@pytest.mark.parametrize("rows,vocab", [(512, 32000), (384, 32000), (320, 32000), (256, 32000),
+                                        (64, 33000)])
+def test_stages_of_large_tiles(s, rows, vocab):
     """One whole stage to more than two turns of the rings, without and with a
     partial one behind."""
     for stages in range(1, 15):
-        large_batch(s, "bf16", rows, 32000, 128 * stages, 128 * stages)
-        large_batch(s, "bf16", rows, 32000, 128 * stages + 60, 128 * stages + 64)
+        large_batch(s, "bf16", rows, vocab, 128 * stages, 128 * stages)
+        large_batch(s, "bf16", rows, vocab, 128 * stages + 60, 128 * stages + 64)
 
 
 @pytest.mark.parametrize("rows", [1, 5, 70])

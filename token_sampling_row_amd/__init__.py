@@ -102,8 +102,8 @@ def load_library():
     lib.beam_step.argtypes = [vp, vp, i32, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp]
     lib.quantize_rows.argtypes = [vp, vp, i32, i32, i32, i64, vp, i64, vp, vp]
     lib.int8_logits.argtypes = [vp, vp, i64, vp, i32, ctypes.POINTER(_Head), vp, i32, i64, vp]
-    lib.sample_hidden.argtypes = [vp, vp, i32, i32, i64, ctypes.POINTER(_Head), vp, i64, vp, vp, i32,
-                                  ctypes.POINTER(_Params), u64, vp, ctypes.POINTER(_Diag), vp]
+    lib.sample_hidden.argtypes = [vp, vp, i32, i32, i64, ctypes.POINTER(_Head), vp, i64, vp, vp,
+                                  i32, ctypes.POINTER(_Params), u64, vp, ctypes.POINTER(_Diag), vp]
     lib.verify_probs.argtypes = [vp, vp, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, i32, i32,
                                  i32, vp, vp, vp, vp]
     lib.sampler_philox.argtypes = [vp, vp, i32, vp, vp]

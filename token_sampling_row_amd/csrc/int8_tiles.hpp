@@ -672,7 +672,13 @@ template <int DT, bool ONCE>
 hipError_t launch_direct(const Int8Args& a, hipStream_t s) {
   if (a.rows <= 16) return launch_ring<DT, 16, 64, 1, 4, 256, 4, 4, ONCE>(a, s);
   if (a.rows <= 32) return launch_ring<DT, 32, 64, 1, 4, 128, 4, 4, ONCE>(a, s);
-  if (a.rows <= 64) return launch_ring<DT, 64, 128, 1, 4, 128, 3, 3, ONCE>(a, s);
+  if (a.rows <= 64) {
+    // all tiles at once, two to a compute unit, where those of half the channels
+    // are no more (us, 64 x 64 and 64 x 128): 50 x 8192 x 4096 10 15, 50 x 16000 16 20,
+    // 50 x 32000 29 30, but 50 x 50000 46 43
+    if (a.vocab <= 512 * 64) return launch_ring<DT, 64, 64, 2, 2, 128, 4, 4, ONCE>(a, s);
+    return launch_ring<DT, 64, 128, 1, 4, 128, 3, 3, ONCE>(a, s);
+  }
   const TilePlan p = plan_tiles(a.rows, a.vocab, a.width);
   Int8Args part = a;
   part.vocab = p.first;

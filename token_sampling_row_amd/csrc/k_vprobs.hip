@@ -154,7 +154,7 @@ struct VpGroup {
     } else if (whole > 0) {
 #pragma unroll
       for (int i = 0; i < kVpGroup; ++i) {
-        const long long at = (long long)min(s0 + i, whole - 1) * (SPAN * ESZ);   // the same in all lanes
+        const long long at = (long long)min(s0 + i, whole - 1) * (SPAN * ESZ);
         p[i] = load16(r.p + at + lane * 16);
         if constexpr (SUB == 1) q[i] = load16(r.q + at + lane * 16);
       }
@@ -355,7 +355,8 @@ __device__ __forceinline__ void vp_write(const VprobsArgs& a, int b, int status,
 // makes the tests and finds the group for itself, so that only the sums wait for
 // each other; 16 wavefronts keep a 128 KB row on its way at once.
 template <int DT>
-__global__ __launch_bounds__(kVpWaves<DT> * kWave) void vprobs_kernel(VprobsArgs a, int groups, int rep) {
+__global__ __launch_bounds__(kVpWaves<DT>* kWave) void vprobs_kernel(VprobsArgs a, int groups,
+                                                                     int rep) {
   __shared__ double sums[kVpGroups];
   const int b = blockIdx.x, lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
