@@ -212,6 +212,14 @@ def _new(stream, device, dtype, *shape):
         return _torch.empty(shape, dtype=dtype, device=device)
 
 
+def _new_like(stream, t, *shape):
+    """The same, of t's type and device (0.4 us less of host time)."""
+    if stream is None:
+        return t.new_empty(*shape)
+    with _torch.cuda.stream(stream):
+        return t.new_empty(*shape)
+
+
 def pack_row_params(params_list):
     """Per-row parameters as the bytes of a tsr_params array (host uint8
     numpy array; copy it to the device for sample_rows_ex's row_params)."""
@@ -473,11 +481,15 @@ class Sampler:
         codes are rows a multiple of 128 bytes apart: not contiguous where W is
         no such multiple."""
         torch = _t()
-        dt = 1 if x.dtype is torch.bfloat16 else _dtype_code(x)
-        if x.dim() != 2:
-            raise ValueError("x: not a matrix")
+        dt = BF16 if x.dtype is torch.bfloat16 else _dtype_code(x)
+        if x.dim() != 2 or x.get_device() != self.device:
+            raise ValueError("x: not a matrix on the handle's GPU")
         rows, width = x.shape
-        xs = self._rows(x, rows, width, "x")
+        xs, one = x.stride()
+        if width < 1 or (width > 1 and one != 1) or (rows > 1 and xs < width):
+            raise ValueError("x: rows empty, not contiguous, or overlapping")
+        if xs < width:   # one row
+            xs = width
         if out is None:
             out = self._new_codes(stream, x.device, rows, width)
             stride = width + -width % 128
@@ -486,7 +498,8 @@ class Sampler:
         else:
             stride = self._rows(out, rows, width, "out")
         if scale is None:
-            scale = _new(stream, x.device, torch.float32, rows)
+            scale = _new_like(stream, x, rows) if dt == F32 else \
+                _new(stream, x.device, torch.float32, rows)
         else:
             self._vector(scale, torch.float32, "scale", rows)
         if rows:
@@ -513,7 +526,8 @@ class Sampler:
         if w != width:
             raise ValueError(f"codes: not [{rows}, {width}]")
         if out is None:
-            out = _new(stream, codes.device, dtype or torch.bfloat16, rows, vocab)
+            out = _new_like(stream, scale, rows, vocab) if dtype is torch.float32 else \
+                _new(stream, codes.device, dtype or torch.bfloat16, rows, vocab)
             out_stride = vocab
         else:
             out_stride = self._rows(out, rows, vocab, "out")
@@ -599,11 +613,11 @@ class Sampler:
         n_ptr = None if draft_lens is None else self._vector(draft_lens, i32, "draft_lens", rows)
         s_ptr = None if out_status is None else self._vector(out_status, i32, "out_status", rows)
         if out_tokens is None:
-            out_tokens = _new(stream, target.device, i32, rows, k1)
+            out_tokens = _new_like(stream, draft_tokens, rows, k1)
         else:
             self._vector(out_tokens, i32, "out_tokens", rows, k1)
         if out_accepted is None:
-            out_accepted = _new(stream, target.device, i32, rows)
+            out_accepted = _new_like(stream, draft_tokens, rows)
         else:
             self._vector(out_accepted, i32, "out_accepted", rows)
         if rows:
