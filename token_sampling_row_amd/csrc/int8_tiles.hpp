@@ -4,7 +4,7 @@
 // Few rows are bound by the weight's bytes: 1 x 128256 x 4096 78 us, 6.7 TB/s of
 // the 6.9 that reads reach here; 64 x 128256 104 us, 5.2 TB/s, its logits' 16 MB
 // among them. Many are bound by the matrix pipes and by what feeds them: 1024 x
-// 151936 x 4096 517 us, 2.46 P op/s, the pipes busy two thirds of it (products
+// 151936 x 4096 502 us, 2.54 P op/s, the pipes busy two thirds of it (products
 // of random codes alone reach 3.8, where the card's power holds its clock). The
 // weight is cut into runs of channels, each read from memory once: every hidden
 // row, or up to 320 of them, meets a run while it is in LDS.
