@@ -357,7 +357,7 @@ typedef struct {
  *  out_logits [rows][vocab] of type dtype, out_stride elements apart; what
  *      lies between vocab and out_stride is left as it is.
  * width <= 131071 (the sum fits 32 bits), vocab <= 2^29 and both operands'
- * strides < 2^23 (TSR_EUNSUPPORTED beyond). Rows that start at 4-byte words are
+ * strides < 2^22 (TSR_EUNSUPPORTED beyond). Rows that start at 4-byte words are
  * read fastest, those at multiples of 128 bytes most of all; other rows are
  * read in whole 4-byte words, so up to three bytes on either side of a row, in
  * words that also hold bytes of it. Uses no workspace. */

@@ -195,7 +195,7 @@ def test_refusals_through_the_c_interface(s):
                 dict(width=0), dict(o=None), dict(dt=2), dict(ost=3), dict(o=vp(out, 2)),
                 dict(head=False)):
         assert logits(**bad) == 1, bad
-    for bad in (dict(width=131072, cst=131072, wst=131072), dict(cst=1 << 23), dict(wst=1 << 23)):
+    for bad in (dict(width=131072, cst=131072, wst=131072), dict(cst=1 << 22), dict(wst=1 << 22)):
         assert logits(**bad) == 4, bad
 
     # more channels than a launch takes, on a handle that allows them
@@ -287,6 +287,20 @@ def test_large_weights(s, dtype, rows, vocab, width, stride):
     """Weights that outgrow the caches, in rows of whole lines; batches in one
     launch and in two."""
     large_batch(s, dtype, rows, vocab, width, stride)
+
+
+@pytest.mark.parametrize("rows", [320, 200])
+@pytest.mark.parametrize("width", [500, 501])
+def test_the_widest_rows(s, rows, width):
+    """Hidden rows nearly 2^22 bytes apart, the last of them past 2^30 bytes."""
+    stride = (1 << 22) - 128 if width % 4 == 0 else (1 << 22) - 1
+    g = torch.Generator(device()).manual_seed(width)
+    c = torch.zeros(rows * stride, dtype=torch.int8, device=device()).view(rows, stride)[:, :width]
+    c.copy_(torch.randint(-128, 128, (rows, width), dtype=torch.int8, device=device(), generator=g))
+    w = torch.randint(-128, 128, (32000, width), dtype=torch.int8, device=device(), generator=g)
+    one = torch.ones(rows, device=device()), torch.ones(32000, device=device())
+    got = s.int8_logits(c, one[0], w, one[1], dtype=torch.float32)
+    assert torch.equal(got.double(), c.double() @ w.double().t())   # sums below 2^24
 
 
 @pytest.mark.parametrize("rows,vocab", [(512, 32000), (384, 32000), (320, 32000), (256, 32000),

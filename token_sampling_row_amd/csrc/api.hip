@@ -111,7 +111,7 @@ constexpr int kMaxQuantWidth = 1 << 30;
 constexpr int kMaxQuantRows = (1 << 24) - 1;   // 256 threads a row: fewer than 2^32 in a launch
 // sums of products of 8-bit integers fit 32 bits: 2^17 - 1 times (-128)^2
 constexpr int kMaxInt8Width = (1 << 17) - 1;
-constexpr int64_t kMaxInt8Stride = 1 << 23;   // a tile's 256 rows within 2^31 bytes
+constexpr int64_t kMaxInt8Stride = 1 << 22;   // a tile's 320 rows within 2^31 bytes
 constexpr int kMaxInt8Vocab = 1 << 29;        // 256 threads to 64 channels: fewer than 2^32
 constexpr int kMaxWideVocab = 1 << 30;          // ids past the last one stay whole numbers
 constexpr int kMaxVprobsRows = (1 << 22) - 1;   // 1024 threads a sequence: fewer than 2^32
