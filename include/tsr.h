@@ -357,10 +357,11 @@ typedef struct {
  *  out_logits [rows][vocab] of type dtype, out_stride elements apart; what
  *      lies between vocab and out_stride is left as it is.
  * width <= 131071 (the sum fits 32 bits), vocab <= 2^29 and both operands'
- * strides < 2^22 (TSR_EUNSUPPORTED beyond). Rows that start at 4-byte words are
- * read fastest, those at multiples of 128 bytes most of all; other rows are
- * read in whole 4-byte words, so up to three bytes on either side of a row, in
- * words that also hold bytes of it. Uses no workspace. */
+ * strides < 2^22 (TSR_EUNSUPPORTED beyond; the stride of a single row is not
+ * used). Rows that start at 4-byte words are read fastest, those at multiples
+ * of 128 bytes most of all; other rows are read in whole 4-byte words, so up to
+ * three bytes on either side of a row, in words that also hold bytes of it.
+ * Uses no workspace. */
 int int8_logits(tsr_handle h, const int8_t* codes, int64_t codes_stride, const float* code_scale,
                 int rows, const tsr_head* head, void* out_logits, int dtype, int64_t out_stride,
                 void* hip_stream);

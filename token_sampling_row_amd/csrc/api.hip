@@ -140,8 +140,10 @@ int check_int8(tsr_handle h, const int8_t* codes, int64_t codes_stride, const fl
   if (!word_aligned(code_scale) || !word_aligned(head->scale) || !word_aligned(head->bias) ||
       !elem_aligned(out_logits, dtype))
     return TSR_EINVAL;
-  if (head->width > kMaxInt8Width || head->vocab > kMaxInt8Vocab ||
-      codes_stride >= kMaxInt8Stride || head->weight_stride >= kMaxInt8Stride)
+  if (head->width > kMaxInt8Width || head->vocab > kMaxInt8Vocab) return TSR_EUNSUPPORTED;
+  // a single row has no next one
+  if ((rows > 1 && codes_stride >= kMaxInt8Stride) ||
+      (head->vocab > 1 && head->weight_stride >= kMaxInt8Stride))
     return TSR_EUNSUPPORTED;
   return TSR_OK;
 }
@@ -543,10 +545,10 @@ int int8_logits(tsr_handle h, const int8_t* codes, int64_t codes_stride, const f
   if (rc != TSR_OK || rows == 0) return rc;
   tsr::Int8Args a{};
   a.x = codes;
-  a.x_stride = (long long)codes_stride;
+  a.x_stride = rows > 1 ? (long long)codes_stride : 0;   // no next row: any alignment and distance
   a.x_scale = code_scale;
   a.w = head->weight;
-  a.w_stride = (long long)head->weight_stride;
+  a.w_stride = head->vocab > 1 ? (long long)head->weight_stride : 0;
   a.w_scale = head->scale;
   a.bias = head->bias;
   a.out = static_cast<unsigned char*>(out_logits);
