@@ -1,5 +1,6 @@
 """int8_logits on views of a single row, by whose stride nothing is read. Scales of
 one and float32 logits: sums below 2^24 are held exactly."""
+import pytest
 
 from tests.gpu_common import device, gpu_available, torch
 
