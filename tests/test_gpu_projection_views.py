@@ -1,5 +1,6 @@
-"""int8_logits on views of a single row, by whose stride nothing is read. Scales of
-one and float32 logits: sums below 2^24 are held exactly."""
+"""int8_logits on views: a single row, by whose stride nothing is read, and hidden
+rows that start at words under large weights in whole lines. Scales of one and
+float32 logits: sums below 2^24 are held exactly."""
 import pytest
 
 from tests.gpu_common import device, gpu_available, torch
@@ -65,3 +66,11 @@ def test_far_rows_are_refused_where_there_are_several(s, rows):
 @pytest.mark.parametrize("off", [0, 4, 64])
 def test_one_row_of_any_width_at_a_word(s, width, off):
     check(s, matrix(1, width, width + off, off, width), matrix(700, width, 4224, 128, 8))
+
+
+@pytest.mark.parametrize("rows", [1, 9, 30, 60, 100, 128, 200, 320, 384, 700])
+@pytest.mark.parametrize("stride,off", [(1404, 0), (1408, 4), (1536, 64)])
+def test_large_weights_under_rows_at_words(s, rows, stride, off):
+    """Weights that outgrow the caches in whole lines, hidden rows that start at
+    words or halves of lines, with a partial stage behind."""
+    check(s, matrix(rows, 1399, stride, off, rows), matrix(40001, 1399, 1408, 0, 9))

@@ -646,10 +646,11 @@ inline TilePlan plan_tiles(int rows, int vocab, int width) {
   return p;
 }
 
-// ONCE where the rows' lines are whole (a line that two loads share would be
-// read twice) and the weight is too large to be in the caches from the call
-// before: 1 x 128256 x 4096 78 us against 93, with rows 4100 apart 92 against 84,
-// 60 x 8192 x 4096 18 against 15. Small tiles that share a weight leave it in the
+// ONCE where the weight's lines are whole (a line that two loads share would be
+// read twice) and it is too large to be in the caches from the call before:
+// 1 x 128256 x 4096 78 us against 93, with its rows 4100 apart 92 against 84,
+// 60 x 8192 x 4096 18 against 15; hidden rows 4100 apart, at words only, 5 x 128256
+// 79 against 92, 256 x 128256 132 against 140. Small tiles that share a weight leave it in the
 // caches for each other (1024 x 131072 x 4096 in 128 x 128 656 us past them, 624
 // in them; in 256 x 256 431 and 453).
 constexpr long long kInt8OnceBytes = 48ll << 20;
@@ -694,13 +695,12 @@ hipError_t launch_direct(const Int8Args& a, hipStream_t s) {
 
 template <int DT>
 hipError_t launch_int8_dt(const Int8Args& a, hipStream_t s) {
-  auto multiple = [&](int n) {
-    return a.x_stride % n == 0 && a.w_stride % n == 0 && (uintptr_t)a.x % n == 0 &&
-           (uintptr_t)a.w % n == 0;
-  };
-  if (multiple(128) && (long long)a.vocab * a.width >= kInt8OnceBytes)
-    return launch_direct<DT, true>(a, s);
-  if (multiple(4)) return launch_direct<DT, false>(a, s);
+  const bool x_words = a.x_stride % 4 == 0 && (uintptr_t)a.x % 4 == 0;
+  auto w_multiple = [&](int n) { return a.w_stride % n == 0 && (uintptr_t)a.w % n == 0; };
+  if (x_words && w_multiple(4)) {
+    const bool once = w_multiple(128) && (long long)a.vocab * a.width >= kInt8OnceBytes;
+    return once ? launch_direct<DT, true>(a, s) : launch_direct<DT, false>(a, s);
+  }
   // measured at width 4095 (us): 1 x 128256 93 (64 rows a tile 109), 30 x 128256 115
   // (123, 128x128 127), 64 x 128256 136 (128x128 141), 256 x 50001 118 (256x128 127,
   // 128x256 134, 256x256 217)
