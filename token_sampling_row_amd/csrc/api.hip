@@ -23,7 +23,7 @@ struct tsr_ctx {
   uint64_t seed;
   tsr::VerifyWs ws;
   tsr::BeamWs bws;
-  tsr::VprobsWs pws;
+  void* pws;   // verify_probs' workspace
   void* ws_block;
 #if TSR_TRACE
   unsigned long long* trace;   // phase stamps (tracing build)
@@ -249,10 +249,8 @@ int sampler_init(tsr_handle* out, int device, int max_rows, int max_vocab, int m
     const size_t rbytes = (size_t)max_rows * 2 * (size_t)(max_k + 1) * sizeof(tsr::RowRec) +
                           (size_t)max_rows * 2 * tsr::kMaxSlices * sizeof(unsigned long long);
     const size_t bbytes = bslots * (sizeof(double) + sizeof(int32_t));
-    const size_t prows = (size_t)(max_rows < tsr::kVpWsRows ? max_rows : tsr::kVpWsRows);
-    const size_t pbytes = prows * (tsr::kVpGroups * sizeof(double) + sizeof(int4));
     const size_t pat = (((vbytes + 7) & ~(size_t)7) + rbytes + bbytes + 15) & ~(size_t)15;
-    const size_t bytes = pat + pbytes;
+    const size_t bytes = pat + tsr::vprobs_ws_bytes(max_rows, max_vocab);
     if (hipMalloc(&h->ws_block, bytes) != hipSuccess) return TSR_ENOMEM;
     if (hipMemset(h->ws_block, 0, bytes) != hipSuccess) return TSR_EDEVICE;
     if (hipDeviceSynchronize() != hipSuccess) return TSR_EDEVICE;
@@ -271,10 +269,7 @@ int sampler_init(tsr_handle* out, int device, int max_rows, int max_vocab, int m
     char* bb = (char*)h->ws_block + ((vbytes + 7) & ~(size_t)7) + rbytes;
     h->bws.score = (double*)bb;
     h->bws.tok = (int32_t*)(bb + bslots * sizeof(double));
-    // verify_probs: per sequence its group sums and what its tests decided
-    h->pws.sums = (double*)((char*)h->ws_block + pat);
-    h->pws.cut = (int4*)(h->pws.sums + prows * tsr::kVpGroups);
-    h->pws.rows = (int)prows;
+    h->pws = (char*)h->ws_block + pat;
 #if TSR_TRACE
     if (hipMalloc(&h->trace, TSR_TRACE_WORDS * sizeof(uint64_t)) != hipSuccess) return TSR_ENOMEM;
     if (hipMemset(h->trace, 0, TSR_TRACE_WORDS * sizeof(uint64_t)) != hipSuccess) return TSR_EDEVICE;

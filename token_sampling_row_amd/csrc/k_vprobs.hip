@@ -25,14 +25,16 @@ constexpr int kVpSliceBlock = kVpSliceWaves * kWave;
 // the model and this call, 12 us against 10.
 constexpr long long kVpOnceBytes = 48ll << 20;
 constexpr int kVpGroup = 4;   // spans of a group; a wavefront has two groups' loads on their way
+constexpr int kVpAlone = 32;  // groups that one workgroup sums as fast as several
+template <int DT> constexpr int kVpUnit = kWave * Fmt<DT>::EPC * kVpGroup;   // ids of a group
 
 // How many workgroups share a row's sums (1: the one-launch kernel, as fast up
 // to 32 groups: 64 x 32000 fp32 9.8 us). A wavefront takes two groups at a time,
 // or one where that leaves places empty (33 x 151935 bf16 11.4 us against 11.9,
 // but 64 x 128256 bf16 15.7 against 14.5); 256 x 128256 fp32 with eight
 // workgroups to a row 37 us, with four 39.
-int vp_slices(int rows, int groups, int ws_rows) {
-  if (rows > ws_rows || groups <= 32) return 1;
+int vp_slices(int rows, int groups) {
+  if (rows > kVpWsRows || groups <= kVpAlone) return 1;
   const int one = (groups + kVpSliceWaves - 1) / kVpSliceWaves;
   const int most = rows * one <= 768 ? one : (one + 1) / 2;
   const int want = (2048 + rows - 1) / rows;
@@ -398,7 +400,7 @@ __global__ __launch_bounds__(kVpSliceBlock) void vprobs_slices_kernel(VprobsArgs
   if (c.status != 0) return;
   const VpRow r = vp_row<DT>(a, b, c.kept, c.token, rep, groups);
   vp_sums_of<DT>(r, !c.refused ? 0 : a.draft ? 1 : 2, slice * kVpSliceWaves + wave,
-                 slices * kVpSliceWaves, groups, lane, ws.sums + (long long)b * kVpGroups);
+                 slices * kVpSliceWaves, groups, lane, ws.sums + (long long)b * groups);
 }
 
 template <int DT>
@@ -412,7 +414,7 @@ __global__ __launch_bounds__(kVpSliceBlock) void vprobs_draw_kernel(VprobsArgs a
   const int x = lane < a.K ? a.tokens[(long long)b * a.K + lane] : 0;
   const float v = a.draw_u[b];
   for (int g = threadIdx.x; g < groups; g += kVpSliceBlock)
-    sums[g] = ws.sums[(long long)b * kVpGroups + g];
+    sums[g] = ws.sums[(long long)b * groups + g];
   __syncthreads();
   if (status == 0) {
     const VpRow r = vp_row<DT>(a, b, cut.y, cut.w, rep, groups);
@@ -433,13 +435,14 @@ __global__ __launch_bounds__(kVpSliceBlock) void vprobs_draw_kernel(VprobsArgs a
 }
 
 template <int DT>
-hipError_t launch_vprobs_dt(const VprobsArgs& a, const VprobsWs& ws, hipStream_t s) {
-  constexpr int UNIT = kWave * Fmt<DT>::EPC * kVpGroup;   // ids of a group at rep 1
-  const int units = (a.V + UNIT - 1) / UNIT;
+hipError_t launch_vprobs_dt(const VprobsArgs& a, void* block, hipStream_t s) {
+  const int units = (a.V + kVpUnit<DT> - 1) / kVpUnit<DT>;
   const int rep = (units + kVpGroups - 1) / kVpGroups;
   const int groups = (units + rep - 1) / rep;
-  const int slices = vp_slices(a.rows, groups, ws.rows);
+  const int slices = vp_slices(a.rows, groups);
   if (slices > 1) {
+    int4* cut = static_cast<int4*>(block);
+    const VprobsWs ws{cut, reinterpret_cast<double*>(cut + a.rows)};
     hipLaunchKernelGGL((vprobs_slices_kernel<DT>), dim3(slices, a.rows), dim3(kVpSliceBlock), 0, s,
                        a, groups, rep, slices, ws);
     const hipError_t e = hipGetLastError();
@@ -455,7 +458,14 @@ hipError_t launch_vprobs_dt(const VprobsArgs& a, const VprobsWs& ws, hipStream_t
 
 }  // namespace
 
-hipError_t launch_vprobs(const VprobsArgs& a, int dtype, const VprobsWs& ws, hipStream_t s) {
+size_t vprobs_ws_bytes(int rows, int vocab) {
+  // float32 rows have the most groups; fewer ids have no more of them
+  const int groups = min((vocab - 1) / kVpUnit<0> + 1, kVpGroups);
+  if (groups <= kVpAlone) return 0;
+  return (size_t)min(rows, kVpWsRows) * (sizeof(int4) + (size_t)groups * sizeof(double));
+}
+
+hipError_t launch_vprobs(const VprobsArgs& a, int dtype, void* ws, hipStream_t s) {
   return dtype == 0 ? launch_vprobs_dt<0>(a, ws, s) : launch_vprobs_dt<1>(a, ws, s);
 }
 

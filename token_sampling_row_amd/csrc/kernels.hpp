@@ -168,16 +168,18 @@ struct VprobsArgs {
   int32_t* out_accepted;
   int32_t* out_status;
 };
-// Its workspace: per sequence (of up to `rows`) kVpGroups sums and what the tests
-// decided (status, drafts kept, whether one was refused, its token).
+// Its workspace, where several workgroups share a sequence: per sequence what the tests
+// decided (status, drafts kept, whether one was refused, its token), and behind
+// all of these each sequence's group sums.
 constexpr int kVpGroups = 1024;   // most groups a row is cut into
-constexpr int kVpWsRows = 512;
+constexpr int kVpWsRows = 512;    // most sequences that are shared
 struct VprobsWs {
-  double* sums;
-  int4* cut;
-  int rows;
+  int4* cut;      // [rows]
+  double* sums;   // [rows][groups]
 };
-hipError_t launch_vprobs(const VprobsArgs& a, int dtype, const VprobsWs& ws, hipStream_t s);
+// Bytes of it that calls of up to `rows` sequences and `vocab` ids take (0: none do).
+size_t vprobs_ws_bytes(int rows, int vocab);
+hipError_t launch_vprobs(const VprobsArgs& a, int dtype, void* ws, hipStream_t s);
 
 hipError_t launch_philox(const uint32_t* ctr, int n, uint32_t k0, uint32_t k1, uint32_t* out,
                          hipStream_t s);
