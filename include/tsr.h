@@ -35,8 +35,9 @@
  *    unaligned access mode the HSA runtime sets, and no byte outside a row
  *    is read.
  *  - A handle is not thread-safe. Two calls on one handle may run on different
- *    streams only if they are not verify calls (verify uses per-handle
- *    workspace).
+ *    streams at the same time unless they use the same workspace of it:
+ *    spec_verify and tree_verify share one, beam_step and verify_probs have
+ *    one each.
  */
 #ifndef TSR_H_
 #define TSR_H_
@@ -415,13 +416,31 @@ int sample_hidden(tsr_handle h, const void* hidden, int hidden_dtype, int rows,
  * (TSR_EUNSUPPORTED beyond). Strides are not negative; rows may overlap or
  * repeat (stride 0). Up to 512 sequences of many ids are summed by several
  * workgroups each, through per-handle workspace of its own: not concurrent
- * with another verify_probs on the handle. */
+ * with another verify_probs on the handle (verify_probs_ex may be). */
 int verify_probs(tsr_handle h, const void* target_probs, int64_t target_seq_stride,
                  int64_t target_row_stride, const void* draft_probs, int64_t draft_seq_stride,
                  int64_t draft_row_stride, int dtype, const int32_t* draft_tokens,
                  const int32_t* draft_lens, const float* accept_u, const float* draw_u, int rows,
                  int K, int vocab, int32_t* out_tokens, int32_t* out_accepted,
                  int32_t* out_status, void* hip_stream);
+
+/* verify_probs with the caller's workspace in place of the handle's: calls with
+ * workspaces of their own may run at the same time on one handle (graphs that
+ * were captured with them as well).
+ *  workspace: device memory, 16-byte aligned, workspace_bytes long; at least
+ *      verify_probs_workspace's bytes (TSR_EINVAL otherwise). Its contents do
+ *      not matter before the call or after it. NULL: the handle's. */
+int verify_probs_ex(tsr_handle h, const void* target_probs, int64_t target_seq_stride,
+                    int64_t target_row_stride, const void* draft_probs, int64_t draft_seq_stride,
+                    int64_t draft_row_stride, int dtype, const int32_t* draft_tokens,
+                    const int32_t* draft_lens, const float* accept_u, const float* draw_u, int rows,
+                    int K, int vocab, int32_t* out_tokens, int32_t* out_accepted,
+                    int32_t* out_status, void* workspace, int64_t workspace_bytes,
+                    void* hip_stream);
+
+/* Bytes of workspace that verify_probs_ex takes for these sizes (under 2^23); 0
+ * where it takes none: one workgroup sums a sequence, or there is nothing to do. */
+int verify_probs_workspace(int dtype, int rows, int vocab);
 
 /* Test hook: out_words[i][0..3] = Philox4x32-10(counters[i][0..3], key = the
  * handle's seed) for i < n, computed on the device by the same function the

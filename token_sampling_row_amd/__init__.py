@@ -25,7 +25,8 @@ ROW_OK, ROW_NONFINITE, ROW_EMPTY, ROW_BADTOKEN, ROW_BADPARAM = 0, 1, 2, 3, 4
 EXPORTED_SYMBOLS = ("sampler_init", "sampler_destroy", "greedy_argmax", "sample_rows",
                     "sample_rows_masked", "sample_rows_ex", "spec_verify", "spec_verify_noalloc",
                     "tree_verify", "beam_step", "quantize_rows", "int8_logits",
-                    "sample_hidden", "verify_probs", "sampler_philox", "sampler_strerror")
+                    "sample_hidden", "verify_probs", "verify_probs_ex", "verify_probs_workspace",
+                    "sampler_philox", "sampler_strerror")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -106,6 +107,8 @@ def load_library():
                                   i32, ctypes.POINTER(_Params), u64, vp, ctypes.POINTER(_Diag), vp]
     lib.verify_probs.argtypes = [vp, vp, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, i32, i32,
                                  i32, vp, vp, vp, vp]
+    lib.verify_probs_ex.argtypes = lib.verify_probs.argtypes[:-1] + [vp, i64, vp]
+    lib.verify_probs_workspace.argtypes = [i32, i32, i32]
     lib.sampler_philox.argtypes = [vp, vp, i32, vp, vp]
     lib.sampler_strerror.argtypes = [i32]
     lib.sampler_strerror.restype = ctypes.c_char_p
@@ -248,7 +251,11 @@ def spec_verify_noalloc(device, seed, target, draft, draft_tokens, params, step:
 
 
 class Sampler:
-    """A handle on one GPU: seed (the Philox key) and the verify workspace."""
+    """A handle on one GPU: seed (the Philox key) and the verify workspace.
+
+    spec_verify and tree_verify share that workspace, and beam_step has one of its
+    own: such calls on one handle must not overlap on different streams. The
+    other calls may."""
 
     def __init__(self, device: int = 0, max_rows: int = 4096, max_vocab: int = 1 << 18,
                  max_k: int = 8, seed: int = 0):
@@ -260,6 +267,7 @@ class Sampler:
         self._h = h
         self.device = device
         self.seed = int(seed)
+        self._vp_bytes = {}   # verify_probs: workspace of a batch by its sizes
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
@@ -582,10 +590,12 @@ class Sampler:
         [rows, K+1, V] and draft [rows, K, V] (None: the draft tokens were
         proposed with certainty) float32 or bfloat16, draft_tokens [rows, K] and
         draft_lens [rows] (None: K each) int32, accept_u [rows, K] and draw_u
-        [rows] float32 in [0, 1) -> (tokens [rows, K+1], accepted [rows])."""
+        [rows] float32 in [0, 1) -> (tokens [rows, K+1], accepted [rows]). Each call
+        has a workspace of its own, from torch's allocator on its stream."""
         torch = _t()
         i32, f32, dev = torch.int32, torch.float32, self.device
-        dt = F32 if target.dtype is f32 else _dtype_code(target)
+        dt = F32 if target.dtype is f32 else BF16 if target.dtype is torch.bfloat16 else \
+            _dtype_code(target)
         if target.dim() != 3 or target.get_device() != dev:
             raise ValueError("target: not [rows, K + 1, vocab] on the handle's GPU")
         rows, k1, vocab = target.shape
@@ -612,20 +622,31 @@ class Sampler:
             self._vector(draw_u, f32, "draw_u", rows)
         n_ptr = None if draft_lens is None else self._vector(draft_lens, i32, "draft_lens", rows)
         s_ptr = None if out_status is None else self._vector(out_status, i32, "out_status", rows)
+        need = self._vp_bytes.get((dt, rows, vocab))
+        if need is None:
+            need = self._vp_bytes[dt, rows, vocab] = \
+                load_library().verify_probs_workspace(dt, rows, vocab)
+        if stream is None:
+            new = draft_tokens.new_empty
+        else:
+            def new(*shape):
+                return _new_like(stream, draft_tokens, *shape)
         if out_tokens is None:
-            out_tokens = _new_like(stream, draft_tokens, rows, k1)
+            out_tokens = new(rows, k1)
         else:
             self._vector(out_tokens, i32, "out_tokens", rows, k1)
         if out_accepted is None:
-            out_accepted = _new_like(stream, draft_tokens, rows)
+            out_accepted = new(rows)
         else:
             self._vector(out_accepted, i32, "out_accepted", rows)
+        ws = new(need // 4) if need else None
         if rows:
-            _check(load_library().verify_probs(
+            _check(load_library().verify_probs_ex(
                 self._h, target.data_ptr(), t_seq, t_row, d_ptr, d_seq, d_row, dt,
                 draft_tokens.data_ptr(), n_ptr, accept_u.data_ptr(), draw_u.data_ptr(), rows, K,
                 vocab, out_tokens.data_ptr(), out_accepted.data_ptr(), s_ptr,
-                _stream_on(dev, stream)), "verify_probs")
+                None if ws is None else ws.data_ptr(), need, _stream_on(dev, stream)),
+                "verify_probs")
         return out_tokens, out_accepted
 
     def philox(self, counters, stream=None):

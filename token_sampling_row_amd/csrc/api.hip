@@ -250,7 +250,7 @@ int sampler_init(tsr_handle* out, int device, int max_rows, int max_vocab, int m
                           (size_t)max_rows * 2 * tsr::kMaxSlices * sizeof(unsigned long long);
     const size_t bbytes = bslots * (sizeof(double) + sizeof(int32_t));
     const size_t pat = (((vbytes + 7) & ~(size_t)7) + rbytes + bbytes + 15) & ~(size_t)15;
-    const size_t bytes = pat + tsr::vprobs_ws_bytes(max_rows, max_vocab);
+    const size_t bytes = pat + tsr::vprobs_ws_most(max_rows, max_vocab);
     if (hipMalloc(&h->ws_block, bytes) != hipSuccess) return TSR_ENOMEM;
     if (hipMemset(h->ws_block, 0, bytes) != hipSuccess) return TSR_EDEVICE;
     if (hipDeviceSynchronize() != hipSuccess) return TSR_EDEVICE;
@@ -582,12 +582,18 @@ int sample_hidden(tsr_handle h, const void* hidden, int hidden_dtype, int rows,
   return rc;
 }
 
-int verify_probs(tsr_handle h, const void* target_probs, int64_t target_seq_stride,
-                 int64_t target_row_stride, const void* draft_probs, int64_t draft_seq_stride,
-                 int64_t draft_row_stride, int dtype, const int32_t* draft_tokens,
-                 const int32_t* draft_lens, const float* accept_u, const float* draw_u, int rows,
-                 int K, int vocab, int32_t* out_tokens, int32_t* out_accepted,
-                 int32_t* out_status, void* hip_stream) {
+int verify_probs_workspace(int dtype, int rows, int vocab) {
+  if ((dtype != TSR_F32 && dtype != TSR_BF16) || rows < 1 || vocab < 1) return 0;
+  return (int)tsr::vprobs_ws_bytes(dtype, rows, vocab);
+}
+
+int verify_probs_ex(tsr_handle h, const void* target_probs, int64_t target_seq_stride,
+                    int64_t target_row_stride, const void* draft_probs, int64_t draft_seq_stride,
+                    int64_t draft_row_stride, int dtype, const int32_t* draft_tokens,
+                    const int32_t* draft_lens, const float* accept_u, const float* draw_u, int rows,
+                    int K, int vocab, int32_t* out_tokens, int32_t* out_accepted,
+                    int32_t* out_status, void* workspace, int64_t workspace_bytes,
+                    void* hip_stream) {
   if (!h || !target_probs || !draft_tokens || !accept_u || !draw_u || !out_tokens || !out_accepted)
     return TSR_EINVAL;
   if (dtype != TSR_F32 && dtype != TSR_BF16) return TSR_EINVAL;
@@ -603,6 +609,9 @@ int verify_probs(tsr_handle h, const void* target_probs, int64_t target_seq_stri
     return TSR_EINVAL;
   if (vocab > kMaxWideVocab || rows > kMaxVprobsRows) return TSR_EUNSUPPORTED;
   if (rows == 0) return TSR_OK;
+  if (workspace && (((uintptr_t)workspace % 16) != 0 ||
+                    workspace_bytes < (int64_t)tsr::vprobs_ws_bytes(dtype, rows, vocab)))
+    return TSR_EINVAL;
   const long long es = esize(dtype);
   tsr::VprobsArgs a{};
   a.target = static_cast<const unsigned char*>(target_probs);
@@ -622,9 +631,22 @@ int verify_probs(tsr_handle h, const void* target_probs, int64_t target_seq_stri
   a.out_accepted = out_accepted;
   a.out_status = out_status;
   return on_device(h->device, [&]() -> int {
-    const hipError_t e = tsr::launch_vprobs(a, dtype, h->pws, (hipStream_t)hip_stream);
+    const hipError_t e = tsr::launch_vprobs(a, dtype, workspace ? workspace : h->pws,
+                                            (hipStream_t)hip_stream);
     return e == hipSuccess ? TSR_OK : TSR_EDEVICE;
   });
+}
+
+int verify_probs(tsr_handle h, const void* target_probs, int64_t target_seq_stride,
+                 int64_t target_row_stride, const void* draft_probs, int64_t draft_seq_stride,
+                 int64_t draft_row_stride, int dtype, const int32_t* draft_tokens,
+                 const int32_t* draft_lens, const float* accept_u, const float* draw_u, int rows,
+                 int K, int vocab, int32_t* out_tokens, int32_t* out_accepted,
+                 int32_t* out_status, void* hip_stream) {
+  return verify_probs_ex(h, target_probs, target_seq_stride, target_row_stride, draft_probs,
+                         draft_seq_stride, draft_row_stride, dtype, draft_tokens, draft_lens,
+                         accept_u, draw_u, rows, K, vocab, out_tokens, out_accepted, out_status,
+                         nullptr, 0, hip_stream);
 }
 
 int sampler_philox(tsr_handle h, const uint32_t* counters, int n, uint32_t* out_words,

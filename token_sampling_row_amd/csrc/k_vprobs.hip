@@ -434,35 +434,53 @@ __global__ __launch_bounds__(kVpSliceBlock) void vprobs_draw_kernel(VprobsArgs a
   vp_write(a, b, status, cut.y, x, token, lane);
 }
 
+// How a batch is cut.
+struct VpPlan {
+  int rep, groups, slices;
+};
+template <int DT>
+VpPlan vp_plan(int rows, int vocab) {
+  const int units = (vocab - 1) / kVpUnit<DT> + 1;
+  VpPlan p;
+  p.rep = (units + kVpGroups - 1) / kVpGroups;
+  p.groups = (units + p.rep - 1) / p.rep;
+  p.slices = vp_slices(rows, p.groups);
+  return p;
+}
+size_t vp_bytes(int rows, int groups) {
+  return (size_t)rows * (sizeof(int4) + (size_t)groups * sizeof(double));
+}
+
 template <int DT>
 hipError_t launch_vprobs_dt(const VprobsArgs& a, void* block, hipStream_t s) {
-  const int units = (a.V + kVpUnit<DT> - 1) / kVpUnit<DT>;
-  const int rep = (units + kVpGroups - 1) / kVpGroups;
-  const int groups = (units + rep - 1) / rep;
-  const int slices = vp_slices(a.rows, groups);
-  if (slices > 1) {
+  const VpPlan p = vp_plan<DT>(a.rows, a.V);
+  if (p.slices > 1) {
     int4* cut = static_cast<int4*>(block);
     const VprobsWs ws{cut, reinterpret_cast<double*>(cut + a.rows)};
-    hipLaunchKernelGGL((vprobs_slices_kernel<DT>), dim3(slices, a.rows), dim3(kVpSliceBlock), 0, s,
-                       a, groups, rep, slices, ws);
+    hipLaunchKernelGGL((vprobs_slices_kernel<DT>), dim3(p.slices, a.rows), dim3(kVpSliceBlock), 0,
+                       s, a, p.groups, p.rep, p.slices, ws);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((vprobs_draw_kernel<DT>), dim3(a.rows), dim3(kVpSliceBlock), 0, s, a, groups,
-                       rep, ws);
+    hipLaunchKernelGGL((vprobs_draw_kernel<DT>), dim3(a.rows), dim3(kVpSliceBlock), 0, s, a,
+                       p.groups, p.rep, ws);
   } else {
     hipLaunchKernelGGL((vprobs_kernel<DT>), dim3(a.rows), dim3(kVpWaves<DT> * kWave), 0, s, a,
-                       groups, rep);
+                       p.groups, p.rep);
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t vprobs_ws_bytes(int rows, int vocab) {
+size_t vprobs_ws_bytes(int dtype, int rows, int vocab) {
+  const VpPlan p = dtype == 0 ? vp_plan<0>(rows, vocab) : vp_plan<1>(rows, vocab);
+  return p.slices > 1 ? vp_bytes(rows, p.groups) : 0;
+}
+
+size_t vprobs_ws_most(int rows, int vocab) {
   // float32 rows have the most groups; fewer ids have no more of them
   const int groups = min((vocab - 1) / kVpUnit<0> + 1, kVpGroups);
-  if (groups <= kVpAlone) return 0;
-  return (size_t)min(rows, kVpWsRows) * (sizeof(int4) + (size_t)groups * sizeof(double));
+  return groups <= kVpAlone ? 0 : vp_bytes(min(rows, kVpWsRows), groups);
 }
 
 hipError_t launch_vprobs(const VprobsArgs& a, int dtype, void* ws, hipStream_t s) {

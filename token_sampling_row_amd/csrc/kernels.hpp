@@ -177,8 +177,10 @@ struct VprobsWs {
   int4* cut;      // [rows]
   double* sums;   // [rows][groups]
 };
-// Bytes of it that calls of up to `rows` sequences and `vocab` ids take (0: none do).
-size_t vprobs_ws_bytes(int rows, int vocab);
+// Bytes of it that a call takes (0: one workgroup sums a sequence), and the most that
+// calls of up to `rows` sequences and `vocab` ids of either type do.
+size_t vprobs_ws_bytes(int dtype, int rows, int vocab);
+size_t vprobs_ws_most(int rows, int vocab);
 hipError_t launch_vprobs(const VprobsArgs& a, int dtype, void* ws, hipStream_t s);
 
 hipError_t launch_philox(const uint32_t* ctr, int n, uint32_t k0, uint32_t k1, uint32_t* out,
