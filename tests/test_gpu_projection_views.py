@@ -74,3 +74,16 @@ def test_large_weights_under_rows_at_words(s, rows, stride, off):
     """Weights that outgrow the caches in whole lines, hidden rows that start at
     words or halves of lines, with a partial stage behind."""
     check(s, matrix(rows, 1399, stride, off, rows), matrix(40001, 1399, 1408, 0, 9))
+
+
+def test_a_device_number_as_text():
+    """As it comes from an environment variable; every call takes it as a number."""
+    with tsr.Sampler("0", max_rows=8, max_vocab=64, max_k=1) as s:
+        codes, scale = s.quantize_rows(torch.ones(2, 16, device=device()))
+        assert bool((codes == 127).all())
+        logits = s.int8_logits(codes, scale, codes, scale, dtype=torch.float32)
+        assert s.sample_rows(logits, {"temperature": 0.0}, 0).tolist() == [0, 0]
+        p = torch.ones(1, 2, 4, device=device())
+        x = torch.zeros(1, 1, dtype=torch.int32, device=device())
+        u = torch.zeros(1, 1, device=device())
+        assert s.verify_probs(p, None, x, u, u[0])[1].tolist() == [1]

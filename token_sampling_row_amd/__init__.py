@@ -265,7 +265,7 @@ class Sampler:
                                 int(max_k), ctypes.c_uint64(int(seed) & (2 ** 64 - 1))),
                "sampler_init")
         self._h = h
-        self.device = device
+        self.device = int(device)
         self.seed = int(seed)
         self._vp_bytes = {}   # verify_probs: workspace of a batch by its sizes
 
