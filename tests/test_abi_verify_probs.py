@@ -30,10 +30,12 @@ def test_a_null_handle(lib):  # noqa: F811
                                None, None, None, None, 0, None) == 1
 
 
+@pytest.mark.parametrize("raw", [0, 7])
 @pytest.mark.parametrize("rows,vocab,takes", [(3, 40000, True), (3, 32000, False),
                                               (600, 40000, False)])
-def test_each_call_brings_its_workspace(lib, monkeypatch, rows, vocab, takes):  # noqa: F811
-    """The binding against a library that records what it is given (host tensors)."""
+def test_each_call_brings_its_workspace(lib, monkeypatch, rows, vocab, takes, raw):  # noqa: F811
+    """The binding against a library that records what it is given (host tensors).
+    On the default stream (0) the handle's workspace is taken."""
     torch = pytest.importorskip("torch")
     calls = []
 
@@ -44,7 +46,7 @@ def test_each_call_brings_its_workspace(lib, monkeypatch, rows, vocab, takes):  
     fake = types.SimpleNamespace(verify_probs=record, verify_probs_ex=record,
                                  verify_probs_workspace=lib.verify_probs_workspace)
     monkeypatch.setattr(tsr, "load_library", lambda: fake)
-    monkeypatch.setattr(tsr, "_stream_on", lambda device, stream: 0)
+    monkeypatch.setattr(tsr, "_stream_on", lambda device, stream: raw)
     s = tsr.Sampler.__new__(tsr.Sampler)
     s._h, s.device, s._vp_bytes = ctypes.c_void_p(), -1, {}   # -1: the host
     p = torch.zeros(1, 2, vocab).expand(rows, 2, vocab)
@@ -54,5 +56,6 @@ def test_each_call_brings_its_workspace(lib, monkeypatch, rows, vocab, takes):  
     for args in calls:
         assert len(args) == 21
         workspace, size = args[18], args[19]
-        assert size == lib.verify_probs_workspace(0, rows, vocab)
-        assert (workspace is not None and workspace % 16 == 0) == takes
+        assert size == (lib.verify_probs_workspace(0, rows, vocab) if raw else 0)
+        assert (workspace is not None and workspace % 16 == 0) == (takes and raw != 0)
+        assert args[20] == raw

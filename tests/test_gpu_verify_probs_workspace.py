@@ -61,12 +61,13 @@ def batch(rows, K, V, seed):
 
 def test_calls_of_one_handle_on_several_streams():
     """Batches whose sequences are summed by several workgroups each, on three streams
-    of one handle at once, each again and again: as each alone."""
+    of one handle at once, the default stream among them, each again and again: as
+    each alone."""
     sets = [batch(rows, 2, V, rows) for rows, V in ((48, 90001), (64, 70001), (33, 100003))]
     with tsr.Sampler(0, max_rows=64, max_vocab=1 << 17, max_k=2) as s:
         want = [s.verify_probs(*a) for a in sets]
         torch.cuda.synchronize()
-        streams = [torch.cuda.Stream() for _ in sets]
+        streams = [None, torch.cuda.Stream(), torch.cuda.Stream()]
         got = [[], [], []]
         for _ in range(10):
             for k, a in enumerate(sets):

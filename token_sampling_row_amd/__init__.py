@@ -590,8 +590,10 @@ class Sampler:
         [rows, K+1, V] and draft [rows, K, V] (None: the draft tokens were
         proposed with certainty) float32 or bfloat16, draft_tokens [rows, K] and
         draft_lens [rows] (None: K each) int32, accept_u [rows, K] and draw_u
-        [rows] float32 in [0, 1) -> (tokens [rows, K+1], accepted [rows]). Each call
-        has a workspace of its own, from torch's allocator on its stream."""
+        [rows] float32 in [0, 1) -> (tokens [rows, K+1], accepted [rows]). Calls on
+        the default stream, which follow each other and are never captured, take the
+        handle's workspace; on other streams each has one of its own, from torch's
+        allocator."""
         torch = _t()
         i32, f32, dev = torch.int32, torch.float32, self.device
         dt = F32 if target.dtype is f32 else BF16 if target.dtype is torch.bfloat16 else \
@@ -622,10 +624,6 @@ class Sampler:
             self._vector(draw_u, f32, "draw_u", rows)
         n_ptr = None if draft_lens is None else self._vector(draft_lens, i32, "draft_lens", rows)
         s_ptr = None if out_status is None else self._vector(out_status, i32, "out_status", rows)
-        need = self._vp_bytes.get((dt, rows, vocab))
-        if need is None:
-            need = self._vp_bytes[dt, rows, vocab] = \
-                load_library().verify_probs_workspace(dt, rows, vocab)
         if stream is None:
             new = draft_tokens.new_empty
         else:
@@ -639,14 +637,23 @@ class Sampler:
             out_accepted = new(rows)
         else:
             self._vector(out_accepted, i32, "out_accepted", rows)
-        ws = new(need // 4) if need else None
+        raw = _stream_on(dev, stream)
+        ws = ws_ptr = None
+        need = 0
+        if raw:
+            need = self._vp_bytes.get((dt, rows, vocab))
+            if need is None:
+                need = self._vp_bytes[dt, rows, vocab] = \
+                    load_library().verify_probs_workspace(dt, rows, vocab)
+            if need:
+                ws = new(need // 4)
+                ws_ptr = ws.data_ptr()
         if rows:
             _check(load_library().verify_probs_ex(
                 self._h, target.data_ptr(), t_seq, t_row, d_ptr, d_seq, d_row, dt,
                 draft_tokens.data_ptr(), n_ptr, accept_u.data_ptr(), draw_u.data_ptr(), rows, K,
                 vocab, out_tokens.data_ptr(), out_accepted.data_ptr(), s_ptr,
-                None if ws is None else ws.data_ptr(), need, _stream_on(dev, stream)),
-                "verify_probs")
+                ws_ptr, need, raw), "verify_probs")
         return out_tokens, out_accepted
 
     def philox(self, counters, stream=None):
