@@ -1,13 +1,17 @@
 // The 8-bit output projection (int8_logits): out[r][n] = sum_k x[r][k] w[n][k]
 // in 32-bit integers, times the row's and the channel's scale.
 //
-// Few rows are bound by the weight's bytes: 1 x 128256 x 4096 78 us, 6.7 TB/s of
+// Few rows are bound by the weight's bytes: 1 x 128256 x 4096 79 us, 6.7 TB/s of
 // the 6.9 that reads reach here; 64 x 128256 104 us, 5.2 TB/s, its logits' 16 MB
-// among them. Many are bound by the matrix pipes and by what feeds them: 1024 x
-// 151936 x 4096 502 us, 2.54 P op/s, the pipes busy two thirds of it (products
-// of random codes alone reach 3.8, where the card's power holds its clock). The
-// weight is cut into runs of channels, each read from memory once: every hidden
-// row, or up to 320 of them, meets a run while it is in LDS.
+// among them. Many are bound by the matrix pipes and by the LDS that feeds them:
+// 1024 x 151936 x 4096 513 us, 2.49 P op/s (its two launches traced alone 500 and
+// 31), the pipes busy two thirds of it (products of random codes alone reach 3.8,
+// where the card's power holds its clock); a stage of a 256 x 256 tile takes 1536
+// cycles of LDS reads and 512 of loads landing there beside 2048 of products.
+// The weight is cut into runs of channels: every hidden row, or up to 320 of
+// them, meets a run while it is in LDS. The tiles of one run share it through an
+// L2; the hidden rows come to each of the eight anew with every round of tiles
+// (909 MB fetched in the first launch of the 1024 rows, the weight 604 of them).
 #pragma once
 
 #include <cmath>
@@ -266,7 +270,9 @@ struct Tile {
           // whole lines of many rows' logits leave the caches before they are read:
           // 256 x 128256 150 us kept in them, 139 not, 1024 x 151936 519 and 511 (24
           // rows 84 and 90; lines that two tiles share, 256 x 50001 x 4095: 122 and
-          // 180)
+          // 180). With the sampler behind, which reads them: 128 x 128256 159 and
+          // 154, 256 x 128256 183 and 174, 1024 x 128256 506 and 508, but 256 x
+          // 32000 65 and 66, 320 x 32000 fp32 79 and 82.
           if (BM >= 128 && whole_lines)
             store16_once(o, v);
           else

@@ -8,7 +8,7 @@
 //
 // Few rows are bound by three trips to memory, each waiting for the last (draft
 // tokens, their probabilities, the row), and the draw's fourth: 1 x 32000 fp32
-// 7.1 us, 64 x 32000 9.4 (12 MB). Many are bound by the rows' bytes: 128 x 128256
+// 7.0 us, 64 x 32000 9.6 (12 MB). Many are bound by the rows' bytes: 128 x 128256
 // fp32 19.6 us for the sums (92 MB, 4.7 TB/s) and 4.9 for the draw.
 #include "kernels.hpp"
 #include "wide_mem.hpp"
@@ -29,7 +29,7 @@ constexpr int kVpAlone = 32;  // groups that one workgroup sums as fast as sever
 template <int DT> constexpr int kVpUnit = kWave * Fmt<DT>::EPC * kVpGroup;   // ids of a group
 
 // How many workgroups share a row's sums (1: the one-launch kernel, as fast up
-// to 32 groups: 64 x 32000 fp32 9.8 us). A wavefront takes two groups at a time,
+// to 32 groups: 64 x 32000 fp32 9.6 us). A wavefront takes two groups at a time,
 // or one where that leaves places empty (33 x 151935 bf16 11.4 us against 11.9,
 // but 64 x 128256 bf16 15.7 against 14.5); 256 x 128256 fp32 with eight
 // workgroups to a row 37 us, with four 39.
@@ -138,8 +138,9 @@ __device__ __forceinline__ double vp_weights(uint4 pr, uint4 qr, int e0, int x, 
 }
 
 // kVpGroup spans from span s0 on: the chunks this lane has of them. All loads
-// are on their way together; spans past the row's whole ones repeat the last
-// of those (`in` tells), the partial one is loaded by itself.
+// are on their way together; spans past the row's whole ones load the last of
+// those again, and are then replaced by the partial one, loaded by itself, or by
+// zeros.
 template <int DT, int SUB>
 struct VpGroup {
   uint4 p[kVpGroup], q[SUB == 1 ? kVpGroup : 1];
