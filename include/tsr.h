@@ -442,6 +442,138 @@ int verify_probs_ex(tsr_handle h, const void* target_probs, int64_t target_seq_s
  * where it takes none: one workgroup sums a sequence, or there is nothing to do. */
 int verify_probs_workspace(int dtype, int rows, int vocab);
 
+/* 8-bit codes of rows that are first added to a residual and normed by their root
+ * mean square: quantize_rows for the hidden states that a model's last block
+ * leaves, before int8_logits.
+ *   h = x + residual, rounded once to their type (h = x without a residual)
+ *   n_i = h_i weight_i / sqrt(mean(h^2) + eps)
+ *  x, residual [rows][width] of type dtype, x_stride and residual_stride
+ *      elements apart; residual NULL: none.
+ *  weight [width] of type weight_dtype; NULL: ones. For a weight that is held
+ *      less one, add the one when it is loaded.
+ *  out_residual [rows][width] of type dtype, out_residual_stride elements apart:
+ *      h. NULL: not kept; it has to be NULL without a residual. It may be x or
+ *      residual itself, with the same stride.
+ *  out_scale [rows] float32: s = max |n| of the row / 127.
+ *  out_codes [rows][width] int8, codes_stride bytes apart: n / s = 127 h_i w_i /
+ *      max |h w|, rounded to the nearest whole number, ties to even, decided on
+ *      that exact quotient.
+ * A row whose h w is zero everywhere gets scale 0 and codes 0. A row in which h or
+ * h w holds NaN or an infinity (h rounded to its type, h w in 64 bits) gets scale
+ * NaN and codes 0, as in quantize_rows. eps is finite and >= 0. Bytes between
+ * the rows are left as they are. Outputs that overlap inputs or each other in any
+ * other way are TSR_EINVAL.
+ * rows is not bound by the handle's max_rows; rows < 2^24, width <= 2^30 and
+ * strides < 2^36 (TSR_EUNSUPPORTED beyond). Uses no workspace. */
+int norm_quantize_rows(tsr_handle h, const void* x, int64_t x_stride, const void* residual,
+                       int64_t residual_stride, int dtype, const void* weight, int weight_dtype,
+                       double eps, int rows, int width, void* out_residual,
+                       int64_t out_residual_stride, int8_t* out_codes, int64_t codes_stride,
+                       float* out_scale, void* hip_stream);
+
+/* Outputs of token_logprobs (device memory); NULL: not wanted.
+ *  logprob [rows][n_tokens] float32: log p of each given token.
+ *  entropy [rows] float32: -sum_j p_j log p_j.
+ *  top_ids, top_logprob [rows][top_k]: the top_k ids of the largest logits, largest
+ *      first, equal ones by the lower id, and their log p. Positions past the
+ *      row's finite logits hold -1 and -inf.
+ *  norm [rows][2] float32: the largest logit M and Z = sum_j exp((z_j - M) / T):
+ *      what token_logprobs_grad takes; M / T + log Z is the log of the sum of all
+ *      exp(z_j / T).
+ *  status [rows]: TSR_ROW_NONFINITE (a NaN or +inf logit) or TSR_ROW_EMPTY (every
+ *      logit is -inf), with NaN in the row's outputs and -1 in its ids; else
+ *      TSR_ROW_BADTOKEN (a token that is neither -1 nor in [0, vocab): NaN for it
+ *      alone); else TSR_ROW_OK. */
+typedef struct {
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprob;
+  float* norm;
+  int32_t* status;
+} tsr_logprobs;
+
+/* Log probabilities of given tokens under p = softmax(logits / temperature), with
+ * the entropy and the likeliest alternatives: scores of prompts, drafts and choices,
+ * and a teacher's top tokens for distill_topk.
+ *  logits [rows][vocab] of type dtype, row_stride elements apart. Logits of -inf
+ *      (tokens that are not allowed) have p = 0 and log p = -inf.
+ *  temperature: finite, >= 1e-30.
+ *  tokens [rows][n_tokens] int32 (NULL with n_tokens 0); -1 is padding, as the
+ *      verify steps leave behind the last token: its log p is 0.
+ *  workspace: 16-byte aligned device memory of at least token_logprobs_workspace
+ *      bytes, the call's own until it is done (NULL where that is 0). Its
+ *      contents do not matter before the call or after it.
+ * rows and vocab are not bound by the handle's. n_tokens <= 1024, top_k <= 64,
+ * rows < 2^22, vocab <= 2^30, row_stride < 2^36 (TSR_EUNSUPPORTED beyond). */
+int token_logprobs(tsr_handle h, const void* logits, int dtype, int rows, int vocab,
+                   int64_t row_stride, double temperature, const int32_t* tokens, int n_tokens,
+                   int top_k, const tsr_logprobs* out, void* workspace, int64_t workspace_bytes,
+                   void* hip_stream);
+
+/* Bytes of workspace that token_logprobs takes for these sizes; 0: none (or sizes
+ * that it does not take). */
+int token_logprobs_workspace(int dtype, int rows, int vocab, int top_k);
+
+/* The gradient of token_logprobs' log p and entropy by the logits:
+ *   out[r][j] = (sum_i g[r][i] [tokens[r][i] = j]
+ *                - p_j (sum_i g[r][i] + ge[r] (log p_j + H[r]))) / temperature
+ * with g = grad_logprob, ge = grad_entropy and H = entropy.
+ *  logits, temperature, tokens: as given to token_logprobs; norm and entropy [rows]:
+ *      as it left them. Tokens of -1 and their g do not count; one that is neither
+ *      -1 nor in [0, vocab) makes its row NaN, as norm does in the rows that
+ *      token_logprobs marked NONFINITE or EMPTY.
+ *  grad_logprob [rows][n_tokens] (NULL with n_tokens 0); grad_entropy [rows], or
+ *      NULL: no gradient comes back to the entropy (entropy may then be NULL).
+ *  out_grad [rows][vocab] of type dtype, grad_stride elements apart, none of it in
+ *      the logits' memory (TSR_EINVAL). What lies between vocab and grad_stride is
+ *      left as it is. Each element is rounded once.
+ * A row to which only zeros come back gets zeros, and its logits are not looked at.
+ * Limits as token_logprobs'. Uses no workspace. */
+int token_logprobs_grad(tsr_handle h, const void* logits, int dtype, int rows, int vocab,
+                        int64_t row_stride, double temperature, const int32_t* tokens,
+                        int n_tokens, const float* norm, const float* grad_logprob,
+                        const float* entropy, const float* grad_entropy, void* out_grad,
+                        int64_t grad_stride, void* hip_stream);
+
+/* Distillation of a draft model from a teacher's top tokens, loss and gradient: per
+ * row the divergence of p = softmax(logits / temperature) from the teacher's q, which
+ * is given by k entries.
+ *  ids, teacher_logprob [rows][k]: token ids and the teacher's log probabilities at the
+ *      same temperature, as token_logprobs' top_ids and top_logprob. An id of -1 is no
+ *      entry, a log probability of -inf one with q = 0. An id that comes twice
+ *      counts with both its q.
+ *  tail 0: q is the entries' exp over their sum (any constant may be added to a row's
+ *      values): L = sum_i q_i (log q_i - log p_i).
+ *  tail 1: q_i = exp(teacher_logprob), and what they leave of 1 (0 where that is at
+ *      most 2^-20, the rounding of the log probabilities) is the teacher's mass q_r of all
+ *      ids that are no entry: L = sum_i q_i (log q_i - log p_i) + q_r (log q_r -
+ *      log p_r), with p_r the sum of p over those ids.
+ *  row_weight [rows] float32 (NULL: 1 each), for instance 1 / rows and 0 for
+ *      padding: out_loss = row_weight * L, and rows of weight 0 get loss and gradient 0,
+ *      their logits and entries not looked at.
+ *  out_loss [rows] float32. +inf where p is 0 at an entry whose q is not.
+ *  out_grad [rows][vocab] of type dtype, grad_stride elements apart: the gradient of the
+ *      sum of out_loss by the logits, (row_weight / temperature) times Q p_j - q_j at
+ *      entries and p_j (Q - q_r / p_r) elsewhere, Q = sum q + q_r; each rounded once.
+ *      NULL: the loss alone. None of it in the logits' memory (TSR_EINVAL). For a
+ *      loss over temperatures the usual factor temperature^2 goes into row_weight.
+ *  out_status [rows] (nullable): TSR_ROW_OK, else loss and gradient are NaN: the first
+ *      that holds of TSR_ROW_BADTOKEN (an id neither -1 nor in [0, vocab)),
+ *      TSR_ROW_NONFINITE (a NaN or +inf log probability), TSR_ROW_EMPTY (no entry with
+ *      q > 0), TSR_ROW_NONFINITE, TSR_ROW_EMPTY (the logits, as in token_logprobs).
+ *  workspace: as token_logprobs', of distill_topk_workspace bytes.
+ * 1 <= k; k <= 64 and the limits of token_logprobs (TSR_EUNSUPPORTED beyond). */
+int distill_topk(tsr_handle h, const void* logits, int dtype, int rows, int vocab,
+                 int64_t row_stride, double temperature, const int32_t* ids,
+                 const float* teacher_logprob, int k, int tail, const float* row_weight,
+                 float* out_loss, void* out_grad, int64_t grad_stride, int32_t* out_status,
+                 void* workspace, int64_t workspace_bytes, void* hip_stream);
+
+/* Bytes of workspace that distill_topk takes for these sizes, with a gradient
+ * (want_grad 1) or without one; 0: none. */
+int distill_topk_workspace(int dtype, int rows, int vocab, int want_grad);
+
 /* Test hook: out_words[i][0..3] = Philox4x32-10(counters[i][0..3], key = the
  * handle's seed) for i < n, computed on the device by the same function the
  * sampler uses. counters and out_words are device memory. */

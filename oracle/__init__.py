@@ -17,6 +17,8 @@ philox   Philox4x32-10 counter-based generator (Salmon, Moraes, Dror, Shaw,
 tree     The tree (multi-candidate) verify step.
 int8     Absmax codes of rows and the logits of an 8-bit projection, with the
          bound that the kernels' roundings keep.
+scores   The RMS norm with a residual and 8-bit codes, log probabilities with
+         their gradient, distillation from a teacher's top entries, with bounds.
 vprobs   The verify step from probabilities and given random numbers.
 beam     One beam-search step (eq. 39.1, Listing 39.1) and the search built on it.
 sampler  The filter chain (temperature, softmax, top-k, top-p, min-p,

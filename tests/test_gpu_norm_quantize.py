@@ -1,0 +1,208 @@
+"""norm_quantize_rows against its reference in 64 bits (oracle/scores.py): codes and sums
+equal, the scale within one rounding to float32 of a value formed in 64 bits (2^-24
+relative, and 2^-30 for what 64 bits lose over the sums)."""
+import numpy as np
+import pytest
+
+from tests.gpu_common import device, gpu_available, torch
+
+import token_sampling_row_amd as tsr
+from oracle import scores as sc
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+TD = {"f32": torch.float32, "bf16": torch.bfloat16}
+NP = {torch.float32: "f32", torch.bfloat16: "bf16"}
+
+
+@pytest.fixture(scope="module")
+def s():
+    with tsr.Sampler(0, max_rows=64, max_vocab=1000, max_k=1, seed=3) as h:
+        yield h
+
+
+def rows_of(rng, rows, width, dtype, size=1.0):
+    x = rng.normal(0, size, (rows, width)) * np.exp(rng.normal(0, 2, (rows, 1)))
+    return torch.from_numpy(x.astype(np.float32)).to(TD[dtype]).to(device())
+
+
+def vals(t):
+    return None if t is None else t.float().cpu().numpy()
+
+
+def check(got, x, w, eps, res, before=None):
+    """`got` against the reference of x, res (as they were: `before`) and w."""
+    xv, rv = before if before is not None else (vals(x), vals(res))
+    codes, scale, h = sc.norm_quantize(xv, vals(w), eps, rv, NP[x.dtype])
+    assert np.array_equal(got[0].cpu().numpy(), codes)
+    g = got[1].cpu().numpy().astype(np.float64)
+    assert np.array_equal(np.isnan(g), np.isnan(scale))
+    ok = ~np.isnan(scale)
+    assert (np.abs(g - scale)[ok] <= scale[ok] * (2.0 ** -24 + 2.0 ** -30) + 2.0 ** -149).all()
+    if rv is not None:
+        assert np.array_equal(vals(got[2]).view(np.uint32)[ok], h.view(np.uint32)[ok])
+        assert np.array_equal(np.isfinite(vals(got[2])), np.isfinite(h))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("wtype", ["f32", "bf16", None])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,width", [(1, 1), (3, 2), (1, 7), (5, 8), (2, 63), (7, 257),
+                                        (4, 1003), (33, 2048), (1, 4096), (3, 4097), (2, 8191),
+                                        (300, 520), (2, 8192), (2, 16384), (2, 16391), (1, 40000)])
+def test_codes_match(s, dtype, wtype, residual, rows, width):
+    rng = np.random.default_rng([rows, width, residual])
+    x = rows_of(rng, rows, width, dtype)
+    res = rows_of(rng, rows, width, dtype, 2.0) if residual else None
+    w = None
+    if wtype:
+        w = torch.from_numpy(rng.normal(1, 0.3, width).astype(np.float32)).to(TD[wtype]).to(device())
+    check(s.norm_quantize_rows(x, w, 1e-5, res), x, w, 1e-5, res)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [257, 2049, 4097])
+@pytest.mark.parametrize("width", [64, 511, 1024, 1537, 2049, 4096, 5003])
+def test_many_rows(s, dtype, rows, width):
+    """On either side of the numbers of rows and chunks at which kernels could divide their
+    work otherwise: some rows against the reference, all against smaller batches."""
+    g = torch.Generator(device()).manual_seed(width)
+    x = torch.randn(rows, width, device=device(), generator=g)
+    x = (x * torch.exp(torch.randn(rows, 1, device=device(), generator=g))).to(TD[dtype])
+    res = torch.randn(rows, width, device=device(), generator=g).to(TD[dtype])
+    w = torch.randn(width, device=device(), generator=g)
+    x[7, width - 1], res[rows - 1, 0], x[rows - 2], res[rows - 2] = float("nan"), 1e30, 0.0, 0.0
+    got = s.norm_quantize_rows(x, w, 1e-6, res)
+    some = [0, 1, 7, rows // 2, rows - 3, rows - 2, rows - 1]
+    check([t[some] for t in got], x[some], w, 1e-6, res[some])
+    for r0 in range(0, rows, 300):
+        part = s.norm_quantize_rows(x[r0:r0 + 300], w, 1e-6, res[r0:r0 + 300])
+        for a, b in zip(part, got):
+            b = b[r0:r0 + 300]
+            assert bool(((a == b) | ((a != a) & (b != b))).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_special_rows(s, dtype):
+    W = 515
+    rng = np.random.default_rng(5)
+    x = rng.normal(0, 1, (14, W))
+    x[0] = 0.0
+    x[1] = -0.0
+    x[2] = rng.integers(-254, 255, W)
+    x[2, 7] = 254.0                       # every odd entry is a half
+    x[3] = 3.25
+    x[4, 0] = np.nan
+    x[5, W - 1] = np.inf
+    x[6, 100] = -np.inf
+    x[7] *= 1e-37
+    x[8] *= 1e-39
+    x[9] = 0.0
+    x[9, 3] = 1e-38
+    x[10] *= 3e37                         # squares past float32
+    x[11] = -np.abs(x[11])
+    x[12] *= 1e-20
+    x[13] = 0.0
+    x[13, W - 1] = -5.0
+    t = torch.from_numpy(x.astype(np.float32)).to(TD[dtype]).to(device())
+    w = torch.from_numpy(rng.normal(1, 0.3, W).astype(np.float32)).to(device())
+    for weight in (None, w, w.bfloat16()):
+        for eps in (0.0, 1e-6, 10.0):
+            check(s.norm_quantize_rows(t, weight, eps), t, weight, eps, None)
+    for bad in (float("nan"), float("inf")):   # one channel of the weight spoils every row
+        v = w.clone()
+        v[9] = bad
+        codes, scale = s.norm_quantize_rows(t, v)
+        assert bool(scale.isnan().all()) and not bool(codes.any())
+    v = w.clone()
+    v[:] = 0.0
+    codes, scale = s.norm_quantize_rows(t, v)
+    assert not bool(codes.any()) and bool((scale[[0, 3, 11]] == 0).all())
+    big = torch.full((2, 40), 3e38, device=device())   # the sum overflows, its parts do not
+    codes, scale, h = s.norm_quantize_rows(big, None, 1e-6, big)
+    assert bool(scale.isnan().all()) and bool(h.isinf().all()) and not bool(codes.any())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_halves_and_near_halves(s, dtype):
+    """Rows made of values whose codes are halves or lie next to them: products of rows and
+    weights whose quotient by the largest is (k + 1/2) / 127 to the last bits."""
+    W = 1016
+    rng = np.random.default_rng(8)
+    k = np.arange(W) % 127
+    x = ((k + 0.5) * 2).astype(np.float32)      # 127 x / 254 = k + 1/2
+    near = np.nextafter(x, np.where(rng.random(W) < 0.5, 0.0, 1e9).astype(np.float32))
+    x = np.stack([x, -x, near, x * 3, near * 5])
+    x[:3, 0], x[3, 0], x[4, 0] = 254.0, 762.0, 1270.0
+    t = torch.from_numpy(x.astype(np.float32)).to(TD[dtype]).to(device())
+    p2 = torch.from_numpy(np.exp2(rng.integers(-3, 1, W)).astype(np.float32)).to(device())
+    p2[0] = 1.0
+    odd = torch.full((W,), 0.7, device=device())
+    for w in (None, p2, p2.bfloat16(), odd, odd.bfloat16()):
+        check(s.norm_quantize_rows(t, w), t, w, 1e-6, None)
+    # both factors with all their bits: x_i w_i next to a half of the largest's share
+    w = np.random.default_rng(9).uniform(0.5, 2, W).astype(np.float32)
+    goal = (k + 0.5) / 127 * 300.0
+    v = (goal / w.astype(np.float64)).astype(np.float32)
+    v[0], w[0] = 300.0, 1.0
+    t = torch.from_numpy(np.stack([v, -v])).to(device())
+    w = torch.from_numpy(w).to(device())
+    check(s.norm_quantize_rows(t, w), t, w, 1e-6, None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("off", [0, 1, 3])
+@pytest.mark.parametrize("width", [5, 1001, 20011])
+def test_strided_rows(s, dtype, off, width):
+    """Rows inside wider tensors, at odd element and byte offsets; what lies between the
+    outputs' rows stays as it was."""
+    rng = np.random.default_rng(off)
+    big = rows_of(rng, 9, width + 99, dtype)
+    rbig = rows_of(rng, 9, width + 51, dtype)
+    x, res = big[:, off:off + width], rbig[:, 2 * off:2 * off + width]
+    w = rows_of(rng, 1, width + 8, dtype)[0, off:off + width]
+    out = torch.full((9, width + 110), 77, dtype=torch.int8, device=device())
+    keep = torch.full((9, width + 33), 77.0, dtype=TD[dtype], device=device())
+    got = s.norm_quantize_rows(x, w, 1e-6, res, out=out[:, off:off + width],
+                               out_residual=keep[:, off:off + width])
+    check(got, x, w, 1e-6, res)
+    for t in (out, keep):
+        assert bool((t[:, :off] == 77).all()) and bool((t[:, off + width:] == 77).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,width", [(4, 100), (5, 4099), (3, 20000), (2100, 1031)])
+@pytest.mark.parametrize("on", ["x", "residual"])
+def test_the_sum_in_place(s, dtype, rows, width, on):
+    rng = np.random.default_rng(3)
+    x, res = rows_of(rng, rows, width, dtype), rows_of(rng, rows, width, dtype)
+    before = (vals(x), vals(res))
+    target = x if on == "x" else res
+    other = (res if on == "x" else x).clone()
+    got = s.norm_quantize_rows(x, None, 1e-6, res, out_residual=target)
+    assert got[2] is target
+    check(got, x, None, 1e-6, res, before)
+    assert torch.equal(other, res if on == "x" else x)
+
+
+def test_the_same_codes_as_of_rows_normed_before(s):
+    """With a weight of ones and no residual the codes are those of quantize_rows, whose
+    scale is the largest value's share rounded to float32: equal but for values within
+    that rounding of a half, (127 + 1) 2^-23 of a code."""
+    g = torch.Generator(device()).manual_seed(1)
+    x = torch.randn(50, 3001, device=device(), generator=g)
+    a, _ = s.norm_quantize_rows(x)
+    b, _ = s.quantize_rows(x)
+    t = x.double() * 127 / x.abs().amax(1, keepdim=True).double()
+    clear = ((t.abs() % 1.0) - 0.5).abs() > 128 * 2.0 ** -23
+    assert torch.equal(a[clear], b[clear]) and float(clear.float().mean()) > 0.99
+
+
+def test_a_channel_past_2_31_bytes(s):
+    """Row offsets beyond 32 bits, in bytes and in elements."""
+    rows, stride = 5, (1 << 31) // 3
+    big = torch.zeros(4 * stride + 64, dtype=torch.bfloat16, device=device())
+    x = big.as_strided((rows, 64), (stride, 1))
+    x.copy_(torch.randn(rows, 64, device=device()))
+    check(s.norm_quantize_rows(x), x, None, 1e-6, None)

@@ -11,12 +11,13 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import Any, NamedTuple
 
 __all__ = [
     "TsrError", "TsrUnavailable", "Params", "Sampler", "library_path", "load_library",
     "spec_verify_noalloc",
     "F32", "BF16", "JOINT", "SEQUENTIAL", "ROW_OK", "ROW_NONFINITE", "ROW_EMPTY",
-    "ROW_BADTOKEN", "ROW_BADPARAM", "EXPORTED_SYMBOLS", "pack_row_params",
+    "ROW_BADTOKEN", "ROW_BADPARAM", "EXPORTED_SYMBOLS", "pack_row_params", "TokenLogprobs",
 ]
 
 F32, BF16 = 0, 1
@@ -26,6 +27,8 @@ EXPORTED_SYMBOLS = ("sampler_init", "sampler_destroy", "greedy_argmax", "sample_
                     "sample_rows_masked", "sample_rows_ex", "spec_verify", "spec_verify_noalloc",
                     "tree_verify", "beam_step", "quantize_rows", "int8_logits",
                     "sample_hidden", "verify_probs", "verify_probs_ex", "verify_probs_workspace",
+                    "norm_quantize_rows", "token_logprobs", "token_logprobs_workspace",
+                    "token_logprobs_grad", "distill_topk", "distill_topk_workspace",
                     "sampler_philox", "sampler_strerror")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -70,6 +73,22 @@ class _Head(ctypes.Structure):
                 ("vocab", ctypes.c_int32), ("width", ctypes.c_int32)]
 
 
+class _Logprobs(ctypes.Structure):
+    _fields_ = [("logprob", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+                ("top_ids", ctypes.c_void_p), ("top_logprob", ctypes.c_void_p),
+                ("norm", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class TokenLogprobs(NamedTuple):
+    """What Sampler.token_logprobs returns; None: not asked for."""
+    logprob: Any       # float32, shaped as the tokens
+    entropy: Any       # [rows] float32
+    top_ids: Any       # [rows, top_k] int32
+    top_logprob: Any   # [rows, top_k] float32
+    norm: Any          # [rows, 2] float32: largest logit, sum of exp((z - largest) / T)
+    status: Any        # [rows] int32
+
+
 _lib = None
 
 
@@ -109,6 +128,17 @@ def load_library():
                                  i32, vp, vp, vp, vp]
     lib.verify_probs_ex.argtypes = lib.verify_probs.argtypes[:-1] + [vp, i64, vp]
     lib.verify_probs_workspace.argtypes = [i32, i32, i32]
+    f64 = ctypes.c_double
+    lib.norm_quantize_rows.argtypes = [vp, vp, i64, vp, i64, i32, vp, i32, f64, i32, i32, vp, i64,
+                                       vp, i64, vp, vp]
+    lib.token_logprobs.argtypes = [vp, vp, i32, i32, i32, i64, f64, vp, i32, i32,
+                                   ctypes.POINTER(_Logprobs), vp, i64, vp]
+    lib.token_logprobs_workspace.argtypes = [i32, i32, i32, i32]
+    lib.token_logprobs_grad.argtypes = [vp, vp, i32, i32, i32, i64, f64, vp, i32, vp, vp, vp, vp,
+                                        vp, i64, vp]
+    lib.distill_topk.argtypes = [vp, vp, i32, i32, i32, i64, f64, vp, vp, i32, i32, vp, vp, vp,
+                                 i64, vp, vp, i64, vp]
+    lib.distill_topk_workspace.argtypes = [i32, i32, i32, i32]
     lib.sampler_philox.argtypes = [vp, vp, i32, vp, vp]
     lib.sampler_strerror.argtypes = [i32]
     lib.sampler_strerror.restype = ctypes.c_char_p
@@ -655,6 +685,196 @@ class Sampler:
                 vocab, out_tokens.data_ptr(), out_accepted.data_ptr(), s_ptr,
                 ws_ptr, need, raw), "verify_probs")
         return out_tokens, out_accepted
+
+    # Around the logits: the norm before the 8-bit projection, log probabilities with
+    # their gradient, and distillation. Checks as above.
+    def _matrix(self, t, what):
+        """Type, rows, columns and row stride of t, a matrix of contiguous rows that do
+        not overlap, on the handle's GPU."""
+        torch = _t()
+        dt = BF16 if t.dtype is torch.bfloat16 else _dtype_code(t)
+        if t.dim() != 2 or t.get_device() != self.device:
+            raise ValueError(f"{what}: not a matrix on the handle's GPU")
+        rows, width = t.shape
+        stride, one = t.stride()
+        if width < 1 or (width > 1 and one != 1) or (rows > 1 and stride < width):
+            raise ValueError(f"{what}: rows empty, not contiguous, or overlapping")
+        return dt, rows, width, stride if stride > width else width
+
+    def norm_quantize_rows(self, x, weight=None, eps=1e-6, residual=None, out=None, scale=None,
+                           out_residual=None, stream=None):
+        """x [rows, W] float32 or bfloat16, plus `residual` [rows, W] of its type (None:
+        nothing is added), normed by the root mean square (weight [W] float32 or
+        bfloat16, None: ones) -> (codes [rows, W] int8, scale [rows] float32) as
+        quantize_rows gives them, and with a residual the sum as the third: new, or
+        in `out_residual`, which may be x or residual itself."""
+        dt, rows, width, xs = self._matrix(x, "x")
+        torch = _torch
+        w_ptr, wdt = None, dt
+        if weight is not None:
+            wdt = _dtype_code(weight)
+            w_ptr = self._vector(weight, weight.dtype, "weight", width)
+        r_ptr, rs, h_ptr, hs = None, 0, None, 0
+        if residual is not None:
+            if residual.dtype is not x.dtype:
+                raise ValueError("residual: not of x's type")
+            r_ptr, rs = residual.data_ptr(), self._rows(residual, rows, width, "residual")
+            if out_residual is None:
+                out_residual, hs = _new_like(stream, x, rows, width), width
+            elif out_residual.dtype is not x.dtype:
+                raise ValueError("out_residual: not of x's type")
+            else:
+                hs = self._rows(out_residual, rows, width, "out_residual")
+            h_ptr = out_residual.data_ptr()
+        elif out_residual is not None:
+            raise ValueError("out_residual: there is no residual")
+        if out is None:
+            out = self._new_codes(stream, x.device, rows, width)
+            stride = width + -width % 128
+        elif out.dtype is not torch.int8:
+            raise ValueError("out: not int8")
+        else:
+            stride = self._rows(out, rows, width, "out")
+        if scale is None:
+            scale = _new(stream, x.device, torch.float32, rows)
+        else:
+            self._vector(scale, torch.float32, "scale", rows)
+        if rows:
+            _check(load_library().norm_quantize_rows(
+                self._h, x.data_ptr(), xs, r_ptr, rs, dt, w_ptr, wdt, eps, rows, width, h_ptr, hs,
+                out.data_ptr(), stride, scale.data_ptr(), _stream_on(self.device, stream)),
+                "norm_quantize_rows")
+        return (out, scale) if residual is None else (out, scale, out_residual)
+
+    def _tokens(self, tokens, rows):
+        """Pointer to tokens [rows] or [rows, n] int32, and n."""
+        n = tokens.shape[1] if tokens.dim() == 2 else 1
+        shape = (rows, n) if tokens.dim() == 2 else (rows,)
+        return self._vector(tokens, _torch.int32, "tokens", *shape), n
+
+    def token_logprobs(self, logits, tokens=None, top_k=0, temperature=1.0, entropy=True,
+                       norm=True, status=None, stream=None):
+        """Log probabilities under softmax(logits / temperature): logits [rows, V]
+        float32 or bfloat16, tokens [rows] or [rows, n] int32 (-1: padding, 0) or None
+        -> TokenLogprobs, with the entropy, the top_k likeliest ids and what
+        token_logprobs_grad takes (norm). ``status``: a preallocated [rows] int32
+        tensor, or None."""
+        dt, rows, vocab, stride = self._matrix(logits, "logits")
+        torch = _torch
+        f32 = torch.float32
+        o = _Logprobs()
+        t_ptr, n, lp = None, 0, None
+        if tokens is not None:
+            t_ptr, n = self._tokens(tokens, rows)
+        new = logits.new_empty if dt == F32 and stream is None else \
+            (lambda *shape: _new(stream, logits.device, f32, *shape))
+        if tokens is not None:
+            lp = new(*tokens.shape)
+            o.logprob = lp.data_ptr()
+        H = new(rows) if entropy else None
+        nz = new(rows, 2) if norm else None
+        ids = top = None
+        if top_k > 0:
+            top = new(rows, top_k)
+            ids = _new(stream, logits.device, torch.int32, rows, top_k)
+            o.top_ids, o.top_logprob = ids.data_ptr(), top.data_ptr()
+        if entropy:
+            o.entropy = H.data_ptr()
+        if norm:
+            o.norm = nz.data_ptr()
+        if status is not None:
+            o.status = self._vector(status, torch.int32, "status", rows)
+        if rows:
+            lib = load_library()
+            ws, need = self._workspace(lib.token_logprobs_workspace, stream, logits.device, dt,
+                                       rows, vocab, top_k)
+            _check(lib.token_logprobs(
+                self._h, logits.data_ptr(), dt, rows, vocab, stride, temperature, t_ptr, n, top_k,
+                ctypes.byref(o), None if ws is None else ws.data_ptr(), need,
+                _stream_on(self.device, stream)), "token_logprobs")
+        return TokenLogprobs(lp, H, ids, top, nz, status)
+
+    def _workspace(self, size, stream, device, *sizes):
+        """A call's own workspace of size(*sizes) bytes, from torch's allocator (calls on
+        several streams, and captured ones, each have theirs), and the bytes."""
+        need = size(*sizes)
+        if need <= 0:
+            return None, 0
+        return _new(stream, device, _torch.uint8, need), need
+
+    def token_logprobs_grad(self, logits, tokens, norm, grad_logprob, entropy=None,
+                            grad_entropy=None, temperature=1.0, out=None, stream=None):
+        """The gradient of token_logprobs by the logits: logits, tokens and temperature as
+        it took them, norm and entropy as it gave them, grad_logprob shaped as the
+        tokens and grad_entropy [rows] (None: nothing comes back to the entropy),
+        float32 -> [rows, V] of the logits' type, new or in `out`."""
+        dt, rows, vocab, stride = self._matrix(logits, "logits")
+        f32 = _torch.float32
+        t_ptr, n, g_ptr = None, 0, None
+        if tokens is not None:
+            t_ptr, n = self._tokens(tokens, rows)
+            if grad_logprob is None:
+                raise ValueError("grad_logprob: tokens without a gradient")
+            g_ptr = self._vector(grad_logprob, f32, "grad_logprob", *tokens.shape)
+        elif grad_logprob is not None:
+            raise ValueError("grad_logprob: there are no tokens")
+        n_ptr = self._vector(norm, f32, "norm", rows, 2)
+        h_ptr = ge_ptr = None
+        if grad_entropy is not None:
+            if entropy is None:
+                raise ValueError("entropy: needed for its gradient")
+            ge_ptr = self._vector(grad_entropy, f32, "grad_entropy", rows)
+            h_ptr = self._vector(entropy, f32, "entropy", rows)
+        out, out_stride = self._grad_out(logits, out, rows, vocab, stream)
+        if rows:
+            _check(load_library().token_logprobs_grad(
+                self._h, logits.data_ptr(), dt, rows, vocab, stride, temperature, t_ptr, n, n_ptr,
+                g_ptr, h_ptr, ge_ptr, out.data_ptr(), out_stride,
+                _stream_on(self.device, stream)), "token_logprobs_grad")
+        return out
+
+    def _grad_out(self, logits, out, rows, vocab, stream):
+        if out is None:
+            return _new_like(stream, logits, rows, vocab), vocab
+        if out.dtype is not logits.dtype:
+            raise ValueError("the gradient is not of the logits' type")
+        return out, self._rows(out, rows, vocab, "the gradient")
+
+    def distill_topk(self, logits, ids, teacher_logprob, temperature=1.0, tail=False,
+                     row_weight=None, grad=True, status=None, stream=None):
+        """Loss of the logits [rows, V] against a teacher's top tokens, ids [rows, k]
+        int32 and their log probabilities [rows, k] float32 (as token_logprobs gives
+        them at this temperature), and its gradient. ``tail``: the teacher's remaining
+        mass counts as one entry for all other ids; else the entries are
+        renormalised. ``row_weight`` [rows] float32 multiplies loss and gradient.
+        ``grad``: True (a new tensor), a tensor to hold it, or False. Returns (loss
+        [rows] float32, gradient [rows, V] of the logits' type, or None)."""
+        dt, rows, vocab, stride = self._matrix(logits, "logits")
+        f32 = _torch.float32
+        if ids.dim() != 2 or ids.shape[1] < 1:
+            raise ValueError("ids: not [rows, k]")
+        k = ids.shape[1]
+        i_ptr = self._vector(ids, _torch.int32, "ids", rows, k)
+        t_ptr = self._vector(teacher_logprob, f32, "teacher_logprob", rows, k)
+        w_ptr = None if row_weight is None else self._vector(row_weight, f32, "row_weight", rows)
+        s_ptr = None if status is None else self._vector(status, _torch.int32, "status", rows)
+        g_ptr, gs = None, 0
+        if grad is False or grad is None:
+            grad = None
+        else:
+            grad, gs = self._grad_out(logits, None if grad is True else grad, rows, vocab, stream)
+            g_ptr = grad.data_ptr()
+        loss = _new(stream, logits.device, f32, rows)
+        if rows:
+            lib = load_library()
+            ws, need = self._workspace(lib.distill_topk_workspace, stream, logits.device, dt,
+                                       rows, vocab, int(grad is not None))
+            _check(lib.distill_topk(
+                self._h, logits.data_ptr(), dt, rows, vocab, stride, temperature, i_ptr, t_ptr, k,
+                int(bool(tail)), w_ptr, loss.data_ptr(), g_ptr, gs, s_ptr,
+                None if ws is None else ws.data_ptr(), need, _stream_on(self.device, stream)),
+                "distill_topk")
+        return loss, grad
 
     def philox(self, counters, stream=None):
         """counters: [n, 4] int32/uint32 device tensor -> [n, 4] words (int32 view)."""

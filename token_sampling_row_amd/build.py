@@ -31,7 +31,7 @@ VERIFY_NCS = (1, 2, 4, 8, 16)               # must match kVerifyNcs
 VERIFY_WIDE_NCS = (24, 32, 38)              # must match kVerifyWideNcs
 DISPATCH = ["k_greedy.hip", "k_beam.hip", "k_sample_f32.hip", "k_sample_bf16.hip", "k_verify_f32.hip",
             "k_verify_bf16.hip", "k_misc.hip", "k_quant.hip", "k_int8_f32.hip", "k_int8_bf16.hip",
-            "k_vprobs.hip", "api.hip"]
+            "k_vprobs.hip", "k_norm.hip", "k_logprob.hip", "k_distill.hip", "api.hip"]
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", os.path.join(ROOT, "include"),
          # no packed fp32 instructions (v_pk_add/mul/fma_f32) anywhere
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

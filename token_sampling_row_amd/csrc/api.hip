@@ -148,6 +148,35 @@ int check_int8(tsr_handle h, const int8_t* codes, int64_t codes_stride, const fl
   return TSR_OK;
 }
 
+constexpr int kMaxScoreRows = (1 << 22) - 1;    // 256 threads a slice of a row, 64 slices at most
+constexpr int64_t kMaxScoreStride = 1ll << 36;   // rows times it, in bytes, within 2^63
+constexpr int kMaxScoreTokens = 1024;           // the gradient compares a row's tokens in pairs
+
+// Whether [a, a + n) and [b, b + m) have a byte in common.
+bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && n > 0 && m > 0 && x < y + (uintptr_t)m && y < x + (uintptr_t)n;
+}
+
+// Bytes from the first row's start to the last one's end.
+int64_t extent(int rows, int width, int64_t stride, int size) {
+  return rows > 0 ? ((int64_t)(rows - 1) * stride + width) * size : 0;
+}
+
+// Arguments of rows of logits that the scoring calls share. Strides times rows stay
+// within 64 bits.
+int check_scores(const void* logits, int dtype, int rows, int vocab, int64_t row_stride,
+                 double temperature) {
+  if (!logits) return TSR_EINVAL;
+  if (dtype != TSR_F32 && dtype != TSR_BF16) return TSR_EINVAL;
+  if (rows < 0 || vocab < 1 || row_stride < vocab || !elem_aligned(logits, dtype))
+    return TSR_EINVAL;
+  if (!isfinite(temperature) || temperature < kTemperatureMin) return TSR_EINVAL;
+  if (vocab > kMaxWideVocab || rows > kMaxScoreRows || row_stride >= kMaxScoreStride)
+    return TSR_EUNSUPPORTED;
+  return TSR_OK;
+}
+
 // Arguments every verify entry point checks (the handle's limits aside).
 int check_verify(const void* target_logits, const void* draft_logits, int dtype,
                  const int32_t* draft_tokens, int rows, int K, int vocab,
@@ -647,6 +676,210 @@ int verify_probs(tsr_handle h, const void* target_probs, int64_t target_seq_stri
                          draft_seq_stride, draft_row_stride, dtype, draft_tokens, draft_lens,
                          accept_u, draw_u, rows, K, vocab, out_tokens, out_accepted, out_status,
                          nullptr, 0, hip_stream);
+}
+
+int norm_quantize_rows(tsr_handle h, const void* x, int64_t x_stride, const void* residual,
+                       int64_t residual_stride, int dtype, const void* weight, int weight_dtype,
+                       double eps, int rows, int width, void* out_residual,
+                       int64_t out_residual_stride, int8_t* out_codes, int64_t codes_stride,
+                       float* out_scale, void* hip_stream) {
+  if (!h) return TSR_EINVAL;
+  const int rc = check_quantize(x, dtype, rows, width, x_stride, out_codes, codes_stride,
+                                out_scale);
+  if (rc != TSR_OK) return rc;
+  if (!isfinite(eps) || eps < 0.0) return TSR_EINVAL;
+  if (weight && ((weight_dtype != TSR_F32 && weight_dtype != TSR_BF16) ||
+                 !elem_aligned(weight, weight_dtype)))
+    return TSR_EINVAL;
+  if (residual && (residual_stride < width || !elem_aligned(residual, dtype))) return TSR_EINVAL;
+  if (out_residual && (!residual || out_residual_stride < width ||
+                       !elem_aligned(out_residual, dtype)))
+    return TSR_EINVAL;
+  if (x_stride >= kMaxScoreStride || codes_stride >= kMaxScoreStride ||
+      (residual && residual_stride >= kMaxScoreStride) ||
+      (out_residual && out_residual_stride >= kMaxScoreStride))
+    return TSR_EUNSUPPORTED;
+  if (rows == 0) return TSR_OK;
+  const int es = esize(dtype);
+  const int64_t nx = extent(rows, width, x_stride, es);
+  const int64_t nr = residual ? extent(rows, width, residual_stride, es) : 0;
+  const int64_t nh = out_residual ? extent(rows, width, out_residual_stride, es) : 0;
+  const int64_t nq = extent(rows, width, codes_stride, 1);
+  const int64_t nw = weight ? (int64_t)width * esize(weight_dtype) : 0, ns = (int64_t)rows * 4;
+  // the sum may take the place of x or of the residual, row for row
+  const bool on_x = out_residual == x && (rows == 1 || out_residual_stride == x_stride);
+  const bool on_r =
+      out_residual == residual && (rows == 1 || out_residual_stride == residual_stride);
+  if ((!on_x && overlap(out_residual, nh, x, nx)) ||
+      (!on_r && overlap(out_residual, nh, residual, nr)) ||
+      overlap(out_residual, nh, weight, nw) || overlap(out_residual, nh, out_scale, ns))
+    return TSR_EINVAL;
+  if (overlap(out_codes, nq, x, nx) || overlap(out_codes, nq, residual, nr) ||
+      overlap(out_codes, nq, out_residual, nh) || overlap(out_codes, nq, weight, nw) ||
+      overlap(out_codes, nq, out_scale, ns))
+    return TSR_EINVAL;
+  if (overlap(out_scale, ns, x, nx) || overlap(out_scale, ns, residual, nr) ||
+      overlap(out_scale, ns, weight, nw))
+    return TSR_EINVAL;
+  tsr::NormArgs a{};
+  a.x = static_cast<const unsigned char*>(x);
+  a.x_stride = (long long)x_stride * es;
+  a.residual = static_cast<const unsigned char*>(residual);
+  a.r_stride = (long long)residual_stride * es;
+  a.weight = static_cast<const unsigned char*>(weight);
+  a.eps = eps;
+  a.rows = rows;
+  a.width = width;
+  a.out_h = static_cast<unsigned char*>(out_residual);
+  a.h_stride = (long long)out_residual_stride * es;
+  a.codes = out_codes;
+  a.q_stride = (long long)codes_stride;
+  a.scale = out_scale;
+  return on_device(h->device, [&]() -> int {
+    const hipError_t e =
+        tsr::launch_norm_quantize(a, dtype, weight ? weight_dtype : dtype, (hipStream_t)hip_stream);
+    return e == hipSuccess ? TSR_OK : TSR_EDEVICE;
+  });
+}
+
+int token_logprobs_workspace(int dtype, int rows, int vocab, int top_k) {
+  if ((dtype != TSR_F32 && dtype != TSR_BF16) || rows < 1 || vocab < 1 || top_k < 0 ||
+      top_k > tsr::kMaxTop || rows > kMaxScoreRows || vocab > kMaxWideVocab)
+    return 0;
+  return (int)tsr::logprobs_ws_bytes(dtype, rows, vocab, top_k);
+}
+
+int token_logprobs(tsr_handle h, const void* logits, int dtype, int rows, int vocab,
+                   int64_t row_stride, double temperature, const int32_t* tokens, int n_tokens,
+                   int top_k, const tsr_logprobs* out, void* workspace, int64_t workspace_bytes,
+                   void* hip_stream) {
+  if (!h || !out) return TSR_EINVAL;
+  const int rc = check_scores(logits, dtype, rows, vocab, row_stride, temperature);
+  if (rc != TSR_OK) return rc;
+  if (n_tokens < 0 || top_k < 0 || (n_tokens > 0 && (!tokens || !out->logprob)) ||
+      (top_k > 0 && (!out->top_ids || !out->top_logprob)))
+    return TSR_EINVAL;
+  if (!word_aligned(tokens) || !word_aligned(out->logprob) || !word_aligned(out->entropy) ||
+      !word_aligned(out->top_ids) || !word_aligned(out->top_logprob) ||
+      !word_aligned(out->norm) || !word_aligned(out->status))
+    return TSR_EINVAL;
+  if (n_tokens > kMaxScoreTokens || top_k > tsr::kMaxTop) return TSR_EUNSUPPORTED;
+  if (rows == 0) return TSR_OK;
+  const int64_t need = (int64_t)tsr::logprobs_ws_bytes(dtype, rows, vocab, top_k);
+  if (need && (!workspace || ((uintptr_t)workspace % 16) != 0 || workspace_bytes < need))
+    return TSR_EINVAL;
+  tsr::LogprobArgs a{};
+  a.logits = static_cast<const unsigned char*>(logits);
+  a.stride_bytes = (long long)row_stride * esize(dtype);
+  a.rows = rows;
+  a.V = vocab;
+  a.c = (float)(1.4426950408889634 / temperature);
+  a.inv_t = 1.0 / temperature;
+  a.tokens = tokens;
+  a.n = n_tokens;
+  a.k = top_k;
+  a.logprob = out->logprob;
+  a.entropy = out->entropy;
+  a.top_ids = out->top_ids;
+  a.top_logprob = out->top_logprob;
+  a.norm = out->norm;
+  a.status = out->status;
+  return on_device(h->device, [&]() -> int {
+    const hipError_t e = tsr::launch_logprobs(a, dtype, workspace, (hipStream_t)hip_stream);
+    return e == hipSuccess ? TSR_OK : TSR_EDEVICE;
+  });
+}
+
+int token_logprobs_grad(tsr_handle h, const void* logits, int dtype, int rows, int vocab,
+                        int64_t row_stride, double temperature, const int32_t* tokens,
+                        int n_tokens, const float* norm, const float* grad_logprob,
+                        const float* entropy, const float* grad_entropy, void* out_grad,
+                        int64_t grad_stride, void* hip_stream) {
+  if (!h) return TSR_EINVAL;
+  const int rc = check_scores(logits, dtype, rows, vocab, row_stride, temperature);
+  if (rc != TSR_OK) return rc;
+  if (!norm || !out_grad || n_tokens < 0 || (n_tokens > 0 && (!tokens || !grad_logprob)) ||
+      (grad_entropy && !entropy) || grad_stride < vocab || !elem_aligned(out_grad, dtype))
+    return TSR_EINVAL;
+  if (!word_aligned(tokens) || !word_aligned(norm) || !word_aligned(grad_logprob) ||
+      !word_aligned(entropy) || !word_aligned(grad_entropy))
+    return TSR_EINVAL;
+  if (n_tokens > kMaxScoreTokens || grad_stride >= kMaxScoreStride) return TSR_EUNSUPPORTED;
+  if (rows == 0) return TSR_OK;
+  // the logits are read again where the tokens are: the gradient has memory of its own
+  if (overlap(out_grad, extent(rows, vocab, grad_stride, esize(dtype)), logits,
+              extent(rows, vocab, row_stride, esize(dtype))))
+    return TSR_EINVAL;
+  tsr::LogprobGradArgs a{};
+  a.logits = static_cast<const unsigned char*>(logits);
+  a.stride_bytes = (long long)row_stride * esize(dtype);
+  a.rows = rows;
+  a.V = vocab;
+  a.c = (float)(1.4426950408889634 / temperature);
+  a.inv_t = (float)(1.0 / temperature);
+  a.tokens = tokens;
+  a.n = n_tokens;
+  a.norm = norm;
+  a.g = grad_logprob;
+  a.entropy = entropy;
+  a.ge = grad_entropy;
+  a.out = static_cast<unsigned char*>(out_grad);
+  a.out_stride_bytes = (long long)grad_stride * esize(dtype);
+  return on_device(h->device, [&]() -> int {
+    const hipError_t e = tsr::launch_logprobs_grad(a, dtype, (hipStream_t)hip_stream);
+    return e == hipSuccess ? TSR_OK : TSR_EDEVICE;
+  });
+}
+
+int distill_topk_workspace(int dtype, int rows, int vocab, int want_grad) {
+  if ((dtype != TSR_F32 && dtype != TSR_BF16) || rows < 1 || vocab < 1 || rows > kMaxScoreRows ||
+      vocab > kMaxWideVocab)
+    return 0;
+  return (int)tsr::distill_ws_bytes(dtype, rows, vocab, want_grad != 0);
+}
+
+int distill_topk(tsr_handle h, const void* logits, int dtype, int rows, int vocab,
+                 int64_t row_stride, double temperature, const int32_t* ids,
+                 const float* teacher_logprob, int k, int tail, const float* row_weight,
+                 float* out_loss, void* out_grad, int64_t grad_stride, int32_t* out_status,
+                 void* workspace, int64_t workspace_bytes, void* hip_stream) {
+  if (!h) return TSR_EINVAL;
+  const int rc = check_scores(logits, dtype, rows, vocab, row_stride, temperature);
+  if (rc != TSR_OK) return rc;
+  if (!ids || !teacher_logprob || !out_loss || k < 1 || (tail != 0 && tail != 1)) return TSR_EINVAL;
+  if (out_grad && (grad_stride < vocab || !elem_aligned(out_grad, dtype))) return TSR_EINVAL;
+  if (!word_aligned(ids) || !word_aligned(teacher_logprob) || !word_aligned(row_weight) ||
+      !word_aligned(out_loss) || !word_aligned(out_status))
+    return TSR_EINVAL;
+  if (k > tsr::kMaxTop || (out_grad && grad_stride >= kMaxScoreStride)) return TSR_EUNSUPPORTED;
+  if (rows == 0) return TSR_OK;
+  // the logits are read more than once: the gradient has memory of its own
+  if (out_grad && overlap(out_grad, extent(rows, vocab, grad_stride, esize(dtype)), logits,
+                          extent(rows, vocab, row_stride, esize(dtype))))
+    return TSR_EINVAL;
+  const int64_t need = (int64_t)tsr::distill_ws_bytes(dtype, rows, vocab, out_grad != nullptr);
+  if (need && (!workspace || ((uintptr_t)workspace % 16) != 0 || workspace_bytes < need))
+    return TSR_EINVAL;
+  tsr::DistillArgs a{};
+  a.logits = static_cast<const unsigned char*>(logits);
+  a.stride_bytes = (long long)row_stride * esize(dtype);
+  a.rows = rows;
+  a.V = vocab;
+  a.c = (float)(1.4426950408889634 / temperature);
+  a.inv_t = 1.0 / temperature;
+  a.ids = ids;
+  a.teacher = teacher_logprob;
+  a.k = k;
+  a.tail = tail;
+  a.weight = row_weight;
+  a.loss = out_loss;
+  a.grad = static_cast<unsigned char*>(out_grad);
+  a.grad_stride_bytes = (long long)grad_stride * esize(dtype);
+  a.status = out_status;
+  return on_device(h->device, [&]() -> int {
+    const hipError_t e = tsr::launch_distill(a, dtype, workspace, (hipStream_t)hip_stream);
+    return e == hipSuccess ? TSR_OK : TSR_EDEVICE;
+  });
 }
 
 int sampler_philox(tsr_handle h, const uint32_t* counters, int n, uint32_t* out_words,

@@ -183,6 +183,80 @@ size_t vprobs_ws_bytes(int dtype, int rows, int vocab);
 size_t vprobs_ws_most(int rows, int vocab);
 hipError_t launch_vprobs(const VprobsArgs& a, int dtype, void* ws, hipStream_t s);
 
+// norm_quantize_rows: h = x + residual, codes and scales of its RMS norm. Strides in bytes.
+struct NormArgs {
+  const unsigned char* x;
+  long long x_stride;
+  const unsigned char* residual;   // null: h = x
+  long long r_stride;
+  const unsigned char* weight;     // null: ones
+  double eps;
+  int rows, width;
+  unsigned char* out_h;            // null: h is not kept
+  long long h_stride;
+  int8_t* codes;
+  long long q_stride;
+  float* scale;
+};
+hipError_t launch_norm_quantize(const NormArgs& a, int dtype, int weight_dtype, hipStream_t s);
+
+// token_logprobs; every output may be null.
+struct LogprobArgs {
+  const unsigned char* logits;
+  long long stride_bytes;
+  int rows, V;
+  float c;                  // log2(e) / T
+  double inv_t;             // 1 / T
+  const int32_t* tokens;    // [rows][n]
+  int n, k;
+  float* logprob;           // [rows][n]
+  float* entropy;           // [rows]
+  int32_t* top_ids;         // [rows][k]
+  float* top_logprob;       // [rows][k]
+  float* norm;              // [rows][2]
+  int32_t* status;          // [rows]
+};
+constexpr int kMaxTop = 64;   // most alternatives of a row, most teacher entries of one
+hipError_t launch_logprobs(const LogprobArgs& a, int dtype, void* ws, hipStream_t s);
+size_t logprobs_ws_bytes(int dtype, int rows, int vocab, int k);
+
+// token_logprobs_grad.
+struct LogprobGradArgs {
+  const unsigned char* logits;
+  long long stride_bytes;
+  int rows, V;
+  float c;
+  float inv_t;
+  const int32_t* tokens;    // [rows][n]
+  int n;
+  const float* norm;        // [rows][2]
+  const float* g;           // [rows][n]
+  const float* entropy;     // [rows], null where ge is
+  const float* ge;          // [rows], null: no gradient of the entropy
+  unsigned char* out;
+  long long out_stride_bytes;
+};
+hipError_t launch_logprobs_grad(const LogprobGradArgs& a, int dtype, hipStream_t s);
+
+// distill_topk.
+struct DistillArgs {
+  const unsigned char* logits;
+  long long stride_bytes;
+  int rows, V;
+  float c;
+  double inv_t;
+  const int32_t* ids;       // [rows][k]
+  const float* teacher;     // [rows][k]
+  int k, tail;
+  const float* weight;      // [rows], null: 1 each
+  float* loss;              // [rows]
+  unsigned char* grad;      // null: no gradient
+  long long grad_stride_bytes;
+  int32_t* status;          // [rows], may be null
+};
+hipError_t launch_distill(const DistillArgs& a, int dtype, void* ws, hipStream_t s);
+size_t distill_ws_bytes(int dtype, int rows, int vocab, int grad);
+
 hipError_t launch_philox(const uint32_t* ctr, int n, uint32_t k0, uint32_t k1, uint32_t* out,
                          hipStream_t s);
 

@@ -1,0 +1,79 @@
+// What the kernels around the logits share (token_logprobs, distill_topk):
+// weights of logits against a row's largest, log probabilities, keys of the
+// likeliest ids, and the gradient p_j (A + B x_j) with its stores.
+#pragma once
+
+#include "device_common.hpp"
+
+namespace tsr {
+
+constexpr double kLn2 = 0.6931471805599453;
+
+// (v - M) log2(e) / T. Held above -2000, where the weight 2^x is 0 anyway, so
+// that a logit of -inf gives products of 0 and not NaN.
+__device__ __forceinline__ float exponent(float v, float M, float c) {
+  return fmaxf((v - M) * c, -2000.0f);
+}
+
+// log p of a logit v: (v - M) / T - log Z, formed in 64 bits and rounded once.
+__device__ __forceinline__ float log_prob(float v, float M, double Z, double inv_t) {
+  return (float)(((double)v - (double)M) * inv_t - log(Z));
+}
+
+// Keys of ids that order as (value, then the lower id) do; 0 is below all of them.
+__device__ __forceinline__ unsigned long long top_key(float v, int id) {
+  return ((unsigned long long)fkey(v) << 32) | (0xFFFFFFFFu - (uint32_t)id);
+}
+__device__ __forceinline__ int top_id(unsigned long long key) {
+  return (int)(0xFFFFFFFFu - (uint32_t)key);
+}
+__device__ __forceinline__ float top_value(unsigned long long key) {
+  return key2f((uint32_t)(key >> 32));
+}
+
+// One element of a row's gradient: e (A + B x), e = 2^x, x = (z - M) log2(e) / T.
+struct GradRow {
+  float M, c, A, B;
+  __device__ __forceinline__ float at(float z) const {
+    const float x = exponent(z, M, c);
+    return __builtin_amdgcn_exp2f(x) * fmaf(B, x, A);
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ void store_elem(unsigned char* row, long long i, float v) {
+  if constexpr (DT == 0)
+    *reinterpret_cast<float*>(row + i * 4) = v;
+  else
+    *reinterpret_cast<uint16_t*>(row + i * 2) = __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// The workgroup's largest value, NaN where there is one.
+template <int BLOCK>
+__device__ __forceinline__ float block_maxn(float v, BlockScratch& s) {
+  constexpr int W = BLOCK / kWave;
+  v = wave_maxn(v);
+  __syncthreads();
+  if (__lane_id() == 0) s.f[threadIdx.x / kWave] = v;
+  __syncthreads();
+  float r = s.f[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) r = fmaxn(r, s.f[w]);
+  return r;
+}
+
+template <int BLOCK>
+__device__ __forceinline__ unsigned long long block_max_u64(unsigned long long v,
+                                                            BlockScratch& s) {
+  constexpr int W = BLOCK / kWave;
+  v = wave_reduce(v, [](unsigned long long a, unsigned long long b) { return a > b ? a : b; });
+  __syncthreads();
+  if (__lane_id() == 0) s.q[threadIdx.x / kWave] = v;
+  __syncthreads();
+  unsigned long long r = s.q[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) r = s.q[w] > r ? s.q[w] : r;
+  return r;
+}
+
+}  // namespace tsr
