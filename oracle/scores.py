@@ -141,6 +141,9 @@ def logprobs_grad(z, tokens, norm, g, T=1.0, H=0.0, ge=0.0, dtype="f32"):
     size = p * (abs(G) + abs(ge) * (np.abs(logp) + 2 * np.log(Z) + abs(H)))
     ax = np.where(p > 0, np.abs(np.where(np.isfinite(x), x, 0.0)), 0.0)
     off = size * (2.1 * ax + 12.0) * U
+    # an exponent may be formed as z c - fl(M c), with what the rounding of M c leaves, at
+    # most u |M c|, put back through a factor that is itself rounded (twice, u each)
+    off += p * abs(ge) * 4 * U * U * abs(M / T / LN2)
     for t, gi in real:
         out[t] += gi
         off[t] += abs(gi) * (len(real) + 2) * U   # their sum in float32, one fma

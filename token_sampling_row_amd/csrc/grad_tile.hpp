@@ -1,0 +1,88 @@
+// A row's gradient p (A + B x), written in tiles (token_logprobs_grad, distill_topk).
+//
+// Bound by memory: each logit is read once and each element written once.
+#pragma once
+
+#include "row_slice.hpp"
+
+namespace tsr {
+
+constexpr int kTileChunks = 4;   // 16-byte chunks a thread
+template <int DT>
+constexpr int kTileIds = kSliceBlock * kTileChunks * Fmt<DT>::EPC;
+
+template <int DT>
+__device__ __forceinline__ uint4 pack(const float* v) {
+  if constexpr (DT == 0)
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  else
+    return make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                      bf16_pair(v[6], v[7]));
+}
+
+template <bool ONCE>
+__device__ __forceinline__ void store16(void* p, uint4 v) {
+  if constexpr (ONCE) {
+    store16_once(p, v);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    store_words<4>(p, w);
+  }
+}
+
+// Ids [tile * kTileIds, ...) of a row of V. ONCE: written past the caches.
+template <int DT, bool ONCE>
+__device__ __forceinline__ void put_tile(const unsigned char* row, unsigned char* out, int V,
+                                         int tile, const GradRow& g) {
+  constexpr int EPC = Fmt<DT>::EPC;
+  const int whole = V / EPC;
+  const int first = tile * kSliceBlock * kTileChunks + (int)threadIdx.x;
+  uint4 c[kTileChunks];
+#pragma unroll
+  for (int j = 0; j < kTileChunks; ++j)   // chunks past the last whole one repeat it
+    c[j] = whole ? load16(row + (long long)min(first + j * kSliceBlock, whole - 1) * 16)
+                 : make_uint4(0, 0, 0, 0);
+  const auto all = [&](auto&& of) {
+#pragma unroll
+    for (int j = 0; j < kTileChunks; ++j) {
+      float v[EPC];
+      unpack<DT>(c[j], v);
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) v[e] = of(v[e]);
+      const int i = first + j * kSliceBlock;
+      if (i < whole) store16<ONCE>(out + (long long)i * 16, pack<DT>(v));
+    }
+  };
+  if (g.plain)
+    all([&](float z) { return g.of<true, true>(z); });
+  else if (g.B != 0.0f)
+    all([&](float z) { return g.of<true, false>(z); });
+  else
+    all([&](float z) { return g.of<false, false>(z); });
+  // the elements behind the last whole chunk, with the tile that they lie in
+  const int at = whole * EPC;
+  if (at < V && at / kTileIds<DT> == tile && (int)threadIdx.x < V - at)
+    store_elem<DT>(out, at + (int)threadIdx.x, g.at(load_elem<DT>(row, at + (int)threadIdx.x)));
+}
+
+template <int DT>
+__device__ __forceinline__ void zero_tile(unsigned char* out, int V, int tile) {
+  constexpr int EPC = Fmt<DT>::EPC;
+  const int whole = V / EPC;
+#pragma unroll
+  for (int j = 0; j < kTileChunks; ++j) {
+    const int i = (tile * kTileChunks + j) * kSliceBlock + (int)threadIdx.x;
+    if (i < whole) store16<false>(out + (long long)i * 16, make_uint4(0, 0, 0, 0));
+  }
+  const int at = whole * EPC;
+  if (at < V && at / kTileIds<DT> == tile && (int)threadIdx.x < V - at)
+    store_elem<DT>(out, at + (int)threadIdx.x, 0.0f);
+}
+
+template <int DT>
+int tiles_of(int V) {
+  return (int)(((long long)V + kTileIds<DT> - 1) / kTileIds<DT>);
+}
+
+}  // namespace tsr

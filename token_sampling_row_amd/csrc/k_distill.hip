@@ -133,11 +133,9 @@ __global__ __launch_bounds__(kDtBlock) void distill_kernel(DistillArgs a) {
   if (!out) return;
   const double each = weight * a.inv_t;
   const double whole = e.sum + e.rest;
-  GradRow p;
-  p.M = Mr;
-  p.c = a.c;
-  p.A = status ? nan : Zr > 0.0 ? (float)(each * (whole * f / Z - e.rest / Zr)) : 0.0f;
-  p.B = 0.0f;
+  const GradRow p(Mr, a.c,
+                  status ? (double)nan : Zr > 0.0 ? each * (whole * f / Z - e.rest / Zr) : 0.0,
+                  0.0);
   for (int i = threadIdx.x; i < a.V; i += kDtBlock)
     store_elem<DT>(out, i, p.at(load_elem<DT>(row, i)));
   __syncthreads();

@@ -5,18 +5,282 @@
 //   x_j = (z_j - M) / T, M = max z, Z = sum_j exp(x_j), log p_j = x_j - log Z
 //   H = log Z - sum_j exp(x_j) x_j / Z   (both terms >= 0: nothing cancels)
 //   dL/dz_j = (sum_i g_i [t_i = j] - p_j (sum_i g_i + gH (log p_j + H))) / T
-#include "kernels.hpp"
-#include "scores.hpp"
-#include "wide_mem.hpp"
+#include <algorithm>
+#include <type_traits>
+
+#include "grad_tile.hpp"
 
 namespace tsr {
 namespace {
 
 constexpr int kLpBlock = 256;
 
-// One workgroup to a row.
+// ------------------------------------------------------------ the likeliest ids
+// Keys of ids that may be among the k largest, in a region of LDS for each wavefront.
+template <int REGION>
+struct Candidates {
+  unsigned long long key[kSliceWaves][REGION];
+  int n[kSliceWaves];
+};
+constexpr int kSliceRegion = 128;   // keys of a wavefront in a slice
+constexpr int kJoinRegion = 512;    // and of one that joins slices
+
+// put(rank, key) for each candidate that fewer than k exceed. Keys differ, so ranks do.
+template <int REGION, class F>
+__device__ __forceinline__ void rank_candidates(const Candidates<REGION>& c, int k, F&& put) {
+  int n[kSliceWaves], total = 0;
+#pragma unroll
+  for (int w = 0; w < kSliceWaves; ++w) total += n[w] = c.n[w];
+  for (int i = threadIdx.x; i < total; i += kSliceBlock) {
+    int w = 0, at = i;
+    while (at >= n[w]) at -= n[w++];
+    const unsigned long long mine = c.key[w][at];
+    int rank = 0;
+#pragma unroll
+    for (int v = 0; v < kSliceWaves; ++v)
+#pragma unroll 4
+      for (int q = 0; q < n[v]; ++q) rank += c.key[v][q] > mine;
+    if (rank < k) put(rank, mine);
+  }
+}
+
+// The slice's candidates. `tau`: the k largest of the slice are at least that (keys of
+// values). Every wavefront has seen j = ceil(k / 4) threads whose largest logit is at
+// least tau, so there are k such elements; there are few more.
+template <int DT, int NC>
+__device__ __forceinline__ void gather(const Slice<DT, NC>& s, int V, uint32_t tau, int k,
+                                       Candidates<kSliceRegion>& c, BlockScratch& scratch) {
+  constexpr int EPC = Fmt<DT>::EPC;
+  const int wave = threadIdx.x / kWave;
+  const float least = key2f(tau);
+  int n = 0;
+  s.each(V, [&](const float* v, int id) {
+    if (!__any(max_of<DT>(v) >= least)) return;
+#pragma unroll
+    for (int e = 0; e < EPC; ++e) {
+      const bool in = v[e] >= least && v[e] > kNegInf;
+      const unsigned long long who = __ballot(in);
+      const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+                                                   __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+      if (in && at < kSliceRegion) c.key[wave][at] = top_key(v[e], id + e);
+      n += __popcll(who);
+    }
+  });
+  if (__lane_id() == 0) c.n[wave] = n;
+  __syncthreads();
+  int most = 0;
+#pragma unroll
+  for (int w = 0; w < kSliceWaves; ++w) most = max(most, c.n[w]);
+  if (most <= kSliceRegion) return;
+  // Too many (equal logits, or the largest with few threads): one at a time. Each thread
+  // keeps its largest key below those taken, and looks for its next when it is taken.
+  __syncthreads();
+  unsigned long long best = 0, last = ~0ull;
+  int taken = 0;
+  for (int i = 0; i < k; ++i) {
+    if (best == 0 && last != 0) {
+      s.each_again(V, [&](const float* v, int id) {
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) {
+          const unsigned long long key = top_key(v[e], id + e);
+          if (v[e] > kNegInf && key < last && key > best) best = key;
+        }
+      });
+      if (best == 0) last = 0;   // none is left with this thread
+    }
+    const unsigned long long top = block_max_u64<kSliceBlock>(best, scratch);
+    if (top == 0) break;
+    if (threadIdx.x == 0) c.key[0][i] = top;
+    ++taken;
+    if (best == top) {
+      last = top;
+      best = 0;
+    }
+  }
+  if (threadIdx.x < kSliceWaves) c.n[threadIdx.x] = threadIdx.x == 0 ? taken : 0;
+  __syncthreads();
+}
+
+// ------------------------------------------------------------ a row's outputs
+__device__ __forceinline__ int row_status(float M) {
+  return M == kNegInf ? 2 : !(M < kPosInf) ? 1 : 0;
+}
+
+// Everything of row r but its alternatives, by T threads. Every thread of the wavefronts
+// that call this has the row's sums.
+template <int DT, int T>
+__device__ __forceinline__ void put_row(const LogprobArgs& a, long long r, const Sums& all,
+                                        double logZ, int t) {
+  const unsigned char* row = a.logits + r * a.stride_bytes;
+  const int status = row_status(all.M);
+  const float nan = __uint_as_float(0x7FC00000u);
+  bool bad = false;
+  for (int i = t; i < a.n; i += T) {
+    const int id = a.tokens[r * a.n + i];
+    float lp = 0.0f;
+    if (id != -1) {
+      const bool in = id >= 0 && id < a.V;
+      bad |= !in;
+      lp = in && !status ? log_prob(load_elem<DT>(row, id), all.M, logZ, a.inv_t) : nan;
+    }
+    a.logprob[r * a.n + i] = lp;
+  }
+  const bool any_bad = __any(bad);
+  if (t == 0) {
+    if (a.entropy) a.entropy[r] = status ? nan : (float)(logZ - all.S / all.Z * kLn2);
+    if (a.norm) {
+      a.norm[2 * r] = status ? nan : all.M;
+      a.norm[2 * r + 1] = status ? nan : (float)all.Z;
+    }
+    if (a.status) a.status[r] = status ? status : any_bad ? 3 : 0;
+  }
+}
+
+// The k alternatives from the candidates.
+template <int REGION>
+__device__ __forceinline__ void put_top(const LogprobArgs& a, long long r, const Sums& all,
+                                        double logZ, const Candidates<REGION>& c) {
+  const int status = row_status(all.M);
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kSliceWaves; ++w) total += c.n[w];
+  if (status) total = 0;
+  for (int i = total + threadIdx.x; i < a.k; i += kSliceBlock) {   // positions past the last
+    a.top_ids[r * a.k + i] = -1;
+    a.top_logprob[r * a.k + i] = status ? __uint_as_float(0x7FC00000u) : kNegInf;
+  }
+  if (status) return;
+  rank_candidates(c, a.k, [&](int rank, unsigned long long key) {
+    a.top_ids[r * a.k + rank] = top_id(key);
+    a.top_logprob[r * a.k + rank] = log_prob(top_value(key), all.M, logZ, a.inv_t);
+  });
+}
+
+// Workspace: each slice's sums, then each slice's k largest keys, largest first.
+struct LpWs {
+  Sums* sums;                  // [rows][slices]
+  unsigned long long* keys;    // [rows][slices][k]
+};
+
+// One workgroup to a slice of a row; with one slice it is the whole row's.
+template <int DT, int NC, bool TOP, bool ONCE>
+__global__ __launch_bounds__(kSliceBlock) void logprob_slice_kernel(LogprobArgs a, Cut cut,
+                                                                    LpWs ws) {
+  __shared__ Sums each[kSliceWaves];
+  __shared__ uint32_t bound[kSliceWaves];
+  __shared__ typename std::conditional<TOP, Candidates<kSliceRegion>, int>::type cands;
+  __shared__ typename std::conditional<TOP, BlockScratch, int>::type scratch;
+  const int slice = blockIdx.x % cut.slices;
+  const long long r = blockIdx.x / cut.slices;
+  Slice<DT, NC> s;
+  s.template load<ONCE>(a.logits + r * a.stride_bytes, a.V, slice, cut);
+  const float m = s.largest(a.V);
+  if constexpr (TOP) {
+    const int j = (a.k + kSliceWaves - 1) / kSliceWaves;   // at most 16
+    const uint32_t sorted = wave_sort_desc<64>(fkey(m));
+    const uint32_t jth = readlane_u32(sorted, j - 1);
+    if (__lane_id() == 0) bound[threadIdx.x / kWave] = jth;
+  }
+  float off;
+  const Sums mine = s.sums(a.V, m, a.c, off);
+  const Sums all = join_block(mine, a.c, off, each);
+  if constexpr (TOP) {
+    uint32_t tau = bound[0];
+#pragma unroll
+    for (int w = 1; w < kSliceWaves; ++w) tau = min(tau, bound[w]);
+    if (all.M == all.M)
+      gather(s, a.V, tau, a.k, cands, scratch);
+    else if (threadIdx.x < kSliceWaves)
+      cands.n[threadIdx.x] = 0;
+  }
+  if (cut.slices == 1) {
+    const double logZ = log(all.Z);
+    if (threadIdx.x < kWave) put_row<DT, kWave>(a, r, all, logZ, threadIdx.x);
+    if constexpr (TOP) {
+      __syncthreads();
+      put_top(a, r, all, logZ, cands);
+    }
+    return;
+  }
+  const long long at = r * cut.slices + slice;
+  if (threadIdx.x == 0) ws.sums[at] = all;
+  if constexpr (TOP) {
+    __syncthreads();
+    unsigned long long* keys = ws.keys + at * a.k;
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kSliceWaves; ++w) total += cands.n[w];
+    for (int i = total + threadIdx.x; i < a.k; i += kSliceBlock) keys[i] = 0;
+    rank_candidates(cands, a.k, [&](int rank, unsigned long long key) { keys[rank] = key; });
+  }
+}
+
+// The sums of a row from its slices', by each wavefront for itself (64 slices at most).
+__device__ __forceinline__ Sums join_slices(const Sums* sums, int slices, float c) {
+  const int lane = __lane_id();
+  Sums one{kNegInf, 0.0, 0.0};
+  if (lane < slices) one = sums[lane];
+  rebase(one, wave_maxn(one.M), c, 0.0f);
+  one.Z = wave_sum(one.Z);
+  one.S = wave_sum(one.S);
+  return one;
+}
+
+// Without alternatives: one wavefront to a row.
 template <int DT>
-__global__ __launch_bounds__(kLpBlock) void logprob_kernel(LogprobArgs a) {
+__global__ __launch_bounds__(kSliceBlock) void logprob_join_kernel(LogprobArgs a, int slices,
+                                                                   LpWs ws) {
+  const long long r = (long long)blockIdx.x * kSliceWaves + threadIdx.x / kWave;
+  if (r >= a.rows) return;
+  const Sums all = join_slices(ws.sums + r * slices, slices, a.c);
+  put_row<DT, kWave>(a, r, all, log(all.Z), __lane_id());
+}
+
+// With alternatives: one workgroup to a row. Each slice's j = ceil(k / slices) largest
+// are k ids together, so the smallest of the slices' j-th keys bounds the k largest.
+template <int DT>
+__global__ __launch_bounds__(kSliceBlock) void logprob_top_join_kernel(LogprobArgs a, int slices,
+                                                                       LpWs ws) {
+  __shared__ Candidates<kJoinRegion> cands;
+  constexpr int EACH = kJoinRegion / kWave;   // keys to a thread
+  const long long r = blockIdx.x;
+  const int lane = __lane_id(), wave = threadIdx.x / kWave;
+  const unsigned long long* keys = ws.keys + r * slices * a.k;
+  const int j = (a.k + slices - 1) / slices;
+  unsigned long long tau = ~0ull;
+  if (lane < slices) tau = keys[lane * a.k + j - 1];
+  unsigned long long mine[EACH];
+  const int total = slices * a.k;
+#pragma unroll
+  for (int q = 0; q < EACH; ++q) {
+    const int i = q * kSliceBlock + (int)threadIdx.x;
+    mine[q] = i < total ? keys[i] : 0;
+  }
+  const Sums all = join_slices(ws.sums + r * slices, slices, a.c);
+  const double logZ = log(all.Z);
+  tau = wave_reduce(tau, [](unsigned long long x, unsigned long long y) { return x < y ? x : y; });
+  int n = 0;
+#pragma unroll
+  for (int q = 0; q < EACH; ++q) {
+    const bool in = mine[q] != 0 && mine[q] >= tau;
+    const unsigned long long who = __ballot(in);
+    if (in)
+      cands.key[wave][n + __builtin_amdgcn_mbcnt_hi(
+                              (uint32_t)(who >> 32),
+                              __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0))] = mine[q];
+    n += __popcll(who);
+  }
+  if (lane == 0) cands.n[wave] = n;
+  if (wave == kSliceWaves - 1) put_row<DT, kWave>(a, r, all, logZ, lane);
+  __syncthreads();
+  put_top(a, r, all, logZ, cands);
+}
+
+// ------------------------------------------------------------ rows past the slices
+// Vocabularies that 64 slices do not hold (over 2^20 float32 or 2^21 bf16 ids): one
+// workgroup to a row, which it reads once for each sum and each alternative.
+template <int DT>
+__global__ __launch_bounds__(kLpBlock) void logprob_wide_kernel(LogprobArgs a) {
   __shared__ BlockScratch scratch;
   const long long r = blockIdx.x;
   const unsigned char* row = a.logits + r * a.stride_bytes;
@@ -35,6 +299,7 @@ __global__ __launch_bounds__(kLpBlock) void logprob_kernel(LogprobArgs a) {
     Z = block_sum<kLpBlock>(Z, scratch);
     S = block_sum<kLpBlock>(S, scratch);
   }
+  const double logZ = log(Z);
   int bad_token = 0;
   const float nan = __uint_as_float(0x7FC00000u);
   for (int i = threadIdx.x; i < a.n; i += kLpBlock) {
@@ -43,13 +308,13 @@ __global__ __launch_bounds__(kLpBlock) void logprob_kernel(LogprobArgs a) {
     if (t != -1) {
       const bool in = t >= 0 && t < a.V;
       bad_token |= !in;
-      lp = in && !status ? log_prob(load_elem<DT>(row, t), M, Z, a.inv_t) : nan;
+      lp = in && !status ? log_prob(load_elem<DT>(row, t), M, logZ, a.inv_t) : nan;
     }
-    if (a.logprob) a.logprob[r * a.n + i] = lp;
+    a.logprob[r * a.n + i] = lp;
   }
   bad_token = block_max<kLpBlock>(bad_token, scratch);
   if (threadIdx.x == 0) {
-    if (a.entropy) a.entropy[r] = status ? nan : (float)((log(Z) - S / Z * kLn2));
+    if (a.entropy) a.entropy[r] = status ? nan : (float)(logZ - S / Z * kLn2);
     if (a.norm) {
       a.norm[2 * r] = status ? nan : M;
       a.norm[2 * r + 1] = status ? nan : (float)Z;
@@ -71,59 +336,61 @@ __global__ __launch_bounds__(kLpBlock) void logprob_kernel(LogprobArgs a) {
     last = best;
     if (threadIdx.x == 0) {
       const long long at = r * a.k + j;
-      if (a.top_ids) a.top_ids[at] = best ? top_id(best) : -1;
-      if (a.top_logprob)
-        a.top_logprob[at] = best ? log_prob(top_value(best), M, Z, a.inv_t)
-                                 : status ? nan : kNegInf;
+      a.top_ids[at] = best ? top_id(best) : -1;
+      a.top_logprob[at] = best ? log_prob(top_value(best), M, logZ, a.inv_t)
+                               : status ? nan : kNegInf;
     }
   }
 }
 
-template <int DT>
-__global__ __launch_bounds__(kLpBlock) void logprob_grad_kernel(LogprobGradArgs a) {
-  __shared__ BlockScratch scratch;
-  const long long r = blockIdx.x;
+// ------------------------------------------------------------ the gradient
+// One workgroup to a tile of a row; every wavefront forms the row's factors for itself.
+template <int DT, bool ONCE>
+__global__ __launch_bounds__(kSliceBlock) void logprob_grad_kernel(LogprobGradArgs a, int tiles) {
+  const int tile = blockIdx.x % tiles;
+  const long long r = blockIdx.x / tiles;
   const unsigned char* row = a.logits + r * a.stride_bytes;
   unsigned char* out = a.out + r * a.out_stride_bytes;
+  const int32_t* tokens = a.tokens + r * a.n;
+  const float* gs = a.g + r * a.n;
+  const int t0 = tile * kTileIds<DT>, t1 = min(a.V, t0 + kTileIds<DT>);
   double G = 0.0;
-  int any = 0;
-  for (int i = threadIdx.x; i < a.n; i += kLpBlock) {
-    const int t = a.tokens[r * a.n + i];
+  bool any = false, here = false;   // something comes back to the row; a token lies in the tile
+  for (int i = __lane_id(); i < a.n; i += kWave) {
+    const int t = tokens[i];
+    const float g = gs[i];
     if (t == -1) continue;
-    const float g = a.g[r * a.n + i];
-    any |= g != 0.0f;
-    G += t >= 0 && t < a.V ? (double)g : __longlong_as_double(0x7FF8000000000000ll);
+    const bool in = t >= 0 && t < a.V;
+    any |= g != 0.0f || !in;
+    here |= t >= t0 && t < t1;
+    G += in ? (double)g : __longlong_as_double(0x7FF8000000000000ll);
   }
-  G = block_sum<kLpBlock>(G, scratch);
   const float ge = a.ge ? a.ge[r] : 0.0f;
-  any = block_max<kLpBlock>(any, scratch) || ge != 0.0f || G != 0.0;
-  if (!any) {   // nothing comes back to this row: its logits are not looked at
-    for (int i = threadIdx.x; i < a.V; i += kLpBlock) store_elem<DT>(out, i, 0.0f);
+  if (!__any(any) && ge == 0.0f) {   // the row's logits are not looked at
+    zero_tile<DT>(out, a.V, tile);
     return;
   }
-  GradRow p;
-  p.M = a.norm[2 * r];
+  G = wave_sum(G);
   const float Z = a.norm[2 * r + 1];
-  p.c = a.c;
-  p.A = -(float)G * a.inv_t / Z;
-  p.B = 0.0f;
+  const double each = (double)a.inv_t / (double)Z;
+  double A = -G * each, B = 0.0;
   if (ge != 0.0f) {
-    const float H = a.entropy[r];
-    p.A = (float)(-(G + (double)ge * ((double)H - log((double)Z))) * a.inv_t / Z);
-    p.B = -ge * a.inv_t / Z * (float)kLn2;
+    A -= each * (double)ge * ((double)a.entropy[r] - log((double)Z));
+    B = -each * (double)ge * kLn2;
   }
-  for (int i = threadIdx.x; i < a.V; i += kLpBlock)
-    store_elem<DT>(out, i, p.at(load_elem<DT>(row, i)));
+  const GradRow p(a.norm[2 * r], a.c, A, B);
+  put_tile<DT, ONCE>(row, out, a.V, tile, p);
+  if (!__any(here)) return;   // the same for all of the workgroup
   __syncthreads();
-  for (int i = threadIdx.x; i < a.n; i += kLpBlock) {
-    const int t = a.tokens[r * a.n + i];
-    if (t < 0 || t >= a.V) continue;
+  for (int i = threadIdx.x; i < a.n; i += kSliceBlock) {
+    const int t = tokens[i];
+    if (t < t0 || t >= t1) continue;
     float g = 0.0f;
     bool first = true;
     for (int k = 0; k < a.n; ++k) {
-      if (a.tokens[r * a.n + k] != t) continue;
+      if (tokens[k] != t) continue;
       if (k < i) first = false;
-      g += a.g[r * a.n + k];
+      g += gs[k];
     }
     if (first) store_elem<DT>(out, t, fmaf(g, a.inv_t, p.at(load_elem<DT>(row, t))));
   }
@@ -131,22 +398,115 @@ __global__ __launch_bounds__(kLpBlock) void logprob_grad_kernel(LogprobGradArgs 
 
 }  // namespace
 
-size_t logprobs_ws_bytes(int, int, int, int) { return 0; }
+namespace {
 
-hipError_t launch_logprobs(const LogprobArgs& a, int dtype, void*, hipStream_t s) {
-  if (dtype == 0)
-    hipLaunchKernelGGL((logprob_kernel<0>), dim3(a.rows), dim3(kLpBlock), 0, s, a);
-  else
-    hipLaunchKernelGGL((logprob_kernel<1>), dim3(a.rows), dim3(kLpBlock), 0, s, a);
-  return hipGetLastError();
+constexpr int kSlicesMost = 64;     // a lane of the joining wavefront each
+constexpr int kKeysMost = kJoinRegion * kSliceWaves;   // of a row's slices together
+constexpr int kBatchRows = 8192;    // rows whose slices are in the workspace at a time
+
+// How rows are cut (slices 0: not at all, the wide kernel).
+Cut lp_cut(int dtype, int rows, int vocab, int k) {
+  const int whole = vocab / (dtype == 0 ? 4 : 8);
+  const int most = kMaxSlices16 * kSliceBlock;   // chunks of the largest slice
+  const int limit = k ? min(kSlicesMost, kKeysMost / k) : kSlicesMost;
+  Cut c{1, whole, 1};
+  if ((long long)whole > (long long)most * limit) return Cut{0, 0, 0};
+  int slices = max(1, (whole + most - 1) / most);
+  const int want = static_cast<int>(min(1024ll / max(rows, 1), 64ll));   // TUNE
+  slices = max(slices, std::min({want, limit, (whole + kSliceBlock - 1) / kSliceBlock}));
+  c.slices = slices;
+  c.per = (whole + slices - 1) / slices;
+  while (c.nc * kSliceBlock < c.per) c.nc *= 2;
+  return c;
 }
 
+template <int DT, bool TOP, bool ONCE>
+void launch_slices(const LogprobArgs& a, const Cut& cut, const LpWs& ws, hipStream_t s) {
+  const dim3 grid((unsigned)a.rows * (unsigned)cut.slices), block(kSliceBlock);
+  switch (cut.nc) {
+    case 1: hipLaunchKernelGGL((logprob_slice_kernel<DT, 1, TOP, ONCE>), grid, block, 0, s, a, cut, ws); break;
+    case 2: hipLaunchKernelGGL((logprob_slice_kernel<DT, 2, TOP, ONCE>), grid, block, 0, s, a, cut, ws); break;
+    case 4: hipLaunchKernelGGL((logprob_slice_kernel<DT, 4, TOP, ONCE>), grid, block, 0, s, a, cut, ws); break;
+    case 8: hipLaunchKernelGGL((logprob_slice_kernel<DT, 8, TOP, ONCE>), grid, block, 0, s, a, cut, ws); break;
+    default: hipLaunchKernelGGL((logprob_slice_kernel<DT, 16, TOP, ONCE>), grid, block, 0, s, a, cut, ws);
+  }
+}
+
+template <int DT>
+hipError_t launch_dt(const LogprobArgs& all, void* workspace, hipStream_t s) {
+  const Cut cut = lp_cut(DT, all.rows, all.V, all.k);
+  if (cut.slices == 0) {
+    hipLaunchKernelGGL((logprob_wide_kernel<DT>), dim3(all.rows), dim3(kLpBlock), 0, s, all);
+    return hipGetLastError();
+  }
+  for (int r0 = 0; r0 < all.rows; r0 += kBatchRows) {
+    LogprobArgs a = all;
+    a.rows = min(kBatchRows, all.rows - r0);
+    a.logits += (long long)r0 * a.stride_bytes;
+    if (a.tokens) a.tokens += (long long)r0 * a.n, a.logprob += (long long)r0 * a.n;
+    if (a.entropy) a.entropy += r0;
+    if (a.k) a.top_ids += (long long)r0 * a.k, a.top_logprob += (long long)r0 * a.k;
+    if (a.norm) a.norm += 2ll * r0;
+    if (a.status) a.status += r0;
+    LpWs ws{static_cast<Sums*>(workspace), nullptr};
+    ws.keys = reinterpret_cast<unsigned long long*>(ws.sums + (long long)a.rows * cut.slices);
+    if (a.k)
+      launch_slices<DT, true, false>(a, cut, ws, s);
+    else
+      launch_slices<DT, false, false>(a, cut, ws, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (cut.slices == 1) continue;
+    if (a.k)
+      hipLaunchKernelGGL((logprob_top_join_kernel<DT>), dim3(a.rows), dim3(kSliceBlock), 0, s, a,
+                         cut.slices, ws);
+    else
+      hipLaunchKernelGGL((logprob_join_kernel<DT>), dim3((a.rows + kSliceWaves - 1) / kSliceWaves),
+                         dim3(kSliceBlock), 0, s, a, cut.slices, ws);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t logprobs_ws_bytes(int dtype, int rows, int vocab, int k) {
+  const Cut cut = lp_cut(dtype, rows, vocab, k);
+  if (cut.slices <= 1) return 0;
+  return (size_t)min(rows, kBatchRows) * cut.slices * (sizeof(Sums) + 8 * (size_t)k);
+}
+
+hipError_t launch_logprobs(const LogprobArgs& a, int dtype, void* ws, hipStream_t s) {
+  return dtype == 0 ? launch_dt<0>(a, ws, s) : launch_dt<1>(a, ws, s);
+}
+
+namespace {
+
+template <int DT>
+hipError_t launch_grad(const LogprobGradArgs& all, hipStream_t s) {
+  const int tiles = tiles_of<DT>(all.V);
+  const int batch = max(1, (1 << 23) / tiles);   // workgroups of a launch: fewer than 2^24
+  for (int r0 = 0; r0 < all.rows; r0 += batch) {
+    LogprobGradArgs a = all;
+    a.rows = min(batch, all.rows - r0);
+    a.logits += (long long)r0 * a.stride_bytes;
+    a.out += (long long)r0 * a.out_stride_bytes;
+    if (a.n) a.tokens += (long long)r0 * a.n, a.g += (long long)r0 * a.n;
+    a.norm += 2ll * r0;
+    if (a.ge) a.ge += r0, a.entropy += r0;
+    hipLaunchKernelGGL((logprob_grad_kernel<DT, false>), dim3(a.rows * tiles), dim3(kSliceBlock), 0,
+                       s, a, tiles);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
 hipError_t launch_logprobs_grad(const LogprobGradArgs& a, int dtype, hipStream_t s) {
-  if (dtype == 0)
-    hipLaunchKernelGGL((logprob_grad_kernel<0>), dim3(a.rows), dim3(kLpBlock), 0, s, a);
-  else
-    hipLaunchKernelGGL((logprob_grad_kernel<1>), dim3(a.rows), dim3(kLpBlock), 0, s, a);
-  return hipGetLastError();
+  return dtype == 0 ? launch_grad<0>(a, s) : launch_grad<1>(a, s);
 }
 
 }  // namespace tsr

@@ -1,0 +1,200 @@
+// A row of logits cut into slices, one to a workgroup, each held in registers: read
+// once, its sums taken against each thread's own largest logit (no exchange before the
+// exponentials) and joined afterwards.
+//
+// A thread's weights: rc = fl(m c) for its largest m, x = fma(z, c, -rc), e = 2^x.
+// x is the exponent (z - m) c but for rc - m c, the same for all of the thread's
+// elements and known exactly (one fma): it goes into the factor that joins the
+// thread to the others. That is one fma an element where (z - m) c takes two
+// roundings and two instructions.
+#pragma once
+
+#include "kernels.hpp"
+#include "scores.hpp"
+#include "wide_mem.hpp"
+
+namespace tsr {
+
+constexpr int kSliceBlock = 256;
+constexpr int kSliceWaves = kSliceBlock / kWave;
+constexpr int kMaxSlices16 = 16;   // most 16-byte chunks a thread holds
+
+// How a row is cut: `slices` workgroups of up to `per` whole chunks each, `nc` to a
+// thread (the elements behind the last whole chunk go with the last slice).
+struct Cut {
+  int slices, per, nc;
+};
+
+// Weights against a largest logit M: their sum, and that of weight times exponent.
+struct Sums {
+  float M;
+  double Z, S;
+};
+
+// What joins sums against m to others against M: 2^d with d = (m - M) c + off. -inf has
+// no weight; NaN stays.
+__device__ __forceinline__ void rebase(Sums& a, float M, float c, float off) {
+  const float d = a.M == M ? off : fmaxf(fmaf(a.M - M, c, off), -2000.0f);
+  const double f = (double)__builtin_amdgcn_exp2f(d);
+  a.S = f * fma(a.Z, (double)d, a.S);
+  a.Z *= f;
+  a.M = M;
+}
+
+// The workgroup's sums from its threads'; `each` has a place for every wavefront.
+__device__ __forceinline__ Sums join_block(Sums a, float c, float off, Sums* each) {
+  rebase(a, wave_maxn(a.M), c, off);
+  a.Z = wave_sum(a.Z);
+  a.S = wave_sum(a.S);
+  if (__lane_id() == 0) each[threadIdx.x / kWave] = a;
+  __syncthreads();
+  float M = each[0].M;
+#pragma unroll
+  for (int w = 1; w < kSliceWaves; ++w) M = fmaxn(M, each[w].M);
+  Sums all{M, 0.0, 0.0};
+#pragma unroll
+  for (int w = 0; w < kSliceWaves; ++w) {
+    Sums one = each[w];
+    rebase(one, M, c, 0.0f);
+    all.Z += one.Z;
+    all.S += one.S;
+  }
+  return all;
+}
+
+// The elements of a chunk as the pass sees them. Passes over the same registers unpack
+// bf16 anew: kept from one pass to the next the values would take twice the chunks'
+// registers. A shift and a mask that the compiler does not know to be the other pass's
+// keep it from that (bf16, 16 chunks: 82 registers against 158).
+struct Pass {
+  int sixteen;
+  uint32_t high;
+  __device__ __forceinline__ Pass() {
+    asm volatile("s_mov_b32 %0, 16" : "=s"(sixteen));
+    asm volatile("s_mov_b32 %0, 0xffff0000" : "=s"(high));
+  }
+  template <int DT>
+  __device__ __forceinline__ void unpack(const uint4 r, float* v) const {
+    if constexpr (DT == 0) {
+      tsr::unpack<0>(r, v);
+    } else {
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << sixteen);
+        v[2 * i + 1] = __uint_as_float(w[i] & high);
+      }
+    }
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ float max_of(const float* v) {
+  if constexpr (DT == 0) return fmaxn(fmax3n(v[0], v[1], v[2]), v[3]);
+  return fmaxn(fmax3n(fmax3n(v[0], v[1], v[2]), v[3], v[4]), fmax3n(v[5], v[6], v[7]));
+}
+
+template <int DT, int NC>
+struct Slice {
+  static constexpr int EPC = Fmt<DT>::EPC;
+  const unsigned char* row;
+  uint4 c[NC];
+  uint4 rest;   // the elements behind the last whole chunk, with one thread of the last slice
+  int lo, hi;   // the slice's whole chunks
+  bool ragged;
+
+  __device__ __forceinline__ int chunk_id(int j) const {
+    return lo + j * kSliceBlock + (int)threadIdx.x;
+  }
+
+  template <bool ONCE>
+  __device__ __forceinline__ void load(const unsigned char* at, int V, int slice, const Cut& cut) {
+    row = at;
+    const int whole = V / EPC;
+    lo = slice * cut.per;
+    hi = min(lo + cut.per, whole);
+    ragged = slice == cut.slices - 1 && whole * EPC < V;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int i = chunk_id(j);
+      const void* p = i < hi ? static_cast<const void*>(row + (long long)i * 16)
+                             : static_cast<const void*>(&g_neg_inf_chunk[DT]);
+      c[j] = ONCE ? load16_once(p) : load16(p);
+    }
+    rest = neg_inf_chunk<DT>();
+    if (ragged && threadIdx.x == kSliceBlock - 1) rest = load_chunk_slow<DT>(row, whole, V);
+  }
+
+  // f(values, number of the first) for each chunk of the thread
+  template <class F>
+  __device__ __forceinline__ void each(int V, F&& f) const {
+    const Pass pass;
+    float v[EPC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      pass.unpack<DT>(c[j], v);
+      f(v, chunk_id(j) * EPC);
+      sched_fence();
+    }
+    if (ragged) {
+      pass.unpack<DT>(rest, v);
+      f(v, V / EPC * EPC);
+    }
+  }
+
+  // The same for passes that are seldom taken: the chunks read again, one at a time.
+  template <class F>
+  __device__ __forceinline__ void each_again(int V, F&& f) const {
+    float v[EPC];
+#pragma unroll 1
+    for (int i = lo + (int)threadIdx.x; i < hi; i += kSliceBlock) {
+      tsr::unpack<DT>(load16(row + (long long)i * 16), v);
+      f(v, i * EPC);
+    }
+    if (ragged) {
+      tsr::unpack<DT>(rest, v);
+      f(v, V / EPC * EPC);
+    }
+  }
+
+  __device__ __forceinline__ float largest(int V) const {
+    float m = kNegInf;
+    each(V, [&](const float* v, int) { m = fmaxn(m, max_of<DT>(v)); });
+    return m;
+  }
+
+  // The thread's sums against its largest logit m (S in units of log 2) and what its
+  // exponents are short of. Eight products at most are added in float32. Exponents are
+  // held above -2000, where weights are 0: a logit of -inf gives 0 in S and not NaN.
+  __device__ __forceinline__ Sums sums(int V, float m, float c_log2, float& off) const {
+    const float ref = m > kNegInf ? m : 0.0f;
+    const float rc = ref * c_log2;
+    off = -fmaf(ref, c_log2, -rc);
+    Sums a{m, 0.0, 0.0};
+    const auto add = [&](const float* v, auto&& x_of) {
+      float z = 0.0f, s = 0.0f;
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) {
+        const float x = x_of(v[e]);
+        const float w = __builtin_amdgcn_exp2f(x);
+        z += w;
+        s = fmaf(w, x, s);
+      }
+      a.Z += (double)z;
+      a.S += (double)s;
+    };
+    if (fabsf(rc) <= 0x1p20f) {
+      each(V, [&](const float* v, int) {
+        add(v, [&](float z) { return fmaxf(fmaf(z, c_log2, -rc), -2000.0f); });
+      });
+    } else {   // the rounding of m c is no small shift of the exponents
+      off = 0.0f;
+      each_again(V, [&](const float* v, int) {
+        add(v, [&](float z) { return exponent(z, ref, c_log2); });
+      });
+    }
+    return a;
+  }
+};
+
+}  // namespace tsr

@@ -16,8 +16,8 @@ __device__ __forceinline__ float exponent(float v, float M, float c) {
 }
 
 // log p of a logit v: (v - M) / T - log Z, formed in 64 bits and rounded once.
-__device__ __forceinline__ float log_prob(float v, float M, double Z, double inv_t) {
-  return (float)(((double)v - (double)M) * inv_t - log(Z));
+__device__ __forceinline__ float log_prob(float v, float M, double logZ, double inv_t) {
+  return (float)(((double)v - (double)M) * inv_t - logZ);
 }
 
 // Keys of ids that order as (value, then the lower id) do; 0 is below all of them.
@@ -31,12 +31,35 @@ __device__ __forceinline__ float top_value(unsigned long long key) {
   return key2f((uint32_t)(key >> 32));
 }
 
-// One element of a row's gradient: e (A + B x), e = 2^x, x = (z - M) log2(e) / T.
+// A row's gradient: e (A + B X), e = 2^X, X = (z - M) log2(e) / T. X is formed in one fma
+// against rc = fl(M c); what it is short of, rc - M c, is the same for the whole row,
+// known exactly, and goes into A and B. Where M c is so large that this is no small
+// shift, the difference is formed first.
 struct GradRow {
-  float M, c, A, B;
-  __device__ __forceinline__ float at(float z) const {
-    const float x = exponent(z, M, c);
+  float M, c, rc, A, B;
+  bool plain;   // the difference first
+  __device__ __forceinline__ GradRow(float M, float c, double A0, double B0) : M(M), c(c) {
+    rc = M * c;
+    const float off = -fmaf(M, c, -rc);
+    plain = !(fabsf(rc) <= 0x1p20f);
+    const double f = plain ? 1.0 : (double)__builtin_amdgcn_exp2f(off);
+    A = (float)(plain ? A0 : f * (A0 + B0 * (double)off));
+    B = (float)(f * B0);
+  }
+  // Exponents are held above -2000 where B counts: a logit of -inf has a gradient of 0
+  template <bool WITH_B, bool PLAIN>
+  __device__ __forceinline__ float of(float z) const {
+    if constexpr (PLAIN) {
+      const float x = exponent(z, M, c);
+      return __builtin_amdgcn_exp2f(x) * fmaf(B, x, A);
+    }
+    float x = fmaf(z, c, -rc);
+    if constexpr (!WITH_B) return __builtin_amdgcn_exp2f(x) * A;
+    x = fmaxf(x, -2000.0f);
     return __builtin_amdgcn_exp2f(x) * fmaf(B, x, A);
+  }
+  __device__ __forceinline__ float at(float z) const {
+    return plain ? of<true, true>(z) : B != 0.0f ? of<true, false>(z) : of<false, false>(z);
   }
 };
 
