@@ -8,38 +8,47 @@
 //
 // p_r is summed over the ids outside S themselves, and their weights are taken against
 // their own largest: as 1 - sum_S p it would be lost where S holds nearly everything.
-#include "kernels.hpp"
-#include "scores.hpp"
-#include "wide_mem.hpp"
+#include <algorithm>
+
+#include "grad_tile.hpp"
 
 namespace tsr {
 namespace {
 
-constexpr int kDtBlock = 256;
-constexpr int kDtTile = 32768;        // ids whose membership in S one pass of LDS holds
 constexpr float kRestMin = 0x1p-20f;  // a remainder below this is rounding of the entries
 
 // The entries of a row, one to a lane of a wavefront.
 struct Entries {
-  int id;          // -1: none, or a lane past the last
-  bool first;      // no lower lane holds the same id
-  double q, log_q; // the teacher's probability
-  double same;     // sum of q over the lanes of this id
+  int id;              // -1: none, or a lane past the last
+  bool first;          // no lower lane holds the same id
+  double q, log_q;     // the teacher's probability
+  double same;         // sum of q over the lanes of this id
   double sum, rest;
   int status;
 };
 
-__device__ __forceinline__ Entries load_entries(const DistillArgs& a, long long r) {
+__device__ __forceinline__ int raw_id(const DistillArgs& a, long long r) {
+  const int lane = __lane_id();
+  return lane < a.k ? a.ids[r * a.k + lane] : -1;
+}
+__device__ __forceinline__ float teacher_of(const DistillArgs& a, long long r) {
+  const int lane = __lane_id();
+  return lane < a.k ? a.teacher[r * a.k + lane] : kNegInf;
+}
+// -1 for what is no id of the vocabulary
+__device__ __forceinline__ int valid_id(const DistillArgs& a, int id) {
+  return id >= 0 && id < a.V ? id : -1;
+}
+
+__device__ __forceinline__ Entries entries_of(const DistillArgs& a, int id, float t) {
   Entries e;
   const int lane = __lane_id();
-  const bool in = lane < a.k;
-  e.id = in ? a.ids[r * a.k + lane] : -1;
-  const float t = in ? a.teacher[r * a.k + lane] : kNegInf;
-  const bool real = e.id != -1;
+  e.id = id;
+  const bool real = id != -1;
   e.status = 0;
-  const bool outside = real && (e.id < 0 || e.id >= a.V);
-  if (__ballot(outside)) e.status = 3;
-  else if (__ballot(real && !(t < kPosInf))) e.status = 1;
+  const bool outside = real && valid_id(a, id) < 0;
+  if (__any(outside)) e.status = 3;
+  else if (__any(real && !(t < kPosInf))) e.status = 1;
   const float top = wave_max(real ? t : kNegInf);   // drops NaN: those rows are marked
   if (!e.status && top == kNegInf) e.status = 2;
   if (outside) e.id = -1;
@@ -58,101 +67,322 @@ __device__ __forceinline__ Entries load_entries(const DistillArgs& a, long long 
     e.sum = 1.0;
   }
   e.first = e.id >= 0;
-  e.same = 0.0;
-  for (int l = 0; l < a.k; ++l) {
-    const int other = (int)readlane_u32((uint32_t)e.id, l);
-    const double q = readlane_f64(e.q, l);
-    if (other != e.id) continue;
-    e.same += q;
-    if (l < lane) e.first = false;
+  e.same = e.q;
+  for (int l = 0; l < a.k; ++l) {   // the same id again
+    const bool again = (int)readlane_u32((uint32_t)e.id, l) == e.id && l != lane;
+    if (__any(again)) {
+      const double q = readlane_f64(e.q, l);
+      if (again) e.same += q;
+      if (again && l < lane) e.first = false;
+    }
   }
   return e;
 }
 
-template <int DT>
-__global__ __launch_bounds__(kDtBlock) void distill_kernel(DistillArgs a) {
-  __shared__ BlockScratch scratch;
-  __shared__ uint32_t in_s[kDtTile / 32];
+// What the gradient of a row takes: p_j (A + 0 x) against M, and an entry's own value.
+struct RowGrad {
+  float M;
+  double A;
+  float entry;
+};
+
+// Loss, status and the gradient's factors of row r from its entries and the sums of the
+// other ids (all ids without a tail), by one wavefront. z: the entry's logit.
+__device__ __forceinline__ RowGrad finish_row(const DistillArgs& a, long long r, float weight,
+                                              const Entries& e, float z, const Sums& other) {
+  const float Ms = a.tail ? wave_maxn(e.id >= 0 ? z : kNegInf) : kNegInf;
+  const float M = fmaxn(other.M, Ms);
+  const int status = e.status ? e.status : M == kNegInf ? 2 : !(M < kPosInf) ? 1 : 0;
+  const double Zr = other.Z;
+  const double log_f = ((double)other.M - (double)M) * a.inv_t;
+  const double f = other.M > kNegInf ? exp(log_f) : 0.0;   // a weight against other.M, against M
+  const double ez =
+      e.id >= 0 ? (double)__builtin_amdgcn_exp2f(exponent(z, M, a.c)) : 0.0;
+  const double Z = Zr * f + (a.tail ? wave_sum(e.first ? ez : 0.0) : 0.0);
+  const double logZ = log(Z);
+  double term = 0.0;
+  if (e.q > 0.0) term = e.q * (e.log_q - (((double)z - (double)M) * a.inv_t - logZ));
+  double loss = wave_sum(term);
+  if (e.rest > 0.0)   // +inf where the draft gives the other ids nothing
+    loss += e.rest * (log(e.rest) - (other.M > kNegInf ? log(Zr) + log_f - logZ
+                                                       : -__builtin_huge_val()));
+  const float nan = __uint_as_float(0x7FC00000u);
+  if (__lane_id() == 0) {
+    a.loss[r] = status ? nan : (float)(loss * weight);
+    if (a.status) a.status[r] = status;
+  }
+  const double each = (double)weight * a.inv_t;
+  const double whole = e.sum + e.rest;
+  RowGrad g;
+  // without an id outside S there is no weight to multiply: any M and a factor of 0
+  g.M = other.M == kNegInf ? 0.0f : other.M;
+  g.A = status ? (double)nan : Zr > 0.0 ? each * (whole * f / Z - e.rest / Zr) : 0.0;
+  g.entry = status ? nan : (float)(each * (whole * ez / Z - e.same));
+  return g;
+}
+
+// ------------------------------------------------------------ a row in one workgroup
+// Read once: the gradient is formed from the registers that the sums were.
+template <int DT, int NC, int BLOCK>
+__global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
+  constexpr int EPC = Fmt<DT>::EPC;
+  __shared__ Sums each[BLOCK / kWave];
+  __shared__ typename Slice<DT, NC, BLOCK>::LeftOut left_out;
+  __shared__ Entries entries[kWave];   // kept here between the two uses: registers are short
+  __shared__ struct {
+    float M;
+    double A;
+  } row_grad;
   const long long r = blockIdx.x;
-  const unsigned char* row = a.logits + r * a.stride_bytes;
   unsigned char* out = a.grad ? a.grad + r * a.grad_stride_bytes : nullptr;
+  const int whole = a.V / EPC;
   const float weight = a.weight ? a.weight[r] : 1.0f;
   if (weight == 0.0f) {   // the row does not count: neither its logits nor its entries do
-    if (out)
-      for (int i = threadIdx.x; i < a.V; i += kDtBlock) store_elem<DT>(out, i, 0.0f);
+    if (out) {
+      for (int i = threadIdx.x; i < whole; i += BLOCK)
+        store16<false>(out + (long long)i * 16, make_uint4(0, 0, 0, 0));
+      if ((int)threadIdx.x < a.V - whole * EPC)
+        store_elem<DT>(out, whole * EPC + (int)threadIdx.x, 0.0f);
+    }
     if (threadIdx.x == 0) {
       a.loss[r] = 0.0f;
       if (a.status) a.status[r] = 0;
     }
     return;
   }
-  const Entries e = load_entries(a, r);   // each wavefront for itself
-  // with a tail the entries' ids are left out of the sums and come back one by one
-  const auto bits = [&](int t0) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kDtTile / 32; i += kDtBlock) in_s[i] = 0;
-    __syncthreads();
-    if (a.tail && threadIdx.x < kWave && e.id >= t0 && e.id - t0 < kDtTile)
-      atomicOr(&in_s[(e.id - t0) / 32], 1u << ((e.id - t0) % 32));
-    __syncthreads();
-  };
-  const auto left_out = [&](int i) { return in_s[i / 32] >> (i % 32) & 1; };
-  const float z = e.id >= 0 ? load_elem<DT>(row, e.id) : kNegInf;
-  const float Ms = wave_maxn(a.tail ? z : kNegInf);
-  float Mr = kNegInf;
-  for (int t0 = 0; t0 < a.V; t0 += kDtTile) {
-    bits(t0);
-    for (int i = threadIdx.x; i < min(a.V - t0, kDtTile); i += kDtBlock)
-      if (!left_out(i)) Mr = fmaxn(Mr, load_elem<DT>(row, t0 + i));
-  }
-  Mr = block_maxn<kDtBlock>(Mr, scratch);
-  const float M = fmaxn(Mr, Ms);
-  const int status = e.status ? e.status : M == kNegInf ? 2 : !(M < kPosInf) ? 1 : 0;
-  if (Mr == kNegInf) Mr = 0.0f;   // any number: all their weights are 0
-  double Zr = 0.0;
-  for (int t0 = 0; t0 < a.V; t0 += kDtTile) {
-    bits(t0);
-    for (int i = threadIdx.x; i < min(a.V - t0, kDtTile); i += kDtBlock)
-      if (!left_out(i))
-        Zr += (double)__builtin_amdgcn_exp2f(exponent(load_elem<DT>(row, t0 + i), Mr, a.c));
-  }
-  Zr = block_sum<kDtBlock>(Zr, scratch);
-  const double ez = e.id >= 0 ? exp(((double)z - (double)M) * a.inv_t) : 0.0;
-  const double log_f = ((double)Mr - (double)M) * a.inv_t;
-  const double f = Zr > 0.0 ? exp(log_f) : 0.0;   // what a weight against Mr is against M
-  const double Z = Zr * f + wave_sum(a.tail && e.first ? ez : 0.0);
-  double term = 0.0;
-  if (e.q > 0.0) term = e.q * (e.log_q - (((double)z - (double)M) * a.inv_t - log(Z)));
-  double loss = wave_sum(term);
-  if (e.rest > 0.0) loss += e.rest * (log(e.rest) - (log(Zr) + log_f - log(Z)));
-  const float nan = __uint_as_float(0x7FC00000u);
-  if (threadIdx.x == 0) {
-    a.loss[r] = status ? nan : (float)(loss * weight);
-    if (a.status) a.status[r] = status;
+  const int id = raw_id(a, r);
+  const float t = teacher_of(a, r);
+  const unsigned char* row = a.logits + r * a.stride_bytes;
+  Slice<DT, NC, BLOCK> s;
+  s.template load<false>(row, a.V, 0, Cut{1, whole, NC});
+  if (threadIdx.x < kWave) entries[threadIdx.x] = entries_of(a, id, t);   // the row is on its way
+  if (a.tail) s.leave_out(a.V, valid_id(a, id), left_out);
+  float off;
+  const float m = s.largest();
+  const Sums mine = s.template sums<false>(a.V, m, a.c, off);
+  const Sums other = join_block<BLOCK / kWave>(mine, a.c, off, each);
+  float own = 0.0f;   // the entry's gradient
+  if (threadIdx.x < kWave) {
+    const Entries e = entries[threadIdx.x];
+    const float z = e.id >= 0 ? load_elem<DT>(row, e.id) : kNegInf;
+    const RowGrad g = finish_row(a, r, weight, e, z, other);
+    own = g.entry;
+    if (threadIdx.x == 0) {
+      row_grad.M = g.M;
+      row_grad.A = g.A;
+    }
   }
   if (!out) return;
-  const double each = weight * a.inv_t;
-  const double whole = e.sum + e.rest;
-  const GradRow p(Mr, a.c,
-                  status ? (double)nan : Zr > 0.0 ? each * (whole * f / Z - e.rest / Zr) : 0.0,
-                  0.0);
-  for (int i = threadIdx.x; i < a.V; i += kDtBlock)
-    store_elem<DT>(out, i, p.at(load_elem<DT>(row, i)));
   __syncthreads();
-  if (threadIdx.x < kWave && !status && e.first)
-    store_elem<DT>(out, e.id, (float)(each * (whole * ez / Z - e.same)));
+  const GradRow p(row_grad.M, a.c, row_grad.A, 0.0);
+  const Pass pass;
+  const auto put = [&](auto&& of) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      float v[EPC];
+      pass.unpack<DT>(s.c[j], v);
+#pragma unroll
+      for (int i = 0; i < EPC; ++i) v[i] = of(v[i]);
+      unsigned char* base = out + j * BLOCK * 16;   // uniform
+      if (j * BLOCK + (int)threadIdx.x < whole) store16<false>(base + threadIdx.x * 16u, pack<DT>(v));
+      sched_fence();
+    }
+  };
+  if (p.plain)
+    put([&](float x) { return p.of<true, true>(x); });
+  else
+    put([&](float x) { return p.of<false, false>(x); });
+  if ((int)threadIdx.x < a.V - whole * EPC)
+    store_elem<DT>(out, whole * EPC + (int)threadIdx.x,
+                   p.at(load_elem<DT>(row, whole * EPC + (int)threadIdx.x)));
+  __syncthreads();   // the entries' own values over what was put there
+  if (threadIdx.x < kWave && entries[threadIdx.x].first)
+    store_elem<DT>(out, entries[threadIdx.x].id, own);
+}
+
+// ------------------------------------------------------------ wider rows
+// Workspace: the sums of each slice, what the gradient takes of each row, and each
+// entry's gradient (k to a row).
+struct DtRow {
+  double A;
+  float M;
+  float weight;
+};
+struct DtWs {
+  Sums* sums;      // [rows][slices]
+  DtRow* rows;     // [rows]
+  float* entry;    // [rows][k]
+};
+
+template <int DT, int NC>
+__global__ __launch_bounds__(kSliceBlock) void distill_slice_kernel(DistillArgs a, Cut cut,
+                                                                    DtWs ws) {
+  __shared__ Sums each[kSliceWaves];
+  __shared__ typename Slice<DT, NC>::LeftOut left_out;
+  const int slice = blockIdx.x % cut.slices;
+  const long long r = blockIdx.x / cut.slices;
+  if (a.weight && a.weight[r] == 0.0f) return;
+  const int id = a.tail ? valid_id(a, raw_id(a, r)) : -1;
+  Slice<DT, NC> s;
+  s.template load<false>(a.logits + r * a.stride_bytes, a.V, slice, cut);
+  if (a.tail) s.leave_out(a.V, id, left_out);
+  float off;
+  const float m = s.largest();
+  const Sums mine = s.template sums<false>(a.V, m, a.c, off);
+  const Sums all = join_block<kSliceWaves>(mine, a.c, off, each);
+  if (threadIdx.x == 0) ws.sums[r * cut.slices + slice] = all;
+}
+
+// One wavefront to a row.
+template <int DT>
+__global__ __launch_bounds__(kSliceBlock) void distill_join_kernel(DistillArgs a, int slices,
+                                                                   DtWs ws) {
+  const long long r = (long long)blockIdx.x * kSliceWaves + threadIdx.x / kWave;
+  if (r >= a.rows) return;
+  const int lane = __lane_id();
+  const float weight = a.weight ? a.weight[r] : 1.0f;
+  if (weight == 0.0f) {
+    if (lane == 0) {
+      a.loss[r] = 0.0f;
+      if (a.status) a.status[r] = 0;
+      ws.rows[r].weight = 0.0f;
+    }
+    return;
+  }
+  const int id = raw_id(a, r);
+  const float t = teacher_of(a, r);
+  const float z =
+      valid_id(a, id) >= 0 ? load_elem<DT>(a.logits + r * a.stride_bytes, id) : kNegInf;
+  const Sums other = join_slices(ws.sums + r * slices, slices, a.c);
+  const Entries e = entries_of(a, id, t);
+  const RowGrad g = finish_row(a, r, weight, e, z, other);
+  if (lane == 0) ws.rows[r] = DtRow{g.A, g.M, weight};
+  if (lane < a.k) ws.entry[r * a.k + lane] = g.entry;
+}
+
+// One workgroup to a tile of a row.
+template <int DT>
+__global__ __launch_bounds__(kSliceBlock) void distill_grad_kernel(DistillArgs a, int tiles,
+                                                                   DtWs ws) {
+  const int tile = blockIdx.x % tiles;
+  const long long r = blockIdx.x / tiles;
+  unsigned char* out = a.grad + r * a.grad_stride_bytes;
+  const DtRow d = ws.rows[r];
+  if (d.weight == 0.0f) {
+    zero_tile<DT>(out, a.V, tile);
+    return;
+  }
+  const int id = valid_id(a, raw_id(a, r)), lane = __lane_id();
+  const float own = lane < a.k ? ws.entry[r * a.k + lane] : 0.0f;
+  put_tile<DT, false>(a.logits + r * a.stride_bytes, out, a.V, tile, GradRow(d.M, a.c, d.A, 0.0));
+  const bool here = id >= 0 && id / kTileIds<DT> == tile;
+  if (!__any(here)) return;   // the same for all of the workgroup
+  __syncthreads();
+  // an id that comes twice has the same value with each
+  if (threadIdx.x < kWave && here) store_elem<DT>(out, id, own);
+}
+
+
+// Rows of up to this many chunks take one workgroup each, and are read once.
+constexpr int kRowBlock = 1024;
+constexpr int kRowChunks = 20 * kRowBlock;
+
+// How rows are cut; nc 0: not at all, one workgroup of kRowBlock threads to a row.
+Cut dt_cut(int dtype, int rows, int vocab) {
+  const int whole = vocab / (dtype == 0 ? 4 : 8);
+  if (whole <= kMaxSliceChunks) return cut_of(whole, 1);   // TUNE
+  if (whole <= kRowChunks && rows >= 128) return Cut{1, whole, 0};
+  return cut_of(whole, std::min({1024 / max(rows, 1), 64, (whole + kSliceBlock - 1) / kSliceBlock}));
+}
+
+template <int DT, int NC, int BLOCK>
+void launch_row(const DistillArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((distill_row_kernel<DT, NC, BLOCK>), dim3(a.rows), dim3(BLOCK), 0, s, a);
+}
+
+template <int DT>
+void launch_rows(const DistillArgs& a, const Cut& cut, hipStream_t s) {
+  switch (cut.nc) {
+    case 1: return launch_row<DT, 1, kSliceBlock>(a, s);
+    case 2: return launch_row<DT, 2, kSliceBlock>(a, s);
+    case 4: return launch_row<DT, 4, kSliceBlock>(a, s);
+    case 8: return launch_row<DT, 8, kSliceBlock>(a, s);
+    case 16: return launch_row<DT, 16, kSliceBlock>(a, s);
+  }
+  if (cut.per <= 8 * kRowBlock) return launch_row<DT, 8, kRowBlock>(a, s);
+  if (cut.per <= 12 * kRowBlock) return launch_row<DT, 12, kRowBlock>(a, s);
+  if (cut.per <= 16 * kRowBlock) return launch_row<DT, 16, kRowBlock>(a, s);
+  return launch_row<DT, 20, kRowBlock>(a, s);
+}
+
+template <int DT>
+void launch_slices(const DistillArgs& a, const Cut& cut, const DtWs& ws, hipStream_t s) {
+  const dim3 grid((unsigned)a.rows * (unsigned)cut.slices), block(kSliceBlock);
+  switch (cut.nc) {
+    case 1: hipLaunchKernelGGL((distill_slice_kernel<DT, 1>), grid, block, 0, s, a, cut, ws); break;
+    case 2: hipLaunchKernelGGL((distill_slice_kernel<DT, 2>), grid, block, 0, s, a, cut, ws); break;
+    case 4: hipLaunchKernelGGL((distill_slice_kernel<DT, 4>), grid, block, 0, s, a, cut, ws); break;
+    case 8: hipLaunchKernelGGL((distill_slice_kernel<DT, 8>), grid, block, 0, s, a, cut, ws); break;
+    default: hipLaunchKernelGGL((distill_slice_kernel<DT, 16>), grid, block, 0, s, a, cut, ws);
+  }
+}
+
+// Rows whose slices and tiles a batch holds: 2^23 workgroups of a launch at most.
+int dt_batch(const Cut& cut, int rows, int tiles) {
+  return std::min(batch_of(cut, rows), max(1, (1 << 23) / tiles));
+}
+
+template <int DT>
+hipError_t launch_dt(const DistillArgs& all, void* workspace, hipStream_t s) {
+  const Cut cut = dt_cut(DT, all.rows, all.V);
+  if (cut.slices == 1) {
+    launch_rows<DT>(all, cut, s);
+    return hipGetLastError();
+  }
+  const int tiles = tiles_of<DT>(all.V), batch = dt_batch(cut, all.rows, tiles);
+  for (int r0 = 0; r0 < all.rows; r0 += batch) {
+    DistillArgs a = all;
+    a.rows = min(batch, all.rows - r0);
+    a.logits += (long long)r0 * a.stride_bytes;
+    a.ids += (long long)r0 * a.k;
+    a.teacher += (long long)r0 * a.k;
+    if (a.weight) a.weight += r0;
+    a.loss += r0;
+    if (a.grad) a.grad += (long long)r0 * a.grad_stride_bytes;
+    if (a.status) a.status += r0;
+    DtWs ws;
+    ws.sums = static_cast<Sums*>(workspace);
+    ws.rows = reinterpret_cast<DtRow*>(ws.sums + (long long)a.rows * cut.slices);
+    ws.entry = reinterpret_cast<float*>(ws.rows + a.rows);
+    launch_slices<DT>(a, cut, ws, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((distill_join_kernel<DT>), dim3((a.rows + kSliceWaves - 1) / kSliceWaves),
+                       dim3(kSliceBlock), 0, s, a, cut.slices, ws);
+    e = hipGetLastError();
+    if (e != hipSuccess || !a.grad) {
+      if (e != hipSuccess) return e;
+      continue;
+    }
+    hipLaunchKernelGGL((distill_grad_kernel<DT>), dim3(a.rows * tiles), dim3(kSliceBlock), 0, s, a,
+                       tiles, ws);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
 
-size_t distill_ws_bytes(int, int, int, int) { return 0; }
+size_t distill_ws_bytes(int dtype, int rows, int vocab, int) {
+  const Cut cut = dt_cut(dtype, rows, vocab);
+  if (cut.slices == 1) return 0;
+  const int batch = dt_batch(cut, rows, dtype == 0 ? tiles_of<0>(vocab) : tiles_of<1>(vocab));
+  return (size_t)batch * (cut.slices * sizeof(Sums) + sizeof(DtRow) + kMaxTop * sizeof(float));
+}
 
-hipError_t launch_distill(const DistillArgs& a, int dtype, void*, hipStream_t s) {
-  if (dtype == 0)
-    hipLaunchKernelGGL((distill_kernel<0>), dim3(a.rows), dim3(kDtBlock), 0, s, a);
-  else
-    hipLaunchKernelGGL((distill_kernel<1>), dim3(a.rows), dim3(kDtBlock), 0, s, a);
-  return hipGetLastError();
+hipError_t launch_distill(const DistillArgs& a, int dtype, void* ws, hipStream_t s) {
+  return dtype == 0 ? launch_dt<0>(a, ws, s) : launch_dt<1>(a, ws, s);
 }
 
 }  // namespace tsr

@@ -174,7 +174,7 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_slice_kernel(LogprobArgs 
   const long long r = blockIdx.x / cut.slices;
   Slice<DT, NC> s;
   s.template load<ONCE>(a.logits + r * a.stride_bytes, a.V, slice, cut);
-  const float m = s.largest(a.V);
+  const float m = s.largest();
   if constexpr (TOP) {
     const int j = (a.k + kSliceWaves - 1) / kSliceWaves;   // at most 16
     const uint32_t sorted = wave_sort_desc<64>(fkey(m));
@@ -182,8 +182,8 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_slice_kernel(LogprobArgs 
     if (__lane_id() == 0) bound[threadIdx.x / kWave] = jth;
   }
   float off;
-  const Sums mine = s.sums(a.V, m, a.c, off);
-  const Sums all = join_block(mine, a.c, off, each);
+  const Sums mine = s.template sums<true>(a.V, m, a.c, off);
+  const Sums all = join_block<kSliceWaves>(mine, a.c, off, each);
   if constexpr (TOP) {
     uint32_t tau = bound[0];
 #pragma unroll
@@ -213,17 +213,6 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_slice_kernel(LogprobArgs 
     for (int i = total + threadIdx.x; i < a.k; i += kSliceBlock) keys[i] = 0;
     rank_candidates(cands, a.k, [&](int rank, unsigned long long key) { keys[rank] = key; });
   }
-}
-
-// The sums of a row from its slices', by each wavefront for itself (64 slices at most).
-__device__ __forceinline__ Sums join_slices(const Sums* sums, int slices, float c) {
-  const int lane = __lane_id();
-  Sums one{kNegInf, 0.0, 0.0};
-  if (lane < slices) one = sums[lane];
-  rebase(one, wave_maxn(one.M), c, 0.0f);
-  one.Z = wave_sum(one.Z);
-  one.S = wave_sum(one.S);
-  return one;
 }
 
 // Without alternatives: one wavefront to a row.
@@ -277,8 +266,9 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_top_join_kernel(LogprobAr
 }
 
 // ------------------------------------------------------------ rows past the slices
-// Vocabularies that 64 slices do not hold (over 2^20 float32 or 2^21 bf16 ids): one
-// workgroup to a row, which it reads once for each sum and each alternative.
+// Alternatives of vocabularies whose slices have more than 2048 of them together (with 64
+// alternatives over 524288 float32 or 1048576 bf16 ids): one workgroup to a row, which it
+// reads once for each sum and each alternative.
 template <int DT>
 __global__ __launch_bounds__(kLpBlock) void logprob_wide_kernel(LogprobArgs a) {
   __shared__ BlockScratch scratch;
@@ -400,24 +390,15 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_grad_kernel(LogprobGradAr
 
 namespace {
 
-constexpr int kSlicesMost = 64;     // a lane of the joining wavefront each
 constexpr int kKeysMost = kJoinRegion * kSliceWaves;   // of a row's slices together
-constexpr int kBatchRows = 8192;    // rows whose slices are in the workspace at a time
 
 // How rows are cut (slices 0: not at all, the wide kernel).
 Cut lp_cut(int dtype, int rows, int vocab, int k) {
   const int whole = vocab / (dtype == 0 ? 4 : 8);
-  const int most = kMaxSlices16 * kSliceBlock;   // chunks of the largest slice
-  const int limit = k ? min(kSlicesMost, kKeysMost / k) : kSlicesMost;
-  Cut c{1, whole, 1};
-  if ((long long)whole > (long long)most * limit) return Cut{0, 0, 0};
-  int slices = max(1, (whole + most - 1) / most);
-  const int want = static_cast<int>(min(1024ll / max(rows, 1), 64ll));   // TUNE
-  slices = max(slices, std::min({want, limit, (whole + kSliceBlock - 1) / kSliceBlock}));
-  c.slices = slices;
-  c.per = (whole + slices - 1) / slices;
-  while (c.nc * kSliceBlock < c.per) c.nc *= 2;
-  return c;
+  int want = std::min({1024 / max(rows, 1), 64, (whole + kSliceBlock - 1) / kSliceBlock});   // TUNE
+  if (k) want = min(want, kKeysMost / k);
+  const Cut c = cut_of(whole, want);
+  return k && c.slices * (long long)k > kKeysMost ? Cut{0, 0, 0} : c;
 }
 
 template <int DT, bool TOP, bool ONCE>
@@ -439,9 +420,10 @@ hipError_t launch_dt(const LogprobArgs& all, void* workspace, hipStream_t s) {
     hipLaunchKernelGGL((logprob_wide_kernel<DT>), dim3(all.rows), dim3(kLpBlock), 0, s, all);
     return hipGetLastError();
   }
-  for (int r0 = 0; r0 < all.rows; r0 += kBatchRows) {
+  const int batch = batch_of(cut, all.rows);
+  for (int r0 = 0; r0 < all.rows; r0 += batch) {
     LogprobArgs a = all;
-    a.rows = min(kBatchRows, all.rows - r0);
+    a.rows = min(batch, all.rows - r0);
     a.logits += (long long)r0 * a.stride_bytes;
     if (a.tokens) a.tokens += (long long)r0 * a.n, a.logprob += (long long)r0 * a.n;
     if (a.entropy) a.entropy += r0;
@@ -474,7 +456,7 @@ hipError_t launch_dt(const LogprobArgs& all, void* workspace, hipStream_t s) {
 size_t logprobs_ws_bytes(int dtype, int rows, int vocab, int k) {
   const Cut cut = lp_cut(dtype, rows, vocab, k);
   if (cut.slices <= 1) return 0;
-  return (size_t)min(rows, kBatchRows) * cut.slices * (sizeof(Sums) + 8 * (size_t)k);
+  return (size_t)batch_of(cut, rows) * cut.slices * (sizeof(Sums) + 8 * (size_t)k);
 }
 
 hipError_t launch_logprobs(const LogprobArgs& a, int dtype, void* ws, hipStream_t s) {

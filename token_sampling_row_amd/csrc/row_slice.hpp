@@ -17,7 +17,6 @@ namespace tsr {
 
 constexpr int kSliceBlock = 256;
 constexpr int kSliceWaves = kSliceBlock / kWave;
-constexpr int kMaxSlices16 = 16;   // most 16-byte chunks a thread holds
 
 // How a row is cut: `slices` workgroups of up to `per` whole chunks each, `nc` to a
 // thread (the elements behind the last whole chunk go with the last slice).
@@ -42,6 +41,7 @@ __device__ __forceinline__ void rebase(Sums& a, float M, float c, float off) {
 }
 
 // The workgroup's sums from its threads'; `each` has a place for every wavefront.
+template <int WAVES>
 __device__ __forceinline__ Sums join_block(Sums a, float c, float off, Sums* each) {
   rebase(a, wave_maxn(a.M), c, off);
   a.Z = wave_sum(a.Z);
@@ -50,16 +50,50 @@ __device__ __forceinline__ Sums join_block(Sums a, float c, float off, Sums* eac
   __syncthreads();
   float M = each[0].M;
 #pragma unroll
-  for (int w = 1; w < kSliceWaves; ++w) M = fmaxn(M, each[w].M);
+  for (int w = 1; w < WAVES; ++w) M = fmaxn(M, each[w].M);
   Sums all{M, 0.0, 0.0};
 #pragma unroll
-  for (int w = 0; w < kSliceWaves; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     Sums one = each[w];
     rebase(one, M, c, 0.0f);
     all.Z += one.Z;
     all.S += one.S;
   }
   return all;
+}
+
+// The sums of a row from its slices', by each wavefront for itself.
+__device__ __forceinline__ Sums join_slices(const Sums* sums, int slices, float c) {
+  Sums one{kNegInf, 0.0, 0.0};
+  for (int i = __lane_id(); i < slices; i += kWave) {
+    Sums next = sums[i];
+    const float M = fmaxn(one.M, next.M);
+    rebase(one, M, c, 0.0f);
+    rebase(next, M, c, 0.0f);
+    one.Z += next.Z;
+    one.S += next.S;
+  }
+  rebase(one, wave_maxn(one.M), c, 0.0f);
+  one.Z = wave_sum(one.Z);
+  one.S = wave_sum(one.S);
+  return one;
+}
+
+constexpr int kMaxSliceChunks = 16 * kSliceBlock;   // of the largest slice, 16 a thread
+
+// A cut of rows of `whole` chunks into `slices` or as many as hold them.
+inline Cut cut_of(int whole, int slices) {
+  Cut c{slices, 0, 1};
+  const int least = (whole + kMaxSliceChunks - 1) / kMaxSliceChunks;
+  c.slices = least > slices ? least : slices < 1 ? 1 : slices;
+  c.per = (whole + c.slices - 1) / c.slices;
+  while (c.nc * kSliceBlock < c.per) c.nc *= 2;
+  return c;
+}
+// Rows whose slices are in the workspace at a time.
+inline int batch_of(const Cut& c, int rows) {
+  const int most = c.slices > 64 ? (1 << 19) / c.slices : 1 << 13;
+  return rows < most ? rows : most;
 }
 
 // The elements of a chunk as the pass sees them. Passes over the same registers unpack
@@ -94,7 +128,7 @@ __device__ __forceinline__ float max_of(const float* v) {
   return fmaxn(fmax3n(fmax3n(v[0], v[1], v[2]), v[3], v[4]), fmax3n(v[5], v[6], v[7]));
 }
 
-template <int DT, int NC>
+template <int DT, int NC, int BLOCK = kSliceBlock>
 struct Slice {
   static constexpr int EPC = Fmt<DT>::EPC;
   const unsigned char* row;
@@ -104,9 +138,11 @@ struct Slice {
   bool ragged;
 
   __device__ __forceinline__ int chunk_id(int j) const {
-    return lo + j * kSliceBlock + (int)threadIdx.x;
+    return lo + j * BLOCK + (int)threadIdx.x;
   }
 
+  // Loads are addressed from a uniform base; threads past the slice's last chunk repeat
+  // it, and `largest` puts -inf in its place.
   template <bool ONCE>
   __device__ __forceinline__ void load(const unsigned char* at, int V, int slice, const Cut& cut) {
     row = at;
@@ -114,15 +150,17 @@ struct Slice {
     lo = slice * cut.per;
     hi = min(lo + cut.per, whole);
     ragged = slice == cut.slices - 1 && whole * EPC < V;
+    const unsigned char* base =
+        whole > 0 ? row + (long long)min(lo, whole - 1) * 16
+                  : reinterpret_cast<const unsigned char*>(&g_neg_inf_chunk[DT]);
+    const uint32_t last = (uint32_t)max(hi - lo - 1, 0);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int i = chunk_id(j);
-      const void* p = i < hi ? static_cast<const void*>(row + (long long)i * 16)
-                             : static_cast<const void*>(&g_neg_inf_chunk[DT]);
+      const unsigned char* p = base + min((uint32_t)(j * BLOCK) + threadIdx.x, last) * 16u;
       c[j] = ONCE ? load16_once(p) : load16(p);
     }
     rest = neg_inf_chunk<DT>();
-    if (ragged && threadIdx.x == kSliceBlock - 1) rest = load_chunk_slow<DT>(row, whole, V);
+    if (ragged && threadIdx.x == BLOCK - 1) rest = load_chunk_slow<DT>(row, whole, V);
   }
 
   // f(values, number of the first) for each chunk of the thread
@@ -147,7 +185,7 @@ struct Slice {
   __device__ __forceinline__ void each_again(int V, F&& f) const {
     float v[EPC];
 #pragma unroll 1
-    for (int i = lo + (int)threadIdx.x; i < hi; i += kSliceBlock) {
+    for (int i = lo + (int)threadIdx.x; i < hi; i += BLOCK) {
       tsr::unpack<DT>(load16(row + (long long)i * 16), v);
       f(v, i * EPC);
     }
@@ -157,15 +195,85 @@ struct Slice {
     }
   }
 
-  __device__ __forceinline__ float largest(int V) const {
-    float m = kNegInf;
-    each(V, [&](const float* v, int) { m = fmaxn(m, max_of<DT>(v)); });
+  // Leaves the ids of a row's entries (one to a lane of every wavefront, -1: none) out of
+  // the slice: their logits become -inf. Eight bits a chunk, a thread's together.
+  struct LeftOut {
+    uint32_t word[BLOCK][(NC + 3) / 4];
+  };
+  __device__ __forceinline__ void leave_out(int V, int id, LeftOut& out) {
+    constexpr int W = (NC + 3) / 4;
+#pragma unroll
+    for (int w = 0; w < W; ++w) out.word[threadIdx.x][w] = 0;
+    __syncthreads();
+    const int q = id < 0 ? -1 : id / EPC - lo;
+    if (threadIdx.x < kWave && q >= 0 && q < hi - lo) {
+      const int j = q / BLOCK;
+      atomicOr(&out.word[q % BLOCK][j / 4], 1u << (8 * (j % 4) + id % EPC));
+    }
+    if (ragged) {   // behind the last whole chunk: with every wavefront's own ids
+      const int at = V / EPC * EPC;
+      uint32_t bits = 0;
+      unsigned long long who = __ballot(id >= at);
+      while (who) {
+        bits |= 1u << ((int)readlane_u32((uint32_t)id, __ffsll((long long)who) - 1) - at);
+        who &= who - 1;
+      }
+      drop(rest, bits);
+    }
+    __syncthreads();
+    uint32_t word[W], any = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) any |= word[w] = out.word[threadIdx.x][w];
+    if (!__any(any != 0)) return;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const uint32_t bits = word[j / 4] >> (8 * (j % 4)) & 255u;
+      if (__any(bits != 0)) drop(c[j], bits);
+    }
+  }
+  static __device__ __forceinline__ void drop(uint4& ch, uint32_t bits) {
+    uint32_t w[4] = {ch.x, ch.y, ch.z, ch.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == 0) {
+        w[i] = bits >> i & 1 ? 0xFF800000u : w[i];
+      } else {
+        w[i] = bits >> (2 * i) & 1 ? (w[i] & 0xFFFF0000u) | 0xFF80u : w[i];
+        w[i] = bits >> (2 * i + 1) & 1 ? (w[i] & 0xFFFFu) | 0xFF800000u : w[i];
+      }
+    }
+    ch = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+
+  // The thread's largest logit, NaN where it holds one.
+  __device__ __forceinline__ float largest() {
+    const Pass pass;
+    float v[EPC], m = kNegInf;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      if ((j + 1) * BLOCK > hi - lo) {   // the same for all threads
+        const uint4 none = neg_inf_chunk<DT>();
+        const bool in = chunk_id(j) < hi;
+        c[j].x = in ? c[j].x : none.x;
+        c[j].y = in ? c[j].y : none.y;
+        c[j].z = in ? c[j].z : none.z;
+        c[j].w = in ? c[j].w : none.w;
+      }
+      pass.unpack<DT>(c[j], v);
+      m = fmaxn(m, max_of<DT>(v));
+      sched_fence();
+    }
+    if (ragged) {
+      pass.unpack<DT>(rest, v);
+      m = fmaxn(m, max_of<DT>(v));
+    }
     return m;
   }
 
   // The thread's sums against its largest logit m (S in units of log 2) and what its
   // exponents are short of. Eight products at most are added in float32. Exponents are
   // held above -2000, where weights are 0: a logit of -inf gives 0 in S and not NaN.
+  template <bool WITH_S>
   __device__ __forceinline__ Sums sums(int V, float m, float c_log2, float& off) const {
     const float ref = m > kNegInf ? m : 0.0f;
     const float rc = ref * c_log2;
@@ -178,18 +286,21 @@ struct Slice {
         const float x = x_of(v[e]);
         const float w = __builtin_amdgcn_exp2f(x);
         z += w;
-        s = fmaf(w, x, s);
+        if constexpr (WITH_S) s = fmaf(w, x, s);
       }
       a.Z += (double)z;
-      a.S += (double)s;
+      if constexpr (WITH_S) a.S += (double)s;
     };
     if (fabsf(rc) <= 0x1p20f) {
       each(V, [&](const float* v, int) {
-        add(v, [&](float z) { return fmaxf(fmaf(z, c_log2, -rc), -2000.0f); });
+        add(v, [&](float z) {
+          const float x = fmaf(z, c_log2, -rc);
+          return WITH_S ? fmaxf(x, -2000.0f) : x;
+        });
       });
     } else {   // the rounding of m c is no small shift of the exponents
       off = 0.0f;
-      each_again(V, [&](const float* v, int) {
+      each(V, [&](const float* v, int) {
         add(v, [&](float z) { return exponent(z, ref, c_log2); });
       });
     }
