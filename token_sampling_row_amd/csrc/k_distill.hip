@@ -158,7 +158,7 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
   if (threadIdx.x < kWave) entries[threadIdx.x] = entries_of(a, id, t);   // the row is on its way
   if (a.tail) s.leave_out(a.V, valid_id(a, id), left_out);
   float off;
-  const float m = s.largest();
+  const float m = s.largest([](int, float) {});
   const Sums mine = s.template sums<false>(a.V, m, a.c, off);
   const Sums other = join_block<BLOCK / kWave>(mine, a.c, off, each);
   float own = 0.0f;   // the entry's gradient
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(kSliceBlock) void distill_slice_kernel(DistillArgs 
   s.template load<false>(a.logits + r * a.stride_bytes, a.V, slice, cut);
   if (a.tail) s.leave_out(a.V, id, left_out);
   float off;
-  const float m = s.largest();
+  const float m = s.largest([](int, float) {});
   const Sums mine = s.template sums<false>(a.V, m, a.c, off);
   const Sums all = join_block<kSliceWaves>(mine, a.c, off, each);
   if (threadIdx.x == 0) ws.sums[r * cut.slices + slice] = all;

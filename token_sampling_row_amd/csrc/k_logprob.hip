@@ -44,31 +44,80 @@ __device__ __forceinline__ void rank_candidates(const Candidates<REGION>& c, int
   }
 }
 
-// The slice's candidates. `tau`: the k largest of the slice are at least that (keys of
-// values). Every wavefront has seen j = ceil(k / 4) threads whose largest logit is at
-// least tau, so there are k such elements; there are few more.
+// Chunks of a slice that hold candidates, a region for each wavefront.
+constexpr int kHits = 64;
+template <int DT>
+struct Hits {
+  uint4 chunk[kSliceWaves][kHits];
+  int id[kSliceWaves][kHits];   // of the chunk's first element
+  int n[kSliceWaves];
+};
+
+// The slice's candidates: its logits of at least `tau` (a key of values), of which there
+// are k at least and few more: every wavefront has j = ceil(k / 4) threads whose largest
+// logit is at least that. `cmax`: the largest of each chunk. A wavefront lists its chunks
+// that hold any, and the workgroup then looks at their elements together: taken where
+// they lie, each chunk would cost its wavefront eight tests for one or two that pass.
 template <int DT, int NC>
-__device__ __forceinline__ void gather(const Slice<DT, NC>& s, int V, uint32_t tau, int k,
-                                       Candidates<kSliceRegion>& c, BlockScratch& scratch) {
+__device__ __forceinline__ void gather(const Slice<DT, NC>& s, int V, const float* cmax,
+                                       uint32_t tau, int k, Candidates<kSliceRegion>& c,
+                                       Hits<DT>& hits, BlockScratch& scratch) {
   constexpr int EPC = Fmt<DT>::EPC;
   const int wave = threadIdx.x / kWave;
   const float least = key2f(tau);
   int n = 0;
-  s.each(V, [&](const float* v, int id) {
-    if (!__any(max_of<DT>(v) >= least)) return;
+  const auto list = [&](float most, uint4 chunk, int id) {
+    const bool in = most >= least && most > kNegInf;
+    const unsigned long long who = __ballot(in);
+    if (who == 0) return;
+    const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+                                                 __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+    if (in && at < kHits) {
+      hits.chunk[wave][at] = chunk;
+      hits.id[wave][at] = id;
+    }
+    n += __popcll(who);
+  };
 #pragma unroll
-    for (int e = 0; e < EPC; ++e) {
-      const bool in = v[e] >= least && v[e] > kNegInf;
+  for (int j = 0; j < NC; ++j) list(cmax[j], s.c[j], s.chunk_id(j) * EPC);
+  if (s.ragged) list(cmax[NC], s.rest, V / EPC * EPC);
+  if (__lane_id() == 0) hits.n[wave] = n;
+  __syncthreads();
+  int count[kSliceWaves], total = 0, most = 0;
+#pragma unroll
+  for (int w = 0; w < kSliceWaves; ++w) {
+    total += count[w] = hits.n[w];
+    most = max(most, count[w]);
+  }
+  n = 0;
+  if (most <= kHits) {
+    for (int i0 = wave * kWave; i0 < total * EPC; i0 += kSliceBlock) {
+      const int i = i0 + (int)__lane_id();
+      int at = i / EPC, w = 0;
+      const int e = i % EPC;
+      while (w < kSliceWaves - 1 && at >= count[w]) at -= count[w++];
+      bool in = i < total * EPC;
+      float v = kNegInf;
+      if (in) {
+        if constexpr (DT == 0)
+          v = reinterpret_cast<const float*>(&hits.chunk[w][at])[e];
+        else
+          v = __uint_as_float(
+              (uint32_t) reinterpret_cast<const uint16_t*>(&hits.chunk[w][at])[e] << 16);
+      }
+      in = v >= least && v > kNegInf;
       const unsigned long long who = __ballot(in);
-      const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+      const int to = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
                                                    __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-      if (in && at < kSliceRegion) c.key[wave][at] = top_key(v[e], id + e);
+      if (in && to < kSliceRegion) c.key[wave][to] = top_key(v, hits.id[w][at] + e);
       n += __popcll(who);
     }
-  });
+  } else {
+    n = kSliceRegion + 1;
+  }
   if (__lane_id() == 0) c.n[wave] = n;
   __syncthreads();
-  int most = 0;
+  most = 0;
 #pragma unroll
   for (int w = 0; w < kSliceWaves; ++w) most = max(most, c.n[w]);
   if (most <= kSliceRegion) return;
@@ -169,16 +218,16 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_slice_kernel(LogprobArgs 
   __shared__ Sums each[kSliceWaves];
   __shared__ uint32_t bound[kSliceWaves];
   __shared__ typename std::conditional<TOP, Candidates<kSliceRegion>, int>::type cands;
+  __shared__ typename std::conditional<TOP, Hits<DT>, int>::type hits;
   __shared__ typename std::conditional<TOP, BlockScratch, int>::type scratch;
   const int slice = blockIdx.x % cut.slices;
   const long long r = blockIdx.x / cut.slices;
   Slice<DT, NC> s;
   s.template load<ONCE>(a.logits + r * a.stride_bytes, a.V, slice, cut);
-  const float m = s.largest();
-  if constexpr (TOP) {
-    const int j = (a.k + kSliceWaves - 1) / kSliceWaves;   // at most 16
-    const uint32_t sorted = wave_sort_desc<64>(fkey(m));
-    const uint32_t jth = readlane_u32(sorted, j - 1);
+  float cmax[NC + 1];
+  const float m = s.largest([&](int j, float most) { cmax[j] = most; });
+  if constexpr (TOP) {   // bf16 values have 16 bits; of float32 ones as many do
+    const uint32_t jth = jth_largest<16>(fkey(m), (a.k + kSliceWaves - 1) / kSliceWaves);
     if (__lane_id() == 0) bound[threadIdx.x / kWave] = jth;
   }
   float off;
@@ -188,8 +237,9 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_slice_kernel(LogprobArgs 
     uint32_t tau = bound[0];
 #pragma unroll
     for (int w = 1; w < kSliceWaves; ++w) tau = min(tau, bound[w]);
+    tau = max(tau, kKeyNegInf);   // cut short, a key of -inf is one of NaN
     if (all.M == all.M)
-      gather(s, a.V, tau, a.k, cands, scratch);
+      gather(s, a.V, cmax, tau, a.k, cands, hits, scratch);
     else if (threadIdx.x < kSliceWaves)
       cands.n[threadIdx.x] = 0;
   }

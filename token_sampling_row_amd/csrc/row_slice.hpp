@@ -219,8 +219,10 @@ struct Slice {
     ch = make_uint4(w[0], w[1], w[2], w[3]);
   }
 
-  // The thread's largest logit, NaN where it holds one.
-  __device__ __forceinline__ float largest() {
+  // The thread's largest logit, NaN where it holds one; of(j, largest of chunk j) for each
+  // (j = NC: the elements behind the last whole chunk).
+  template <class F>
+  __device__ __forceinline__ float largest(F&& of) {
     const Pass pass;
     float v[EPC], m = kNegInf;
 #pragma unroll
@@ -234,27 +236,32 @@ struct Slice {
         c[j].w = in ? c[j].w : none.w;
       }
       pass.unpack<DT>(c[j], v);
-      m = fmaxn(m, max_of<DT>(v));
+      const float most = max_of<DT>(v);
+      of(j, most);
+      m = fmaxn(m, most);
       sched_fence();
     }
+    float most = kNegInf;
     if (ragged) {
       pass.unpack<DT>(rest, v);
-      m = fmaxn(m, max_of<DT>(v));
+      most = max_of<DT>(v);
     }
-    return m;
+    of(NC, most);
+    return fmaxn(m, most);
   }
 
   // The thread's sums against its largest logit m (S in units of log 2) and what its
-  // exponents are short of. Eight products at most are added in float32. Exponents are
+  // exponents are short of. Sixteen products at most are added in float32. Exponents are
   // held above -2000, where weights are 0: a logit of -inf gives 0 in S and not NaN.
   template <bool WITH_S>
   __device__ __forceinline__ Sums sums(int V, float m, float c_log2, float& off) const {
+    constexpr int GROUP = 16 / EPC;   // chunks whose products are added in float32
     const float ref = m > kNegInf ? m : 0.0f;
     const float rc = ref * c_log2;
     off = -fmaf(ref, c_log2, -rc);
     Sums a{m, 0.0, 0.0};
+    float z = 0.0f, s = 0.0f;
     const auto add = [&](const float* v, auto&& x_of) {
-      float z = 0.0f, s = 0.0f;
 #pragma unroll
       for (int e = 0; e < EPC; ++e) {
         const float x = x_of(v[e]);
@@ -262,24 +269,54 @@ struct Slice {
         z += w;
         if constexpr (WITH_S) s = fmaf(w, x, s);
       }
+    };
+    const auto flush = [&] {
       a.Z += (double)z;
       if constexpr (WITH_S) a.S += (double)s;
+      z = s = 0.0f;
     };
     if (fabsf(rc) <= 0x1p20f) {
-      each(V, [&](const float* v, int) {
-        add(v, [&](float z) {
-          const float x = fmaf(z, c_log2, -rc);
-          return WITH_S ? fmaxf(x, -2000.0f) : x;
-        });
-      });
+      const auto x_of = [&](float v) {
+        const float x = fmaf(v, c_log2, -rc);
+        return WITH_S ? fmaxf(x, -2000.0f) : x;
+      };
+      const Pass pass;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        float v[EPC];
+        pass.unpack<DT>(c[j], v);
+        add(v, x_of);
+        if (j % GROUP == GROUP - 1) flush();
+        sched_fence();
+      }
+      if (NC % GROUP) flush();
+      if (ragged) {
+        float v[EPC];
+        pass.unpack<DT>(rest, v);
+        add(v, x_of);
+        flush();
+      }
     } else {   // the rounding of m c is no small shift of the exponents
       off = 0.0f;
       each(V, [&](const float* v, int) {
-        add(v, [&](float z) { return exponent(z, ref, c_log2); });
+        add(v, [&](float y) { return exponent(y, ref, c_log2); });
+        flush();
       });
     }
     return a;
   }
 };
+
+// The j-th largest of a wavefront's keys, or less: its first BITS bits and zeros.
+template <int BITS>
+__device__ __forceinline__ uint32_t jth_largest(uint32_t key, int j) {
+  uint32_t found = 0;
+#pragma unroll
+  for (int b = 31; b > 31 - BITS; --b) {
+    const uint32_t more = found | 1u << b;
+    if (__popcll(__ballot(key >= more)) >= j) found = more;
+  }
+  return found;
+}
 
 }  // namespace tsr

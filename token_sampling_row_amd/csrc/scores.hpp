@@ -46,6 +46,7 @@ __device__ __forceinline__ float log_prob(float v, float M, double logZ, double 
   return (float)(((double)v - (double)M) * inv_t - logZ);
 }
 
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;   // fkey(-inf)
 // Keys of ids that order as (value, then the lower id) do; 0 is below all of them.
 __device__ __forceinline__ unsigned long long top_key(float v, int id) {
   return ((unsigned long long)fkey(v) << 32) | (0xFFFFFFFFu - (uint32_t)id);
