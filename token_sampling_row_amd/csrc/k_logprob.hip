@@ -16,34 +16,13 @@ namespace {
 constexpr int kLpBlock = 256;
 
 // ------------------------------------------------------------ the likeliest ids
-// Keys of ids that may be among the k largest, in a region of LDS for each wavefront.
-template <int REGION>
+// Keys of ids that may be among the k largest of a slice, in any order: more than kKeys
+// are not kept.
+constexpr int kKeys = 256;
 struct Candidates {
-  unsigned long long key[kSliceWaves][REGION];
-  int n[kSliceWaves];
+  unsigned long long key[kKeys];
+  int n;
 };
-constexpr int kSliceRegion = 128;   // keys of a wavefront in a slice
-constexpr int kJoinRegion = 512;    // and of one that joins slices
-
-// put(rank, key) for each candidate that fewer than k exceed. Keys differ, so ranks do.
-template <int REGION, class F>
-__device__ __forceinline__ void rank_candidates(const Candidates<REGION>& c, int k, F&& put) {
-  int n[kSliceWaves], total = 0;
-#pragma unroll
-  for (int w = 0; w < kSliceWaves; ++w) total += n[w] = c.n[w];
-  for (int i = threadIdx.x; i < total; i += kSliceBlock) {
-    int w = 0, at = i;
-    while (at >= n[w]) at -= n[w++];
-    const unsigned long long mine = c.key[w][at];
-    int rank = 0;
-#pragma unroll
-    for (int v = 0; v < kSliceWaves; ++v)
-#pragma unroll 4
-      for (int q = 0; q < n[v]; ++q) rank += c.key[v][q] > mine;
-    if (rank < k) put(rank, mine);
-  }
-}
-
 // Chunks of a slice that hold candidates, a region for each wavefront.
 constexpr int kHits = 64;
 template <int DT>
@@ -53,15 +32,33 @@ struct Hits {
   int n[kSliceWaves];
 };
 
+__device__ __forceinline__ int lanes_below(unsigned long long who) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+                                   __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+}
+
+// put(rank, key) for each candidate that fewer than k exceed. Keys differ, so ranks do.
+template <class F>
+__device__ __forceinline__ void rank_candidates(const Candidates& c, int k, F&& put) {
+  const int n = c.n;
+  if ((int)threadIdx.x >= n) return;
+  const unsigned long long mine = c.key[threadIdx.x];
+  int rank = 0;
+#pragma unroll 4
+  for (int q = 0; q < n; ++q) rank += c.key[q] > mine;
+  if (rank < k) put(rank, mine);
+}
+
 // The slice's candidates: its logits of at least `tau` (a key of values), of which there
 // are k at least and few more: every wavefront has j = ceil(k / 4) threads whose largest
 // logit is at least that. `cmax`: the largest of each chunk. A wavefront lists its chunks
 // that hold any, and the workgroup then looks at their elements together: taken where
 // they lie, each chunk would cost its wavefront eight tests for one or two that pass.
+// c.n is 0 before the call.
 template <int DT, int NC>
 __device__ __forceinline__ void gather(const Slice<DT, NC>& s, int V, const float* cmax,
-                                       uint32_t tau, int k, Candidates<kSliceRegion>& c,
-                                       Hits<DT>& hits, BlockScratch& scratch) {
+                                       uint32_t tau, int k, Candidates& c, Hits<DT>& hits,
+                                       BlockScratch& scratch) {
   constexpr int EPC = Fmt<DT>::EPC;
   const int wave = threadIdx.x / kWave;
   const float least = key2f(tau);
@@ -70,8 +67,7 @@ __device__ __forceinline__ void gather(const Slice<DT, NC>& s, int V, const floa
     const bool in = most >= least && most > kNegInf;
     const unsigned long long who = __ballot(in);
     if (who == 0) return;
-    const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
-                                                 __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+    const int at = n + lanes_below(who);
     if (in && at < kHits) {
       hits.chunk[wave][at] = chunk;
       hits.id[wave][at] = id;
@@ -89,41 +85,33 @@ __device__ __forceinline__ void gather(const Slice<DT, NC>& s, int V, const floa
     total += count[w] = hits.n[w];
     most = max(most, count[w]);
   }
-  n = 0;
   if (most <= kHits) {
     for (int i0 = wave * kWave; i0 < total * EPC; i0 += kSliceBlock) {
       const int i = i0 + (int)__lane_id();
       int at = i / EPC, w = 0;
       const int e = i % EPC;
       while (w < kSliceWaves - 1 && at >= count[w]) at -= count[w++];
-      bool in = i < total * EPC;
       float v = kNegInf;
-      if (in) {
+      if (i < total * EPC) {
         if constexpr (DT == 0)
           v = reinterpret_cast<const float*>(&hits.chunk[w][at])[e];
         else
           v = __uint_as_float(
               (uint32_t) reinterpret_cast<const uint16_t*>(&hits.chunk[w][at])[e] << 16);
       }
-      in = v >= least && v > kNegInf;
+      const bool in = v >= least && v > kNegInf;
       const unsigned long long who = __ballot(in);
-      const int to = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
-                                                   __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-      if (in && to < kSliceRegion) c.key[wave][to] = top_key(v, hits.id[w][at] + e);
-      n += __popcll(who);
+      int first = 0;
+      if (__lane_id() == 0) first = atomicAdd(&c.n, (int)__popcll(who));
+      const int to = __builtin_amdgcn_readfirstlane(first) + lanes_below(who);
+      if (in && to < kKeys) c.key[to] = top_key(v, hits.id[w][at] + e);
     }
-  } else {
-    n = kSliceRegion + 1;
+    __syncthreads();
+    if (c.n <= kKeys) return;
+    __syncthreads();
   }
-  if (__lane_id() == 0) c.n[wave] = n;
-  __syncthreads();
-  most = 0;
-#pragma unroll
-  for (int w = 0; w < kSliceWaves; ++w) most = max(most, c.n[w]);
-  if (most <= kSliceRegion) return;
   // Too many (equal logits, or the largest with few threads): one at a time. Each thread
   // keeps its largest key below those taken, and looks for its next when it is taken.
-  __syncthreads();
   unsigned long long best = 0, last = ~0ull;
   int taken = 0;
   for (int i = 0; i < k; ++i) {
@@ -139,14 +127,14 @@ __device__ __forceinline__ void gather(const Slice<DT, NC>& s, int V, const floa
     }
     const unsigned long long top = block_max_u64<kSliceBlock>(best, scratch);
     if (top == 0) break;
-    if (threadIdx.x == 0) c.key[0][i] = top;
+    if (threadIdx.x == 0) c.key[i] = top;
     ++taken;
     if (best == top) {
       last = top;
       best = 0;
     }
   }
-  if (threadIdx.x < kSliceWaves) c.n[threadIdx.x] = threadIdx.x == 0 ? taken : 0;
+  if (threadIdx.x == 0) c.n = taken;
   __syncthreads();
 }
 
@@ -155,27 +143,44 @@ __device__ __forceinline__ int row_status(float M) {
   return M == kNegInf ? 2 : !(M < kPosInf) ? 1 : 0;
 }
 
-// Everything of row r but its alternatives, by T threads. Every thread of the wavefronts
-// that call this has the row's sums.
-template <int DT, int T>
+// The lane's first token of row r and its logit, loaded ahead of their use.
+struct Given {
+  int id;
+  float z;
+};
+template <int DT>
+__device__ __forceinline__ Given first_token(const LogprobArgs& a, long long r) {
+  Given g{-1, 0.0f};
+  if ((int)__lane_id() < a.n) {
+    g.id = a.tokens[r * a.n + __lane_id()];
+    if (g.id >= 0 && g.id < a.V) g.z = load_elem<DT>(a.logits + r * a.stride_bytes, g.id);
+  }
+  return g;
+}
+
+// Everything of row r but its alternatives, by one wavefront.
+template <int DT>
 __device__ __forceinline__ void put_row(const LogprobArgs& a, long long r, const Sums& all,
-                                        double logZ, int t) {
+                                        double logZ, Given g) {
   const unsigned char* row = a.logits + r * a.stride_bytes;
-  const int status = row_status(all.M);
+  const int status = row_status(all.M), lane = __lane_id();
   const float nan = __uint_as_float(0x7FC00000u);
   bool bad = false;
-  for (int i = t; i < a.n; i += T) {
-    const int id = a.tokens[r * a.n + i];
+  for (int i = lane; i < a.n; i += kWave) {
+    if (i != lane) {
+      g.id = a.tokens[r * a.n + i];
+      if (g.id >= 0 && g.id < a.V) g.z = load_elem<DT>(row, g.id);
+    }
     float lp = 0.0f;
-    if (id != -1) {
-      const bool in = id >= 0 && id < a.V;
+    if (g.id != -1) {
+      const bool in = g.id >= 0 && g.id < a.V;
       bad |= !in;
-      lp = in && !status ? log_prob(load_elem<DT>(row, id), all.M, logZ, a.inv_t) : nan;
+      lp = in && !status ? log_prob(g.z, all.M, logZ, a.inv_t) : nan;
     }
     a.logprob[r * a.n + i] = lp;
   }
   const bool any_bad = __any(bad);
-  if (t == 0) {
+  if (lane == 0) {
     if (a.entropy) a.entropy[r] = status ? nan : (float)(logZ - all.S / all.Z * kLn2);
     if (a.norm) {
       a.norm[2 * r] = status ? nan : all.M;
@@ -185,30 +190,20 @@ __device__ __forceinline__ void put_row(const LogprobArgs& a, long long r, const
   }
 }
 
-// The k alternatives from the candidates.
-template <int REGION>
-__device__ __forceinline__ void put_top(const LogprobArgs& a, long long r, const Sums& all,
-                                        double logZ, const Candidates<REGION>& c) {
-  const int status = row_status(all.M);
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < kSliceWaves; ++w) total += c.n[w];
-  if (status) total = 0;
-  for (int i = total + threadIdx.x; i < a.k; i += kSliceBlock) {   // positions past the last
-    a.top_ids[r * a.k + i] = -1;
-    a.top_logprob[r * a.k + i] = status ? __uint_as_float(0x7FC00000u) : kNegInf;
-  }
-  if (status) return;
-  rank_candidates(c, a.k, [&](int rank, unsigned long long key) {
-    a.top_ids[r * a.k + rank] = top_id(key);
-    a.top_logprob[r * a.k + rank] = log_prob(top_value(key), all.M, logZ, a.inv_t);
-  });
+// Position `i` of row r's alternatives (key 0: there is none).
+__device__ __forceinline__ void put_top(const LogprobArgs& a, long long r, int i,
+                                        unsigned long long key, const Sums& all, double logZ) {
+  const float none = row_status(all.M) ? __uint_as_float(0x7FC00000u) : kNegInf;
+  a.top_ids[r * a.k + i] = key ? top_id(key) : -1;
+  a.top_logprob[r * a.k + i] = key ? log_prob(top_value(key), all.M, logZ, a.inv_t) : none;
 }
 
-// Workspace: each slice's sums, then each slice's k largest keys, largest first.
+// Workspace: each slice's sums, how many candidates it has, and the candidates' keys.
 struct LpWs {
   Sums* sums;                  // [rows][slices]
-  unsigned long long* keys;    // [rows][slices][k]
+  unsigned long long* keys;    // [rows][slices][cap], cap 64 or 128
+  int2* count;                 // [rows][slices]: how many, and a bound that k of them reach
+  int cap;
 };
 
 // One workgroup to a slice of a row; with one slice it is the whole row's.
@@ -217,51 +212,56 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_slice_kernel(LogprobArgs 
                                                                     LpWs ws) {
   __shared__ Sums each[kSliceWaves];
   __shared__ uint32_t bound[kSliceWaves];
-  __shared__ typename std::conditional<TOP, Candidates<kSliceRegion>, int>::type cands;
+  __shared__ typename std::conditional<TOP, Candidates, int>::type cands;
   __shared__ typename std::conditional<TOP, Hits<DT>, int>::type hits;
   __shared__ typename std::conditional<TOP, BlockScratch, int>::type scratch;
   const int slice = blockIdx.x % cut.slices;
   const long long r = blockIdx.x / cut.slices;
   Slice<DT, NC> s;
   s.template load<ONCE>(a.logits + r * a.stride_bytes, a.V, slice, cut);
+  Given given;
+  if (cut.slices == 1 && threadIdx.x < kWave) given = first_token<DT>(a, r);
   float cmax[NC + 1];
   const float m = s.largest([&](int j, float most) { cmax[j] = most; });
   if constexpr (TOP) {   // bf16 values have 16 bits; of float32 ones as many do
     const uint32_t jth = jth_largest<16>(fkey(m), (a.k + kSliceWaves - 1) / kSliceWaves);
     if (__lane_id() == 0) bound[threadIdx.x / kWave] = jth;
+    if (threadIdx.x == 0) cands.n = 0;
   }
   float off;
   const Sums mine = s.template sums<true>(a.V, m, a.c, off);
   const Sums all = join_block<kSliceWaves>(mine, a.c, off, each);
+  uint32_t tau = 0;
   if constexpr (TOP) {
-    uint32_t tau = bound[0];
+    tau = bound[0];
 #pragma unroll
     for (int w = 1; w < kSliceWaves; ++w) tau = min(tau, bound[w]);
     tau = max(tau, kKeyNegInf);   // cut short, a key of -inf is one of NaN
-    if (all.M == all.M)
-      gather(s, a.V, cmax, tau, a.k, cands, hits, scratch);
-    else if (threadIdx.x < kSliceWaves)
-      cands.n[threadIdx.x] = 0;
+    if (row_status(all.M) == 0) gather(s, a.V, cmax, tau, a.k, cands, hits, scratch);
   }
   if (cut.slices == 1) {
     const double logZ = log(all.Z);
-    if (threadIdx.x < kWave) put_row<DT, kWave>(a, r, all, logZ, threadIdx.x);
+    if (threadIdx.x < kWave) put_row<DT>(a, r, all, logZ, given);
     if constexpr (TOP) {
-      __syncthreads();
-      put_top(a, r, all, logZ, cands);
+      for (int i = cands.n + (int)threadIdx.x; i < a.k; i += kSliceBlock)
+        put_top(a, r, i, 0, all, logZ);   // past the last
+      rank_candidates(cands, a.k, [&](int rank, unsigned long long key) {
+        put_top(a, r, rank, key, all, logZ);
+      });
     }
     return;
   }
   const long long at = r * cut.slices + slice;
   if (threadIdx.x == 0) ws.sums[at] = all;
   if constexpr (TOP) {
-    __syncthreads();
-    unsigned long long* keys = ws.keys + at * a.k;
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < kSliceWaves; ++w) total += cands.n[w];
-    for (int i = total + threadIdx.x; i < a.k; i += kSliceBlock) keys[i] = 0;
-    rank_candidates(cands, a.k, [&](int rank, unsigned long long key) { keys[rank] = key; });
+    unsigned long long* keys = ws.keys + at * ws.cap;
+    const int n = cands.n;
+    if (threadIdx.x == 0) ws.count[at] = make_int2(n <= ws.cap ? n : a.k, (int)tau);
+    if (n <= ws.cap) {
+      if ((int)threadIdx.x < n) keys[threadIdx.x] = cands.key[threadIdx.x];
+    } else {
+      rank_candidates(cands, a.k, [&](int rank, unsigned long long key) { keys[rank] = key; });
+    }
   }
 }
 
@@ -271,54 +271,108 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_join_kernel(LogprobArgs a
                                                                    LpWs ws) {
   const long long r = (long long)blockIdx.x * kSliceWaves + threadIdx.x / kWave;
   if (r >= a.rows) return;
+  const Given given = first_token<DT>(a, r);
   const Sums all = join_slices(ws.sums + r * slices, slices, a.c);
-  put_row<DT, kWave>(a, r, all, log(all.Z), __lane_id());
+  put_row<DT>(a, r, all, log(all.Z), given);
 }
 
-// With alternatives: one workgroup to a row. Each slice's j = ceil(k / slices) largest
-// are k ids together, so the smallest of the slices' j-th keys bounds the k largest.
-template <int DT>
+// With alternatives: one wavefront to a row, EACH of its slices' candidates to a lane. The
+// k-th largest is found bit by bit, by counting those that are no smaller; what is left
+// (k, and equal values at the end) goes to the lanes and is sorted.
+template <int DT, int EACH>
 __global__ __launch_bounds__(kSliceBlock) void logprob_top_join_kernel(LogprobArgs a, int slices,
                                                                        LpWs ws) {
-  __shared__ Candidates<kJoinRegion> cands;
-  constexpr int EACH = kJoinRegion / kWave;   // keys to a thread
-  const long long r = blockIdx.x;
+  __shared__ unsigned long long kept[kSliceWaves][2 * kWave];
   const int lane = __lane_id(), wave = threadIdx.x / kWave;
-  const unsigned long long* keys = ws.keys + r * slices * a.k;
-  const int j = (a.k + slices - 1) / slices;
-  unsigned long long tau = ~0ull;
-  if (lane < slices) tau = keys[lane * a.k + j - 1];
-  unsigned long long mine[EACH];
-  const int total = slices * a.k;
+  const long long r = (long long)blockIdx.x * kSliceWaves + wave;
+  if (r >= a.rows) return;
+  int2 count = make_int2(0, 0);
+  if (lane < slices) count = ws.count[r * slices + lane];   // 32 at most
+  const unsigned long long* keys = ws.keys + r * slices * ws.cap;
+  const int slots = slices * ws.cap;
+  unsigned long long key[EACH];
 #pragma unroll
-  for (int q = 0; q < EACH; ++q) {
-    const int i = q * kSliceBlock + (int)threadIdx.x;
-    mine[q] = i < total ? keys[i] : 0;
-  }
+  for (int q = 0; q < EACH; ++q) key[q] = q * kWave < slots ? keys[q * kWave + lane] : 0;
+  const Given given = first_token<DT>(a, r);
   const Sums all = join_slices(ws.sums + r * slices, slices, a.c);
-  const double logZ = log(all.Z);
-  tau = wave_reduce(tau, [](unsigned long long x, unsigned long long y) { return x < y ? x : y; });
+  const bool fine = row_status(all.M) == 0;
+  const int part = ws.cap / kWave;   // 1 or 2
+  int total = 0;
+#pragma unroll
+  for (int q = 0; q < EACH; ++q) {   // places that hold no candidate
+    const int slice = part == 1 ? q : q / 2, at = part == 1 ? 0 : q % 2 * kWave;
+    const int n = slice < slices ? (int)readlane_u32((uint32_t)count.x, slice) - at : 0;
+    if (lane >= n || !fine) key[q] = 0;
+    total += min(max(n, 0), kWave);
+  }
+  const int need = fine ? min(a.k, total) : 0;
+  const auto how_many = [&](unsigned long long least) {
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < EACH; ++q) n += __popcll(__ballot(key[q] >= least));
+    return n;
+  };
+  unsigned long long least = 1;   // every key, where there are no more than k
+  if (total > need && fine) {
+    // between the largest of the slices' bounds, which k reach, and the largest logit: the
+    // bits that these share are the k-th largest's. Keys of bf16 values differ in their
+    // upper 16 bits.
+    const uint32_t from = max(wave_max_u32((uint32_t)count.y), 1u), to = fkey(all.M);
+    constexpr int LAST = DT == 1 ? 16 : 0;
+    int b = 31 - (int)__clz((int)(from ^ to));   // -1: they are equal
+    uint32_t found = b >= 0 ? from >> b >> 1 << b << 1 : from;
+    if (DT == 1) found &= 0xFFFF0000u;
+#pragma unroll 1
+    for (; b >= LAST; --b) {
+      const uint32_t more = found | 1u << b;
+      const int n = how_many((unsigned long long)more << 32);
+      if (n >= need) found = more;
+      if (n == need) break;
+    }
+    least = (unsigned long long)found << 32;
+    if (how_many(least) > 2 * kWave) {   // so many equal values: the lower ids of them
+#pragma unroll 1
+      for (b = 31; b >= 0; --b) {
+        const unsigned long long more = least | 1ull << b;
+        if (how_many(more) >= need) least = more;
+      }
+    }
+  }
   int n = 0;
 #pragma unroll
   for (int q = 0; q < EACH; ++q) {
-    const bool in = mine[q] != 0 && mine[q] >= tau;
+    const bool in = key[q] >= least && key[q] != 0;
     const unsigned long long who = __ballot(in);
-    if (in)
-      cands.key[wave][n + __builtin_amdgcn_mbcnt_hi(
-                              (uint32_t)(who >> 32),
-                              __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0))] = mine[q];
+    if (in) kept[wave][n + lanes_below(who)] = key[q];
     n += __popcll(who);
   }
-  if (lane == 0) cands.n[wave] = n;
-  if (wave == kSliceWaves - 1) put_row<DT, kWave>(a, r, all, logZ, lane);
-  __syncthreads();
-  put_top(a, r, all, logZ, cands);
+  const double logZ = log(all.Z);
+  put_row<DT>(a, r, all, logZ, given);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  unsigned long long sorted = wave_sort_desc<64>(lane < n ? kept[wave][lane] : 0ull);
+  if (n > kWave) {
+    // the larger of the i-th here and the 63 - i-th there: the 64 largest of both, in an
+    // order that one merge sorts
+    const unsigned long long more =
+        wave_sort_desc<64>(lane < n - kWave ? kept[wave][kWave + lane] : 0ull);
+    const unsigned long long turned =
+        (unsigned long long)lane_mirror<64>((uint32_t)(more >> 32)) << 32 |
+        lane_mirror<64>((uint32_t)more);
+    sorted = turned > sorted ? turned : sorted;
+    sorted = cx_layer<32, false>(sorted);
+    sorted = cx_layer<16, false>(sorted);
+    sorted = cx_layer<8, false>(sorted);
+    sorted = cx_layer<4, false>(sorted);
+    sorted = cx_layer<2, false>(sorted);
+    sorted = cx_layer<1, false>(sorted);
+  }
+  if (lane < a.k) put_top(a, r, lane, sorted, all, logZ);
 }
 
 // ------------------------------------------------------------ rows past the slices
-// Alternatives of vocabularies whose slices have more than 2048 of them together (with 64
-// alternatives over 524288 float32 or 1048576 bf16 ids): one workgroup to a row, which it
-// reads once for each sum and each alternative.
+// Alternatives of vocabularies of more slices than their candidates' places hold (more
+// than 40 alternatives: over 262144 float32 or 524288 bf16 ids; fewer: twice as many): one
+// workgroup to a row, which it reads once for each sum and each alternative.
 template <int DT>
 __global__ __launch_bounds__(kLpBlock) void logprob_wide_kernel(LogprobArgs a) {
   __shared__ BlockScratch scratch;
@@ -440,15 +494,39 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_grad_kernel(LogprobGradAr
 
 namespace {
 
-constexpr int kKeysMost = kJoinRegion * kSliceWaves;   // of a row's slices together
+constexpr int kSlotsMost = 2048;   // places for candidates of a row's slices: 32 a lane
+
+// Places for a slice's candidates: some half more than k come as a rule.
+int cap_of(int k) { return k == 0 ? 0 : k <= 40 ? kWave : 2 * kWave; }
 
 // How rows are cut (slices 0: not at all, the wide kernel).
 Cut lp_cut(int dtype, int rows, int vocab, int k) {
   const int whole = vocab / (dtype == 0 ? 4 : 8);
   int want = std::min({1024 / max(rows, 1), 64, (whole + kSliceBlock - 1) / kSliceBlock});   // TUNE
-  if (k) want = min(want, kKeysMost / k);
+  if (k) want = min(want, 1024 / cap_of(k));
   const Cut c = cut_of(whole, want);
-  return k && c.slices * (long long)k > kKeysMost ? Cut{0, 0, 0} : c;
+  return k && c.slices > kSlotsMost / cap_of(k) ? Cut{0, 0, 0} : c;
+}
+
+// Places in the workspace for a batch of rows.
+size_t lp_bytes(const Cut& cut, int rows, int k) {
+  return (size_t)rows * cut.slices *
+         (sizeof(Sums) + (size_t)cap_of(k) * 8 + (k ? sizeof(int2) : 0));
+}
+
+template <int DT>
+void launch_top_join(const LogprobArgs& a, int slices, const LpWs& ws, hipStream_t s) {
+  const dim3 grid((a.rows + kSliceWaves - 1) / kSliceWaves), block(kSliceBlock);
+  const auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, slices, ws);
+  };
+  const int each = slices * ws.cap / kWave;
+  if (each <= 4) return launch(logprob_top_join_kernel<DT, 4>);
+  if (each <= 6) return launch(logprob_top_join_kernel<DT, 6>);
+  if (each <= 8) return launch(logprob_top_join_kernel<DT, 8>);
+  if (each <= 10) return launch(logprob_top_join_kernel<DT, 10>);
+  if (each <= 16) return launch(logprob_top_join_kernel<DT, 16>);
+  launch(logprob_top_join_kernel<DT, 32>);
 }
 
 template <int DT, bool TOP, bool ONCE>
@@ -480,8 +558,12 @@ hipError_t launch_dt(const LogprobArgs& all, void* workspace, hipStream_t s) {
     if (a.k) a.top_ids += (long long)r0 * a.k, a.top_logprob += (long long)r0 * a.k;
     if (a.norm) a.norm += 2ll * r0;
     if (a.status) a.status += r0;
-    LpWs ws{static_cast<Sums*>(workspace), nullptr};
-    ws.keys = reinterpret_cast<unsigned long long*>(ws.sums + (long long)a.rows * cut.slices);
+    LpWs ws;
+    const long long slots = (long long)a.rows * cut.slices;
+    ws.cap = cap_of(a.k);
+    ws.sums = static_cast<Sums*>(workspace);
+    ws.keys = reinterpret_cast<unsigned long long*>(ws.sums + slots);
+    ws.count = reinterpret_cast<int2*>(ws.keys + slots * ws.cap);
     if (a.k)
       launch_slices<DT, true, false>(a, cut, ws, s);
     else
@@ -490,8 +572,7 @@ hipError_t launch_dt(const LogprobArgs& all, void* workspace, hipStream_t s) {
     if (e != hipSuccess) return e;
     if (cut.slices == 1) continue;
     if (a.k)
-      hipLaunchKernelGGL((logprob_top_join_kernel<DT>), dim3(a.rows), dim3(kSliceBlock), 0, s, a,
-                         cut.slices, ws);
+      launch_top_join<DT>(a, cut.slices, ws, s);
     else
       hipLaunchKernelGGL((logprob_join_kernel<DT>), dim3((a.rows + kSliceWaves - 1) / kSliceWaves),
                          dim3(kSliceBlock), 0, s, a, cut.slices, ws);
@@ -506,7 +587,7 @@ hipError_t launch_dt(const LogprobArgs& all, void* workspace, hipStream_t s) {
 size_t logprobs_ws_bytes(int dtype, int rows, int vocab, int k) {
   const Cut cut = lp_cut(dtype, rows, vocab, k);
   if (cut.slices <= 1) return 0;
-  return (size_t)batch_of(cut, rows) * cut.slices * (sizeof(Sums) + 8 * (size_t)k);
+  return lp_bytes(cut, batch_of(cut, rows), k);
 }
 
 hipError_t launch_logprobs(const LogprobArgs& a, int dtype, void* ws, hipStream_t s) {
