@@ -171,7 +171,7 @@ def s(lib, monkeypatch):  # noqa: F811
     monkeypatch.setattr(tsr, "load_library", lambda: fake)
     monkeypatch.setattr(tsr, "_stream_on", lambda device, stream: 7)
     s = tsr.Sampler.__new__(tsr.Sampler)
-    s._h, s.device, s.calls = ctypes.c_void_p(), -1, calls
+    s._h, s.device, s.calls, s._ws_bytes = ctypes.c_void_p(), -1, calls, {}
     return s
 
 

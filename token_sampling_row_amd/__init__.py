@@ -298,6 +298,8 @@ class Sampler:
         self.device = int(device)
         self.seed = int(seed)
         self._vp_bytes = {}   # verify_probs: workspace of a batch by its sizes
+        self._ws_bytes = {}   # the same of token_logprobs and distill_topk
+        self._ws = None       # theirs on the default stream
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
@@ -692,7 +694,8 @@ class Sampler:
         """Type, rows, columns and row stride of t, a matrix of contiguous rows that do
         not overlap, on the handle's GPU."""
         torch = _t()
-        dt = BF16 if t.dtype is torch.bfloat16 else _dtype_code(t)
+        dt = BF16 if t.dtype is torch.bfloat16 else F32 if t.dtype is torch.float32 else \
+            _dtype_code(t)
         if t.dim() != 2 or t.get_device() != self.device:
             raise ValueError(f"{what}: not a matrix on the handle's GPU")
         rows, width = t.shape
@@ -712,8 +715,13 @@ class Sampler:
         torch = _torch
         w_ptr, wdt = None, dt
         if weight is not None:
-            wdt = _dtype_code(weight)
-            w_ptr = self._vector(weight, weight.dtype, "weight", width)
+            wd = weight.dtype
+            wdt = F32 if wd is torch.float32 else BF16 if wd is torch.bfloat16 else \
+                _dtype_code(weight)
+            if weight.shape != (width,) or weight.get_device() != self.device or \
+                    not weight.is_contiguous():
+                self._vector(weight, wd, "weight", width)
+            w_ptr = weight.data_ptr()
         r_ptr, rs, h_ptr, hs = None, 0, None, 0
         if residual is not None:
             if residual.dtype is not x.dtype:
@@ -735,10 +743,14 @@ class Sampler:
             raise ValueError("out: not int8")
         else:
             stride = self._rows(out, rows, width, "out")
-        if scale is None:
-            scale = _new(stream, x.device, torch.float32, rows)
-        else:
+        if scale is not None:
             self._vector(scale, torch.float32, "scale", rows)
+        elif dt == F32:
+            scale = _new_like(stream, x, rows)
+        elif weight is not None and wdt == F32:
+            scale = _new_like(stream, weight, rows)
+        else:
+            scale = _new(stream, x.device, torch.float32, rows)
         if rows:
             _check(load_library().norm_quantize_rows(
                 self._h, x.data_ptr(), xs, r_ptr, rs, dt, w_ptr, wdt, eps, rows, width, h_ptr, hs,
@@ -748,9 +760,12 @@ class Sampler:
 
     def _tokens(self, tokens, rows):
         """Pointer to tokens [rows] or [rows, n] int32, and n."""
-        n = tokens.shape[1] if tokens.dim() == 2 else 1
-        shape = (rows, n) if tokens.dim() == 2 else (rows,)
-        return self._vector(tokens, _torch.int32, "tokens", *shape), n
+        shape = tokens.shape
+        n = shape[1] if len(shape) == 2 else 1
+        if tokens.dtype is not _torch.int32 or shape[0] != rows or len(shape) > 2 or \
+                tokens.get_device() != self.device or not tokens.is_contiguous():
+            self._vector(tokens, _torch.int32, "tokens", *((rows, n) if len(shape) == 2 else (rows,)))
+        return tokens.data_ptr(), n
 
     def token_logprobs(self, logits, tokens=None, top_k=0, temperature=1.0, entropy=True,
                        norm=True, status=None, stream=None):
@@ -761,46 +776,62 @@ class Sampler:
         tensor, or None."""
         dt, rows, vocab, stride = self._matrix(logits, "logits")
         torch = _torch
-        f32 = torch.float32
-        o = _Logprobs()
-        t_ptr, n, lp = None, 0, None
+        dev = logits.device
+        t_ptr, n, lp, H, nz, ids, top = None, 0, None, None, None, None, None
+        lp_ptr = H_ptr = nz_ptr = ids_ptr = top_ptr = s_ptr = None
+        # the first of the new float32 tensors makes the others (0.5 us less of host time each)
+        like = logits if dt == F32 else None
         if tokens is not None:
             t_ptr, n = self._tokens(tokens, rows)
-        new = logits.new_empty if dt == F32 and stream is None else \
-            (lambda *shape: _new(stream, logits.device, f32, *shape))
-        if tokens is not None:
-            lp = new(*tokens.shape)
-            o.logprob = lp.data_ptr()
-        H = new(rows) if entropy else None
-        nz = new(rows, 2) if norm else None
-        ids = top = None
-        if top_k > 0:
-            top = new(rows, top_k)
-            ids = _new(stream, logits.device, torch.int32, rows, top_k)
-            o.top_ids, o.top_logprob = ids.data_ptr(), top.data_ptr()
+            if like is None:
+                lp = like = _new(stream, dev, torch.float32, *tokens.shape)
+            else:
+                lp = _new_like(stream, like, *tokens.shape)
+            lp_ptr = lp.data_ptr()
+        elif like is None:
+            like = _new(stream, dev, torch.float32, 0)
         if entropy:
-            o.entropy = H.data_ptr()
+            H = _new_like(stream, like, rows)
+            H_ptr = H.data_ptr()
         if norm:
-            o.norm = nz.data_ptr()
+            nz = _new_like(stream, like, rows, 2)
+            nz_ptr = nz.data_ptr()
+        if top_k > 0:
+            top = _new_like(stream, like, rows, top_k)
+            ids = _new(stream, dev, torch.int32, rows, top_k) if tokens is None else \
+                _new_like(stream, tokens, rows, top_k)
+            ids_ptr, top_ptr = ids.data_ptr(), top.data_ptr()
         if status is not None:
-            o.status = self._vector(status, torch.int32, "status", rows)
+            s_ptr = self._vector(status, torch.int32, "status", rows)
         if rows:
-            lib = load_library()
-            ws, need = self._workspace(lib.token_logprobs_workspace, stream, logits.device, dt,
-                                       rows, vocab, top_k)
-            _check(lib.token_logprobs(
+            raw = _stream_on(self.device, stream)
+            ws, ws_ptr, need = self._workspace("token_logprobs_workspace", stream, raw, dev, dt,
+                                               rows, vocab, top_k)
+            _check(load_library().token_logprobs(
                 self._h, logits.data_ptr(), dt, rows, vocab, stride, temperature, t_ptr, n, top_k,
-                ctypes.byref(o), None if ws is None else ws.data_ptr(), need,
-                _stream_on(self.device, stream)), "token_logprobs")
+                ctypes.byref(_Logprobs(lp_ptr, H_ptr, ids_ptr, top_ptr, nz_ptr, s_ptr)), ws_ptr,
+                need, raw), "token_logprobs")
         return TokenLogprobs(lp, H, ids, top, nz, status)
 
-    def _workspace(self, size, stream, device, *sizes):
-        """A call's own workspace of size(*sizes) bytes, from torch's allocator (calls on
-        several streams, and captured ones, each have theirs), and the bytes."""
-        need = size(*sizes)
+    def _workspace(self, name, stream, raw, device, *sizes):
+        """The workspace that the library's `name` gives for these sizes: the tensor that
+        holds it, its address and its bytes. Calls on the default stream, which follow each other and are
+        never captured, share the handle's, which grows; on other streams each has one of its
+        own, from torch's allocator."""
+        key = (name, *sizes)
+        need = self._ws_bytes.get(key)
+        if need is None:
+            need = self._ws_bytes[key] = getattr(load_library(), name)(*sizes)
         if need <= 0:
-            return None, 0
-        return _new(stream, device, _torch.uint8, need), need
+            return None, None, 0
+        if raw:
+            ws = _new(stream, device, _torch.uint8, need)
+        else:
+            ws = self._ws
+            if ws is None or ws.numel() < need:
+                with _torch.cuda.stream(_torch.cuda.default_stream(device)):
+                    ws = self._ws = _torch.empty(need, dtype=_torch.uint8, device=device)
+        return ws, ws.data_ptr(), need
 
     def token_logprobs_grad(self, logits, tokens, norm, grad_logprob, entropy=None,
                             grad_entropy=None, temperature=1.0, out=None, stream=None):
@@ -864,15 +895,15 @@ class Sampler:
         else:
             grad, gs = self._grad_out(logits, None if grad is True else grad, rows, vocab, stream)
             g_ptr = grad.data_ptr()
-        loss = _new(stream, logits.device, f32, rows)
+        loss = _new_like(stream, teacher_logprob, rows)
         if rows:
-            lib = load_library()
-            ws, need = self._workspace(lib.distill_topk_workspace, stream, logits.device, dt,
-                                       rows, vocab, int(grad is not None))
-            _check(lib.distill_topk(
+            raw = _stream_on(self.device, stream)
+            ws, ws_ptr, need = self._workspace("distill_topk_workspace", stream, raw,
+                                               logits.device, dt, rows, vocab,
+                                               int(grad is not None))
+            _check(load_library().distill_topk(
                 self._h, logits.data_ptr(), dt, rows, vocab, stride, temperature, i_ptr, t_ptr, k,
-                int(bool(tail)), w_ptr, loss.data_ptr(), g_ptr, gs, s_ptr,
-                None if ws is None else ws.data_ptr(), need, _stream_on(self.device, stream)),
+                int(bool(tail)), w_ptr, loss.data_ptr(), g_ptr, gs, s_ptr, ws_ptr, need, raw),
                 "distill_topk")
         return loss, grad
 

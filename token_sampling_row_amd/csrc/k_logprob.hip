@@ -25,11 +25,11 @@ struct Candidates {
 };
 // Chunks of a slice that hold candidates, a region for each wavefront.
 constexpr int kHits = 64;
-template <int DT>
+template <int WAVES>
 struct Hits {
-  uint4 chunk[kSliceWaves][kHits];
-  int id[kSliceWaves][kHits];   // of the chunk's first element
-  int n[kSliceWaves];
+  uint4 chunk[WAVES][kHits];
+  int id[WAVES][kHits];   // of the chunk's first element
+  int n[WAVES];
 };
 
 __device__ __forceinline__ int lanes_below(unsigned long long who) {
@@ -50,16 +50,16 @@ __device__ __forceinline__ void rank_candidates(const Candidates& c, int k, F&& 
 }
 
 // The slice's candidates: its logits of at least `tau` (a key of values), of which there
-// are k at least and few more: every wavefront has j = ceil(k / 4) threads whose largest
-// logit is at least that. `cmax`: the largest of each chunk. A wavefront lists its chunks
+// are k at least and few more: every wavefront has j = ceil(k / wavefronts) threads whose
+// largest logit is at least that. `cmax`: the largest of each chunk. A wavefront lists its chunks
 // that hold any, and the workgroup then looks at their elements together: taken where
 // they lie, each chunk would cost its wavefront eight tests for one or two that pass.
 // c.n is 0 before the call.
-template <int DT, int NC>
-__device__ __forceinline__ void gather(const Slice<DT, NC>& s, int V, const float* cmax,
-                                       uint32_t tau, int k, Candidates& c, Hits<DT>& hits,
-                                       BlockScratch& scratch) {
-  constexpr int EPC = Fmt<DT>::EPC;
+template <int DT, int NC, int BLOCK>
+__device__ __forceinline__ void gather(const Slice<DT, NC, BLOCK>& s, int V, const float* cmax,
+                                       uint32_t tau, int k, Candidates& c,
+                                       Hits<BLOCK / kWave>& hits, BlockScratch& scratch) {
+  constexpr int EPC = Fmt<DT>::EPC, WAVES = BLOCK / kWave;
   const int wave = threadIdx.x / kWave;
   const float least = key2f(tau);
   int n = 0;
@@ -79,18 +79,18 @@ __device__ __forceinline__ void gather(const Slice<DT, NC>& s, int V, const floa
   if (s.ragged) list(cmax[NC], s.rest, V / EPC * EPC);
   if (__lane_id() == 0) hits.n[wave] = n;
   __syncthreads();
-  int count[kSliceWaves], total = 0, most = 0;
+  int count[WAVES], total = 0, most = 0;
 #pragma unroll
-  for (int w = 0; w < kSliceWaves; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     total += count[w] = hits.n[w];
     most = max(most, count[w]);
   }
   if (most <= kHits) {
-    for (int i0 = wave * kWave; i0 < total * EPC; i0 += kSliceBlock) {
+    for (int i0 = wave * kWave; i0 < total * EPC; i0 += BLOCK) {
       const int i = i0 + (int)__lane_id();
       int at = i / EPC, w = 0;
       const int e = i % EPC;
-      while (w < kSliceWaves - 1 && at >= count[w]) at -= count[w++];
+      while (w < WAVES - 1 && at >= count[w]) at -= count[w++];
       float v = kNegInf;
       if (i < total * EPC) {
         if constexpr (DT == 0)
@@ -125,7 +125,7 @@ __device__ __forceinline__ void gather(const Slice<DT, NC>& s, int V, const floa
       });
       if (best == 0) last = 0;   // none is left with this thread
     }
-    const unsigned long long top = block_max_u64<kSliceBlock>(best, scratch);
+    const unsigned long long top = block_max_u64<BLOCK>(best, scratch);
     if (top == 0) break;
     if (threadIdx.x == 0) c.key[i] = top;
     ++taken;
@@ -207,35 +207,35 @@ struct LpWs {
 };
 
 // One workgroup to a slice of a row; with one slice it is the whole row's.
-template <int DT, int NC, bool TOP, bool ONCE>
-__global__ __launch_bounds__(kSliceBlock) void logprob_slice_kernel(LogprobArgs a, Cut cut,
-                                                                    LpWs ws) {
-  __shared__ Sums each[kSliceWaves];
-  __shared__ uint32_t bound[kSliceWaves];
+template <int DT, int NC, int BLOCK, bool TOP, bool ONCE>
+__global__ __launch_bounds__(BLOCK) void logprob_slice_kernel(LogprobArgs a, Cut cut, LpWs ws) {
+  constexpr int WAVES = BLOCK / kWave;
+  __shared__ Sums each[WAVES];
+  __shared__ uint32_t bound[WAVES];
   __shared__ typename std::conditional<TOP, Candidates, int>::type cands;
-  __shared__ typename std::conditional<TOP, Hits<DT>, int>::type hits;
+  __shared__ typename std::conditional<TOP, Hits<WAVES>, int>::type hits;
   __shared__ typename std::conditional<TOP, BlockScratch, int>::type scratch;
   const int slice = blockIdx.x % cut.slices;
   const long long r = blockIdx.x / cut.slices;
-  Slice<DT, NC> s;
+  Slice<DT, NC, BLOCK> s;
   s.template load<ONCE>(a.logits + r * a.stride_bytes, a.V, slice, cut);
   Given given;
   if (cut.slices == 1 && threadIdx.x < kWave) given = first_token<DT>(a, r);
   float cmax[NC + 1];
   const float m = s.largest([&](int j, float most) { cmax[j] = most; });
   if constexpr (TOP) {   // bf16 values have 16 bits; of float32 ones as many do
-    const uint32_t jth = jth_largest<16>(fkey(m), (a.k + kSliceWaves - 1) / kSliceWaves);
+    const uint32_t jth = jth_largest<16>(fkey(m), (a.k + WAVES - 1) / WAVES);
     if (__lane_id() == 0) bound[threadIdx.x / kWave] = jth;
     if (threadIdx.x == 0) cands.n = 0;
   }
   float off;
   const Sums mine = s.template sums<true>(a.V, m, a.c, off);
-  const Sums all = join_block<kSliceWaves>(mine, a.c, off, each);
+  const Sums all = join_block<WAVES>(mine, a.c, off, each);
   uint32_t tau = 0;
   if constexpr (TOP) {
     tau = bound[0];
 #pragma unroll
-    for (int w = 1; w < kSliceWaves; ++w) tau = min(tau, bound[w]);
+    for (int w = 1; w < WAVES; ++w) tau = min(tau, bound[w]);
     tau = max(tau, kKeyNegInf);   // cut short, a key of -inf is one of NaN
     if (row_status(all.M) == 0) gather(s, a.V, cmax, tau, a.k, cands, hits, scratch);
   }
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_slice_kernel(LogprobArgs 
     const double logZ = log(all.Z);
     if (threadIdx.x < kWave) put_row<DT>(a, r, all, logZ, given);
     if constexpr (TOP) {
-      for (int i = cands.n + (int)threadIdx.x; i < a.k; i += kSliceBlock)
+      for (int i = cands.n + (int)threadIdx.x; i < a.k; i += BLOCK)
         put_top(a, r, i, 0, all, logZ);   // past the last
       rank_candidates(cands, a.k, [&](int rank, unsigned long long key) {
         put_top(a, r, rank, key, all, logZ);
@@ -499,10 +499,25 @@ constexpr int kSlotsMost = 2048;   // places for candidates of a row's slices: 3
 // Places for a slice's candidates: some half more than k come as a rule.
 int cap_of(int k) { return k == 0 ? 0 : k <= 40 ? kWave : 2 * kWave; }
 
+constexpr int kRowBlock = 1024;   // threads of a workgroup that takes a whole row
+
 // How rows are cut (slices 0: not at all, the wide kernel).
+//  - Up to 1024 chunks: one workgroup of 256 threads and one launch. 1000 x 8192 bf16
+//    7.8 us, in workgroups of 1024 threads 13.6; 1024 x 8192 with 20 alternatives 11.4.
+//  - Few rows of up to 8192 chunks: one workgroup of 1024 threads, which saves the join.
+//    1 x 32000 fp32, 20 alternatives 9.9 us against 11.8 in slices and their join; 64 rows
+//    12.4 against 15.4; 256 x 32000 bf16 14.1 against 16.8, but 512 24 against 18. Without
+//    alternatives 512 x 32000 fp32 14.3 against 16.3.
+//  - Else slices: as many as give a thousand workgroups, at least what holds the row.
 Cut lp_cut(int dtype, int rows, int vocab, int k) {
   const int whole = vocab / (dtype == 0 ? 4 : 8);
-  int want = std::min({1024 / max(rows, 1), 64, (whole + kSliceBlock - 1) / kSliceBlock});   // TUNE
+  if (whole <= 4 * kSliceBlock) return cut_of(whole, 1);
+  if (whole <= 8 * kRowBlock && rows <= (k ? 256 : 512)) {
+    Cut c{1, whole, 1, kRowBlock};
+    while (c.nc * kRowBlock < whole) c.nc *= 2;
+    return c;
+  }
+  int want = std::min({1024 / max(rows, 1), 64, (whole + kSliceBlock - 1) / kSliceBlock});
   if (k) want = min(want, 1024 / cap_of(k));
   const Cut c = cut_of(whole, want);
   return k && c.slices > kSlotsMost / cap_of(k) ? Cut{0, 0, 0} : c;
@@ -531,15 +546,26 @@ void launch_top_join(const LogprobArgs& a, int slices, const LpWs& ws, hipStream
 
 template <int DT, bool TOP, bool ONCE>
 void launch_slices(const LogprobArgs& a, const Cut& cut, const LpWs& ws, hipStream_t s) {
-  const dim3 grid((unsigned)a.rows * (unsigned)cut.slices), block(kSliceBlock);
-  switch (cut.nc) {
-    case 1: hipLaunchKernelGGL((logprob_slice_kernel<DT, 1, TOP, ONCE>), grid, block, 0, s, a, cut, ws); break;
-    case 2: hipLaunchKernelGGL((logprob_slice_kernel<DT, 2, TOP, ONCE>), grid, block, 0, s, a, cut, ws); break;
-    case 4: hipLaunchKernelGGL((logprob_slice_kernel<DT, 4, TOP, ONCE>), grid, block, 0, s, a, cut, ws); break;
-    case 8: hipLaunchKernelGGL((logprob_slice_kernel<DT, 8, TOP, ONCE>), grid, block, 0, s, a, cut, ws); break;
-    default: hipLaunchKernelGGL((logprob_slice_kernel<DT, 16, TOP, ONCE>), grid, block, 0, s, a, cut, ws);
+  const auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)a.rows * (unsigned)cut.slices), dim3(cut.block), 0, s,
+                       a, cut, ws);
+  };
+  if (cut.block == kRowBlock) {
+    if (cut.nc == 2) return launch(logprob_slice_kernel<DT, 2, kRowBlock, TOP, false>);
+    if (cut.nc == 4) return launch(logprob_slice_kernel<DT, 4, kRowBlock, TOP, ONCE>);
+    return launch(logprob_slice_kernel<DT, 8, kRowBlock, TOP, ONCE>);
   }
+  if (cut.nc == 1) return launch(logprob_slice_kernel<DT, 1, kSliceBlock, TOP, false>);
+  if (cut.nc == 2) return launch(logprob_slice_kernel<DT, 2, kSliceBlock, TOP, false>);
+  if (cut.nc == 4) return launch(logprob_slice_kernel<DT, 4, kSliceBlock, TOP, ONCE>);
+  if (cut.nc == 8) return launch(logprob_slice_kernel<DT, 8, kSliceBlock, TOP, ONCE>);
+  launch(logprob_slice_kernel<DT, 16, kSliceBlock, TOP, ONCE>);
 }
+
+// Batches of more bytes than this are read past the caches, which could not keep them: 512 x
+// 128256 fp32 with 20 alternatives 51 us against 56, 1024 x 151936 bf16 with 64 76 against
+// 78. Smaller ones may be there still, from the product that wrote them.
+constexpr long long kOnceBytes = 128ll << 20;
 
 template <int DT>
 hipError_t launch_dt(const LogprobArgs& all, void* workspace, hipStream_t s) {
@@ -564,10 +590,13 @@ hipError_t launch_dt(const LogprobArgs& all, void* workspace, hipStream_t s) {
     ws.sums = static_cast<Sums*>(workspace);
     ws.keys = reinterpret_cast<unsigned long long*>(ws.sums + slots);
     ws.count = reinterpret_cast<int2*>(ws.keys + slots * ws.cap);
+    const bool once = (long long)all.rows * all.V * Fmt<DT>::ESZ > kOnceBytes;
     if (a.k)
-      launch_slices<DT, true, false>(a, cut, ws, s);
+      once ? launch_slices<DT, true, true>(a, cut, ws, s)
+           : launch_slices<DT, true, false>(a, cut, ws, s);
     else
-      launch_slices<DT, false, false>(a, cut, ws, s);
+      once ? launch_slices<DT, false, true>(a, cut, ws, s)
+           : launch_slices<DT, false, false>(a, cut, ws, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (cut.slices == 1) continue;

@@ -22,6 +22,7 @@ constexpr int kSliceWaves = kSliceBlock / kWave;
 // thread (the elements behind the last whole chunk go with the last slice).
 struct Cut {
   int slices, per, nc;
+  int block = kSliceBlock;   // threads of a workgroup
 };
 
 // Weights against a largest logit M: their sum, and that of weight times exponent.
