@@ -11,16 +11,6 @@ constexpr int kTileChunks = 4;   // 16-byte chunks a thread
 template <int DT>
 constexpr int kTileIds = kSliceBlock * kTileChunks * Fmt<DT>::EPC;
 
-template <int DT>
-__device__ __forceinline__ uint4 pack(const float* v) {
-  if constexpr (DT == 0)
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                      __float_as_uint(v[3]));
-  else
-    return make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
-                      bf16_pair(v[6], v[7]));
-}
-
 template <bool ONCE>
 __device__ __forceinline__ void store16(void* p, uint4 v) {
   if constexpr (ONCE) {

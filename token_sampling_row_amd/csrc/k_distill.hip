@@ -25,6 +25,7 @@ struct Entries {
   double same;         // sum of q over the lanes of this id
   double sum, rest;
   int status;
+  float z;             // its logit
 };
 
 __device__ __forceinline__ int raw_id(const DistillArgs& a, long long r) {
@@ -54,7 +55,7 @@ __device__ __forceinline__ Entries entries_of(const DistillArgs& a, int id, floa
   if (outside) e.id = -1;
   // with a tail the values are log probabilities; without one any row constant cancels
   const double shift = a.tail || e.status ? 0.0 : (double)top;
-  e.q = real && t > kNegInf ? exp((double)t - shift) : 0.0;
+  e.q = real && t > kNegInf ? exp_small((double)t - shift) : 0.0;
   e.log_q = (double)t - shift;
   e.sum = wave_sum(e.q);
   e.rest = 0.0;
@@ -63,7 +64,7 @@ __device__ __forceinline__ Entries entries_of(const DistillArgs& a, int id, floa
     if (!(e.rest > (double)kRestMin)) e.rest = 0.0;
   } else {
     e.q /= e.sum;
-    e.log_q -= log(e.sum);
+    e.log_q -= log_small(e.sum);
     e.sum = 1.0;
   }
   e.first = e.id >= 0;
@@ -87,24 +88,25 @@ struct RowGrad {
 };
 
 // Loss, status and the gradient's factors of row r from its entries and the sums of the
-// other ids (all ids without a tail), by one wavefront. z: the entry's logit.
+// other ids (all ids without a tail), by one wavefront.
 __device__ __forceinline__ RowGrad finish_row(const DistillArgs& a, long long r, float weight,
-                                              const Entries& e, float z, const Sums& other) {
+                                              const Entries& e, const Sums& other) {
+  const float z = e.z;
   const float Ms = a.tail ? wave_maxn(e.id >= 0 ? z : kNegInf) : kNegInf;
   const float M = fmaxn(other.M, Ms);
   const int status = e.status ? e.status : M == kNegInf ? 2 : !(M < kPosInf) ? 1 : 0;
   const double Zr = other.Z;
   const double log_f = ((double)other.M - (double)M) * a.inv_t;
-  const double f = other.M > kNegInf ? exp(log_f) : 0.0;   // a weight against other.M, against M
+  const double f = other.M > kNegInf ? exp_small(log_f) : 0.0;   // a weight against other.M, against M
   const double ez =
       e.id >= 0 ? (double)__builtin_amdgcn_exp2f(exponent(z, M, a.c)) : 0.0;
   const double Z = Zr * f + (a.tail ? wave_sum(e.first ? ez : 0.0) : 0.0);
-  const double logZ = log(Z);
+  const double logZ = log_small(Z);
   double term = 0.0;
   if (e.q > 0.0) term = e.q * (e.log_q - (((double)z - (double)M) * a.inv_t - logZ));
   double loss = wave_sum(term);
   if (e.rest > 0.0)   // +inf where the draft gives the other ids nothing
-    loss += e.rest * (log(e.rest) - (other.M > kNegInf ? log(Zr) + log_f - logZ
+    loss += e.rest * (log_small(e.rest) - (other.M > kNegInf ? log_small(Zr) + log_f - logZ
                                                        : -__builtin_huge_val()));
   const float nan = __uint_as_float(0x7FC00000u);
   if (__lane_id() == 0) {
@@ -123,7 +125,7 @@ __device__ __forceinline__ RowGrad finish_row(const DistillArgs& a, long long r,
 
 // ------------------------------------------------------------ a row in one workgroup
 // Read once: the gradient is formed from the registers that the sums were.
-template <int DT, int NC, int BLOCK>
+template <int DT, int NC, int BLOCK, bool ONCE>
 __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
   constexpr int EPC = Fmt<DT>::EPC;
   __shared__ Sums each[BLOCK / kWave];
@@ -154,8 +156,14 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
   const float t = teacher_of(a, r);
   const unsigned char* row = a.logits + r * a.stride_bytes;
   Slice<DT, NC, BLOCK> s;
-  s.template load<false>(row, a.V, 0, Cut{1, whole, NC});
-  if (threadIdx.x < kWave) entries[threadIdx.x] = entries_of(a, id, t);   // the row is on its way
+  s.template load<ONCE>(row, a.V, 0, Cut{1, whole, NC});
+  if (a.tail) s.list_left_out(valid_id(a, id), left_out);
+  if (threadIdx.x < kWave) {   // the row is on its way
+    const float z = valid_id(a, id) >= 0 ? load_elem<DT>(row, id) : kNegInf;
+    entries[threadIdx.x] = entries_of(a, id, t);
+    sched_fence();   // z comes after the wavefront's share of the row
+    entries[threadIdx.x].z = z;
+  }
   if (a.tail) s.leave_out(a.V, valid_id(a, id), left_out);
   float off;
   const float m = s.largest([](int, float) {});
@@ -163,9 +171,7 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
   const Sums other = join_block<BLOCK / kWave>(mine, a.c, off, each);
   float own = 0.0f;   // the entry's gradient
   if (threadIdx.x < kWave) {
-    const Entries e = entries[threadIdx.x];
-    const float z = e.id >= 0 ? load_elem<DT>(row, e.id) : kNegInf;
-    const RowGrad g = finish_row(a, r, weight, e, z, other);
+    const RowGrad g = finish_row(a, r, weight, entries[threadIdx.x], other);
     own = g.entry;
     if (threadIdx.x == 0) {
       row_grad.M = g.M;
@@ -184,7 +190,7 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
 #pragma unroll
       for (int i = 0; i < EPC; ++i) v[i] = of(v[i]);
       unsigned char* base = out + j * BLOCK * 16;   // uniform
-      if (j * BLOCK + (int)threadIdx.x < whole) store16<false>(base + threadIdx.x * 16u, pack<DT>(v));
+      if (j * BLOCK + (int)threadIdx.x < whole) store16<ONCE>(base + threadIdx.x * 16u, pack<DT>(v));
       sched_fence();
     }
   };
@@ -225,7 +231,10 @@ __global__ __launch_bounds__(kSliceBlock) void distill_slice_kernel(DistillArgs 
   const int id = a.tail ? valid_id(a, raw_id(a, r)) : -1;
   Slice<DT, NC> s;
   s.template load<false>(a.logits + r * a.stride_bytes, a.V, slice, cut);
-  if (a.tail) s.leave_out(a.V, id, left_out);
+  if (a.tail) {
+    s.list_left_out(id, left_out);
+    s.leave_out(a.V, id, left_out);
+  }
   float off;
   const float m = s.largest([](int, float) {});
   const Sums mine = s.template sums<false>(a.V, m, a.c, off);
@@ -254,8 +263,9 @@ __global__ __launch_bounds__(kSliceBlock) void distill_join_kernel(DistillArgs a
   const float z =
       valid_id(a, id) >= 0 ? load_elem<DT>(a.logits + r * a.stride_bytes, id) : kNegInf;
   const Sums other = join_slices(ws.sums + r * slices, slices, a.c);
-  const Entries e = entries_of(a, id, t);
-  const RowGrad g = finish_row(a, r, weight, e, z, other);
+  Entries e = entries_of(a, id, t);
+  e.z = z;
+  const RowGrad g = finish_row(a, r, weight, e, other);
   if (lane == 0) ws.rows[r] = DtRow{g.A, g.M, weight};
   if (lane < a.k) ws.entry[r * a.k + lane] = g.entry;
 }
@@ -284,35 +294,43 @@ __global__ __launch_bounds__(kSliceBlock) void distill_grad_kernel(DistillArgs a
 
 
 // Rows of up to this many chunks take one workgroup each, and are read once.
-constexpr int kRowBlock = 1024;
+constexpr int kHalfBlock = 512, kRowBlock = 1024;
 constexpr int kRowChunks = 20 * kRowBlock;
 
-// How rows are cut; nc 0: not at all, one workgroup of kRowBlock threads to a row.
+// How rows are cut; one slice: not at all.
 Cut dt_cut(int dtype, int rows, int vocab) {
   const int whole = vocab / (dtype == 0 ? 4 : 8);
   if (whole <= kMaxSliceChunks) return cut_of(whole, 1);   // TUNE
-  if (whole <= kRowChunks && rows >= 128) return Cut{1, whole, 0};
+  if (whole <= kRowChunks && rows >= 128) {
+    const int block = whole <= 16 * kHalfBlock ? kHalfBlock : kRowBlock;
+    return Cut{1, whole, (whole + block - 1) / block, block};
+  }
   return cut_of(whole, std::min({1024 / max(rows, 1), 64, (whole + kSliceBlock - 1) / kSliceBlock}));
 }
 
-template <int DT, int NC, int BLOCK>
-void launch_row(const DistillArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((distill_row_kernel<DT, NC, BLOCK>), dim3(a.rows), dim3(BLOCK), 0, s, a);
-}
+// Batches of more bytes than this, logits and gradient together, are read and written past
+// the caches, which could not keep them.
+constexpr long long kOnceBytes = 192ll << 20;   // TUNE
 
-template <int DT>
+template <int DT, bool ONCE>
 void launch_rows(const DistillArgs& a, const Cut& cut, hipStream_t s) {
-  switch (cut.nc) {
-    case 1: return launch_row<DT, 1, kSliceBlock>(a, s);
-    case 2: return launch_row<DT, 2, kSliceBlock>(a, s);
-    case 4: return launch_row<DT, 4, kSliceBlock>(a, s);
-    case 8: return launch_row<DT, 8, kSliceBlock>(a, s);
-    case 16: return launch_row<DT, 16, kSliceBlock>(a, s);
+  const auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(a.rows), dim3(cut.block), 0, s, a);
+  };
+  if (cut.block == kSliceBlock) {
+    if (cut.nc == 1) return launch(distill_row_kernel<DT, 1, kSliceBlock, false>);
+    if (cut.nc == 2) return launch(distill_row_kernel<DT, 2, kSliceBlock, false>);
+    if (cut.nc == 4) return launch(distill_row_kernel<DT, 4, kSliceBlock, false>);
+    if (cut.nc == 8) return launch(distill_row_kernel<DT, 8, kSliceBlock, ONCE>);
+    return launch(distill_row_kernel<DT, 16, kSliceBlock, ONCE>);
   }
-  if (cut.per <= 8 * kRowBlock) return launch_row<DT, 8, kRowBlock>(a, s);
-  if (cut.per <= 12 * kRowBlock) return launch_row<DT, 12, kRowBlock>(a, s);
-  if (cut.per <= 16 * kRowBlock) return launch_row<DT, 16, kRowBlock>(a, s);
-  return launch_row<DT, 20, kRowBlock>(a, s);
+  if (cut.block == kHalfBlock) {
+    if (cut.nc <= 12) return launch(distill_row_kernel<DT, 12, kHalfBlock, ONCE>);
+    return launch(distill_row_kernel<DT, 16, kHalfBlock, ONCE>);
+  }
+  if (cut.nc <= 12) return launch(distill_row_kernel<DT, 12, kRowBlock, ONCE>);
+  if (cut.nc <= 16) return launch(distill_row_kernel<DT, 16, kRowBlock, ONCE>);
+  launch(distill_row_kernel<DT, 20, kRowBlock, ONCE>);
 }
 
 template <int DT>
@@ -336,7 +354,9 @@ template <int DT>
 hipError_t launch_dt(const DistillArgs& all, void* workspace, hipStream_t s) {
   const Cut cut = dt_cut(DT, all.rows, all.V);
   if (cut.slices == 1) {
-    launch_rows<DT>(all, cut, s);
+    const long long bytes = 2ll * all.rows * all.V * Fmt<DT>::ESZ;
+    all.grad && bytes > kOnceBytes ? launch_rows<DT, true>(all, cut, s)
+                                   : launch_rows<DT, false>(all, cut, s);
     return hipGetLastError();
   }
   const int tiles = tiles_of<DT>(all.V), batch = dt_batch(cut, all.rows, tiles);

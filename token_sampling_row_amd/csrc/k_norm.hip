@@ -47,16 +47,6 @@ __device__ __forceinline__ float stored(float v) {   // rounded to the rows' typ
   return (float)(__bf16)v;
 }
 
-template <int DT>
-__device__ __forceinline__ uint4 pack_chunk(const float* v) {
-  if constexpr (DT == 0)
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                      __float_as_uint(v[3]));
-  else
-    return make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
-                      bf16_pair(v[6], v[7]));
-}
-
 // EPC weights from element i on; past the row's last one 0.
 template <int EPC, int WT>
 __device__ __forceinline__ void load_weights(const unsigned char* w, int i, int n, float* out) {
@@ -89,7 +79,7 @@ __device__ __forceinline__ uint4 add_chunks(uint4 x, uint4 r) {
   unpack<DT>(r, b);
 #pragma unroll
   for (int e = 0; e < Fmt<DT>::EPC; ++e) a[e] += b[e];
-  return pack_chunk<DT>(a);
+  return pack<DT>(a);
 }
 
 template <int DT>

@@ -49,6 +49,14 @@ __device__ __forceinline__ Sums join_block(Sums a, float c, float off, Sums* eac
   a.S = wave_sum(a.S);
   if (__lane_id() == 0) each[threadIdx.x / kWave] = a;
   __syncthreads();
+  if constexpr (WAVES > 4) {   // a lane for each: together they would take 100 registers
+    Sums one{kNegInf, 0.0, 0.0};
+    if ((int)__lane_id() < WAVES) one = each[__lane_id()];
+    rebase(one, reduce_w<16>(one.M, [](float x, float y) { return fmaxn(x, y); }), c, 0.0f);
+    one.Z = sum_w<16>(one.Z);
+    one.S = sum_w<16>(one.S);
+    return one;
+  }
   float M = each[0].M;
 #pragma unroll
   for (int w = 1; w < WAVES; ++w) M = fmaxn(M, each[w].M);
@@ -107,6 +115,8 @@ template <int DT, int NC, int BLOCK = kSliceBlock>
 struct Slice {
   static constexpr int EPC = Fmt<DT>::EPC;
   const unsigned char* row;
+  const unsigned char* base;   // of the slice's chunks, the last of which is `last`
+  uint32_t last;
   uint4 c[NC];
   uint4 rest;   // the elements behind the last whole chunk, with one thread of the last slice
   int lo, hi;   // the slice's whole chunks
@@ -120,22 +130,32 @@ struct Slice {
   // it, and `largest` puts -inf in its place.
   template <bool ONCE>
   __device__ __forceinline__ void load(const unsigned char* at, int V, int slice, const Cut& cut) {
-    row = at;
     const int whole = V / EPC;
     lo = slice * cut.per;
     hi = min(lo + cut.per, whole);
     ragged = slice == cut.slices - 1 && whole * EPC < V;
-    const unsigned char* base =
-        whole > 0 ? row + (long long)min(lo, whole - 1) * 16
-                  : reinterpret_cast<const unsigned char*>(&g_neg_inf_chunk[DT]);
-    const uint32_t last = (uint32_t)max(hi - lo - 1, 0);
+    from(at, V);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const unsigned char* p = base + min((uint32_t)(j * BLOCK) + threadIdx.x, last) * 16u;
-      c[j] = ONCE ? load16_once(p) : load16(p);
-    }
+    for (int j = 0; j < NC; ++j) load_chunk<ONCE>(j);
+    load_rest(V);
+  }
+  // The same in steps: where the loads come from (nullptr: nowhere, chunks of -inf), each
+  // chunk's, and what is behind the last whole one.
+  __device__ __forceinline__ void from(const unsigned char* at, int V) {
+    const int whole = V / EPC;
+    row = at;
+    base = at && whole > 0 ? at + (long long)min(lo, whole - 1) * 16
+                           : reinterpret_cast<const unsigned char*>(&g_neg_inf_chunk[DT]);
+    last = at ? (uint32_t)max(hi - lo - 1, 0) : 0u;
+  }
+  template <bool ONCE>
+  __device__ __forceinline__ void load_chunk(int j) {
+    const unsigned char* p = base + min((uint32_t)(j * BLOCK) + threadIdx.x, last) * 16u;
+    c[j] = ONCE ? load16_once(p) : load16(p);
+  }
+  __device__ __forceinline__ void load_rest(int V) {
     rest = neg_inf_chunk<DT>();
-    if (ragged && threadIdx.x == BLOCK - 1) rest = load_chunk_slow<DT>(row, whole, V);
+    if (ragged && row && threadIdx.x == BLOCK - 1) rest = load_chunk_slow<DT>(row, V / EPC, V);
   }
 
   // f(values, number of the first) for each chunk of the thread
@@ -175,16 +195,20 @@ struct Slice {
   struct LeftOut {
     uint32_t word[BLOCK][(NC + 3) / 4];
   };
-  __device__ __forceinline__ void leave_out(int V, int id, LeftOut& out) {
-    constexpr int W = (NC + 3) / 4;
+  // First the list, which needs no chunk to have come; then the chunks.
+  __device__ __forceinline__ void list_left_out(int id, LeftOut& out) const {
 #pragma unroll
-    for (int w = 0; w < W; ++w) out.word[threadIdx.x][w] = 0;
+    for (int w = 0; w < (NC + 3) / 4; ++w) out.word[threadIdx.x][w] = 0;
     __syncthreads();
     const int q = id < 0 ? -1 : id / EPC - lo;
     if (threadIdx.x < kWave && q >= 0 && q < hi - lo) {
       const int j = q / BLOCK;
       atomicOr(&out.word[q % BLOCK][j / 4], 1u << (8 * (j % 4) + id % EPC));
     }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void leave_out(int V, int id, const LeftOut& out) {
+    constexpr int W = (NC + 3) / 4;
     if (ragged) {   // behind the last whole chunk: with every wavefront's own ids
       const int at = V / EPC * EPC;
       uint32_t bits = 0;
@@ -195,7 +219,6 @@ struct Slice {
       }
       drop(rest, bits);
     }
-    __syncthreads();
     uint32_t word[W], any = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) any |= word[w] = out.word[threadIdx.x][w];

@@ -41,6 +41,27 @@ struct Pass {
   }
 };
 
+// e^x in 64 bits with few registers (the library's exponential takes dozens, in kernels
+// that hold a row in theirs): e^r for r = x / 2^16 from its series to r^4, then squared
+// sixteen times. 2^16 times the base's error of 2^-53 and r^5 / 120: under 2^-36 relative
+// for |x| < 100, where results are not negligible.
+__device__ __forceinline__ double exp_small(double x) {
+  const double r = fmax(x, -740.0) * 0x1p-16;
+  double y = fma(r, fma(r, fma(r, fma(r, 1.0 / 24.0, 1.0 / 6.0), 0.5), 1.0), 1.0);
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) y *= y;
+  return y;
+}
+// ln a, a > 0: y from the hardware's log2 of a's mantissa m (2^-23 off), then the step to
+// y + ln(m e^-y), whose argument is next to 1: exact to 2^-36.
+__device__ __forceinline__ double log_small(double a) {
+  int e;
+  const double m = frexp(a, &e);
+  const double y = (double)__builtin_amdgcn_logf((float)m) * kLn2;
+  const double d = fma(m, exp_small(-y), -1.0);
+  return fma((double)e, kLn2, y + fma(-0.5 * d, d, d));
+}
+
 // log p of a logit v: (v - M) / T - log Z, formed in 64 bits and rounded once.
 __device__ __forceinline__ float log_prob(float v, float M, double logZ, double inv_t) {
   return (float)(((double)v - (double)M) * inv_t - logZ);
@@ -89,6 +110,24 @@ struct GradRow {
     return plain ? of<true, true>(z) : B != 0.0f ? of<true, false>(z) : of<false, false>(z);
   }
 };
+
+// Two floats as bfloat16 in one instruction, each to nearest even; the first below.
+typedef float Float2 __attribute__((ext_vector_type(2)));
+typedef __bf16 Bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_both(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(Float2{a, b}, Bf16x2));
+}
+
+// A chunk of floats in the rows' type.
+template <int DT>
+__device__ __forceinline__ uint4 pack(const float* v) {
+  if constexpr (DT == 0)
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  else
+    return make_uint4(bf16_both(v[0], v[1]), bf16_both(v[2], v[3]), bf16_both(v[4], v[5]),
+                      bf16_both(v[6], v[7]));
+}
 
 template <int DT>
 __device__ __forceinline__ void store_elem(unsigned char* row, long long i, float v) {
