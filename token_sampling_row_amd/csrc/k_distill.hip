@@ -69,9 +69,12 @@ __device__ __forceinline__ Entries entries_of(const DistillArgs& a, int id, floa
   }
   e.first = e.id >= 0;
   e.same = e.q;
-  for (int l = 0; l < a.k; ++l) {   // the same id again
-    const bool again = (int)readlane_u32((uint32_t)e.id, l) == e.id && l != lane;
-    if (__any(again)) {
+  bool twice = false;
+  for (int l = 0; l < a.k; ++l)
+    twice |= (int)readlane_u32((uint32_t)e.id, l) == e.id && l != lane;
+  if (__any(twice && e.first)) {   // an id that comes again
+    for (int l = 0; l < a.k; ++l) {
+      const bool again = (int)readlane_u32((uint32_t)e.id, l) == e.id && l != lane;
       const double q = readlane_f64(e.q, l);
       if (again) e.same += q;
       if (again && l < lane) e.first = false;
@@ -80,47 +83,68 @@ __device__ __forceinline__ Entries entries_of(const DistillArgs& a, int id, floa
   return e;
 }
 
-// What the gradient of a row takes: p_j (A + 0 x) against M, and an entry's own value.
+// A row's sums with its entries': M and Z of all ids, and of the ids outside S (of all,
+// without a tail) against their own largest, Mr and Zr.
+struct RowSums {
+  float M, Mr;
+  double Z, Zr;
+  int status;
+};
+
+// By one wavefront.
+__device__ __forceinline__ RowSums row_sums(const DistillArgs& a, const Entries& e,
+                                            const Sums& other) {
+  RowSums s;
+  s.Mr = other.M;
+  s.Zr = other.Z;
+  s.M = fmaxn(other.M, a.tail ? wave_maxn(e.id >= 0 ? e.z : kNegInf) : kNegInf);
+  s.status = e.status ? e.status : s.M == kNegInf ? 2 : !(s.M < kPosInf) ? 1 : 0;
+  s.Z = other.Z;
+  if (a.tail) {   // what a weight against Mr is against M
+    const float f = other.M > kNegInf ? __builtin_amdgcn_exp2f(exponent(other.M, s.M, a.c)) : 0.0f;
+    const float ez = __builtin_amdgcn_exp2f(exponent(e.z, s.M, a.c));
+    s.Z = other.Z * (double)f + wave_sum(e.first ? (double)ez : 0.0);
+  }
+  return s;
+}
+
+// What the gradient of a row takes: e_j A for weights against M, and an entry's own value.
 struct RowGrad {
   float M;
   double A;
   float entry;
 };
-
-// Loss, status and the gradient's factors of row r from its entries and the sums of the
-// other ids (all ids without a tail), by one wavefront.
-__device__ __forceinline__ RowGrad finish_row(const DistillArgs& a, long long r, float weight,
-                                              const Entries& e, const Sums& other) {
-  const float z = e.z;
-  const float Ms = a.tail ? wave_maxn(e.id >= 0 ? z : kNegInf) : kNegInf;
-  const float M = fmaxn(other.M, Ms);
-  const int status = e.status ? e.status : M == kNegInf ? 2 : !(M < kPosInf) ? 1 : 0;
-  const double Zr = other.Z;
-  const double log_f = ((double)other.M - (double)M) * a.inv_t;
-  const double f = other.M > kNegInf ? exp_small(log_f) : 0.0;   // a weight against other.M, against M
-  const double ez =
-      e.id >= 0 ? (double)__builtin_amdgcn_exp2f(exponent(z, M, a.c)) : 0.0;
-  const double Z = Zr * f + (a.tail ? wave_sum(e.first ? ez : 0.0) : 0.0);
-  const double logZ = log_small(Z);
-  double term = 0.0;
-  if (e.q > 0.0) term = e.q * (e.log_q - (((double)z - (double)M) * a.inv_t - logZ));
-  double loss = wave_sum(term);
-  if (e.rest > 0.0)   // +inf where the draft gives the other ids nothing
-    loss += e.rest * (log_small(e.rest) - (other.M > kNegInf ? log_small(Zr) + log_f - logZ
-                                                       : -__builtin_huge_val()));
+__device__ __forceinline__ RowGrad row_grad_of(const DistillArgs& a, float weight,
+                                               const Entries& e, const RowSums& s) {
+  const double each = (double)weight * a.inv_t, whole = e.sum + e.rest;
+  const double f = a.tail ? (double)__builtin_amdgcn_exp2f(exponent(s.Mr, s.M, a.c)) : 1.0;
+  const double ez = e.id >= 0 ? (double)__builtin_amdgcn_exp2f(exponent(e.z, s.M, a.c)) : 0.0;
   const float nan = __uint_as_float(0x7FC00000u);
-  if (__lane_id() == 0) {
-    a.loss[r] = status ? nan : (float)(loss * weight);
-    if (a.status) a.status[r] = status;
-  }
-  const double each = (double)weight * a.inv_t;
-  const double whole = e.sum + e.rest;
   RowGrad g;
   // without an id outside S there is no weight to multiply: any M and a factor of 0
-  g.M = other.M == kNegInf ? 0.0f : other.M;
-  g.A = status ? (double)nan : Zr > 0.0 ? each * (whole * f / Z - e.rest / Zr) : 0.0;
-  g.entry = status ? nan : (float)(each * (whole * ez / Z - e.same));
+  g.M = s.Mr == kNegInf ? 0.0f : s.Mr;
+  g.A = s.status ? (double)nan : s.Zr > 0.0 ? each * (whole * f / s.Z - e.rest / s.Zr) : 0.0;
+  g.entry = s.status ? nan : (float)(each * (whole * ez / s.Z - e.same));
   return g;
+}
+
+// Loss and status of row r.
+__device__ __forceinline__ void put_loss(const DistillArgs& a, long long r, float weight,
+                                         const Entries& e, const RowSums& s) {
+  const double logZ = log_small(s.Z);
+  double term = 0.0;
+  if (e.q > 0.0) term = e.q * (e.log_q - (((double)e.z - (double)s.M) * a.inv_t - logZ));
+  double loss = wave_sum(term);
+  if (e.rest > 0.0) {   // +inf where the draft gives the other ids nothing
+    const double log_pr = s.Mr > kNegInf
+                              ? log_small(s.Zr) + ((double)s.Mr - (double)s.M) * a.inv_t - logZ
+                              : -__builtin_huge_val();
+    loss += e.rest * (log_small(e.rest) - log_pr);
+  }
+  if (__lane_id() == 0) {
+    a.loss[r] = s.status ? __uint_as_float(0x7FC00000u) : (float)(loss * weight);
+    if (a.status) a.status[r] = s.status;
+  }
 }
 
 // ------------------------------------------------------------ a row in one workgroup
@@ -131,7 +155,9 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
   __shared__ Sums each[BLOCK / kWave];
   __shared__ typename Slice<DT, NC, BLOCK>::LeftOut left_out;
   __shared__ Entries entries[kWave];   // kept here between the two uses: registers are short
+  __shared__ float own[kWave];         // the entries' gradients
   __shared__ struct {
+    RowSums sums;
     float M;
     double A;
   } row_grad;
@@ -157,28 +183,35 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
   const unsigned char* row = a.logits + r * a.stride_bytes;
   Slice<DT, NC, BLOCK> s;
   s.template load<ONCE>(row, a.V, 0, Cut{1, whole, NC});
-  if (a.tail) s.list_left_out(valid_id(a, id), left_out);
+  float z = kNegInf;
   if (threadIdx.x < kWave) {   // the row is on its way
-    const float z = valid_id(a, id) >= 0 ? load_elem<DT>(row, id) : kNegInf;
+    if (valid_id(a, id) >= 0) z = load_elem<DT>(row, id);
     entries[threadIdx.x] = entries_of(a, id, t);
-    sched_fence();   // z comes after the wavefront's share of the row
-    entries[threadIdx.x].z = z;
   }
   if (a.tail) s.leave_out(a.V, valid_id(a, id), left_out);
   float off;
   const float m = s.largest([](int, float) {});
   const Sums mine = s.template sums<false>(a.V, m, a.c, off);
+  if (threadIdx.x < kWave) entries[threadIdx.x].z = z;   // it came last
   const Sums other = join_block<BLOCK / kWave>(mine, a.c, off, each);
-  float own = 0.0f;   // the entry's gradient
+  if (!out) {
+    if (threadIdx.x < kWave) {
+      const Entries& e = entries[threadIdx.x];
+      put_loss(a, r, weight, e, row_sums(a, e, other));
+    }
+    return;
+  }
   if (threadIdx.x < kWave) {
-    const RowGrad g = finish_row(a, r, weight, entries[threadIdx.x], other);
-    own = g.entry;
+    const Entries& e = entries[threadIdx.x];
+    const RowSums sums = row_sums(a, e, other);
+    const RowGrad g = row_grad_of(a, weight, e, sums);
+    own[threadIdx.x] = g.entry;
     if (threadIdx.x == 0) {
+      row_grad.sums = sums;
       row_grad.M = g.M;
       row_grad.A = g.A;
     }
   }
-  if (!out) return;
   __syncthreads();
   const GradRow p(row_grad.M, a.c, row_grad.A, 0.0);
   const Pass pass;
@@ -201,9 +234,11 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
   if ((int)threadIdx.x < a.V - whole * EPC)
     store_elem<DT>(out, whole * EPC + (int)threadIdx.x,
                    p.at(load_elem<DT>(row, whole * EPC + (int)threadIdx.x)));
+  // the loss, while the others store
+  if (threadIdx.x < kWave) put_loss(a, r, weight, entries[threadIdx.x], row_grad.sums);
   __syncthreads();   // the entries' own values over what was put there
   if (threadIdx.x < kWave && entries[threadIdx.x].first)
-    store_elem<DT>(out, entries[threadIdx.x].id, own);
+    store_elem<DT>(out, entries[threadIdx.x].id, own[threadIdx.x]);
 }
 
 // ------------------------------------------------------------ wider rows
@@ -231,10 +266,7 @@ __global__ __launch_bounds__(kSliceBlock) void distill_slice_kernel(DistillArgs 
   const int id = a.tail ? valid_id(a, raw_id(a, r)) : -1;
   Slice<DT, NC> s;
   s.template load<false>(a.logits + r * a.stride_bytes, a.V, slice, cut);
-  if (a.tail) {
-    s.list_left_out(id, left_out);
-    s.leave_out(a.V, id, left_out);
-  }
+  if (a.tail) s.leave_out(a.V, id, left_out);
   float off;
   const float m = s.largest([](int, float) {});
   const Sums mine = s.template sums<false>(a.V, m, a.c, off);
@@ -265,7 +297,9 @@ __global__ __launch_bounds__(kSliceBlock) void distill_join_kernel(DistillArgs a
   const Sums other = join_slices(ws.sums + r * slices, slices, a.c);
   Entries e = entries_of(a, id, t);
   e.z = z;
-  const RowGrad g = finish_row(a, r, weight, e, other);
+  const RowSums sums = row_sums(a, e, other);
+  put_loss(a, r, weight, e, sums);
+  const RowGrad g = row_grad_of(a, weight, e, sums);
   if (lane == 0) ws.rows[r] = DtRow{g.A, g.M, weight};
   if (lane < a.k) ws.entry[r * a.k + lane] = g.entry;
 }

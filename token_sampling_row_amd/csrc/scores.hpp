@@ -50,7 +50,7 @@ __device__ __forceinline__ double exp_small(double x) {
   double y = fma(r, fma(r, fma(r, fma(r, 1.0 / 24.0, 1.0 / 6.0), 0.5), 1.0), 1.0);
 #pragma unroll 1
   for (int i = 0; i < 16; ++i) y *= y;
-  return y;
+  return x < -740.0 ? 0.0 : y;
 }
 // ln a, a > 0: y from the hardware's log2 of a's mantissa m (2^-23 off), then the step to
 // y + ln(m e^-y), whose argument is next to 1: exact to 2^-36.
