@@ -147,6 +147,12 @@ __device__ __forceinline__ void put_loss(const DistillArgs& a, long long r, floa
   }
 }
 
+// A row that does not count.
+__device__ __forceinline__ void put_nothing(const DistillArgs& a, long long r) {
+  a.loss[r] = 0.0f;
+  if (a.status) a.status[r] = 0;
+}
+
 // ------------------------------------------------------------ a row in one workgroup
 // Read once: the gradient is formed from the registers that the sums were.
 template <int DT, int NC, int BLOCK, bool ONCE>
@@ -172,10 +178,7 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
       if ((int)threadIdx.x < a.V - whole * EPC)
         store_elem<DT>(out, whole * EPC + (int)threadIdx.x, 0.0f);
     }
-    if (threadIdx.x == 0) {
-      a.loss[r] = 0.0f;
-      if (a.status) a.status[r] = 0;
-    }
+    if (threadIdx.x == 0) put_nothing(a, r);
     return;
   }
   const int id = raw_id(a, r);
@@ -274,6 +277,20 @@ __global__ __launch_bounds__(kSliceBlock) void distill_slice_kernel(DistillArgs 
   if (threadIdx.x == 0) ws.sums[r * cut.slices + slice] = all;
 }
 
+// Row r's entries and the sums of its slices, by one wavefront.
+template <int DT>
+__device__ __forceinline__ RowSums join_row(const DistillArgs& a, long long r, const Sums* sums,
+                                            int slices, Entries& e) {
+  const int id = raw_id(a, r);
+  const float t = teacher_of(a, r);
+  const float z =
+      valid_id(a, id) >= 0 ? load_elem<DT>(a.logits + r * a.stride_bytes, id) : kNegInf;
+  const Sums other = join_slices(sums, slices, a.c);
+  e = entries_of(a, id, t);
+  e.z = z;
+  return row_sums(a, e, other);
+}
+
 // One wavefront to a row.
 template <int DT>
 __global__ __launch_bounds__(kSliceBlock) void distill_join_kernel(DistillArgs a, int slices,
@@ -284,48 +301,63 @@ __global__ __launch_bounds__(kSliceBlock) void distill_join_kernel(DistillArgs a
   const float weight = a.weight ? a.weight[r] : 1.0f;
   if (weight == 0.0f) {
     if (lane == 0) {
-      a.loss[r] = 0.0f;
-      if (a.status) a.status[r] = 0;
+      put_nothing(a, r);
       ws.rows[r].weight = 0.0f;
     }
     return;
   }
-  const int id = raw_id(a, r);
-  const float t = teacher_of(a, r);
-  const float z =
-      valid_id(a, id) >= 0 ? load_elem<DT>(a.logits + r * a.stride_bytes, id) : kNegInf;
-  const Sums other = join_slices(ws.sums + r * slices, slices, a.c);
-  Entries e = entries_of(a, id, t);
-  e.z = z;
-  const RowSums sums = row_sums(a, e, other);
+  Entries e;
+  const RowSums sums = join_row<DT>(a, r, ws.sums + r * slices, slices, e);
   put_loss(a, r, weight, e, sums);
   const RowGrad g = row_grad_of(a, weight, e, sums);
   if (lane == 0) ws.rows[r] = DtRow{g.A, g.M, weight};
   if (lane < a.k) ws.entry[r * a.k + lane] = g.entry;
 }
 
-// One workgroup to a tile of a row.
-template <int DT>
+// One workgroup to a tile of a row, the last rows first: they are what the caches still
+// hold of the pass before. ONCE: written past the caches. JOIN: with the row's join in each
+// of its tiles (where there are few, that takes less than a launch of its own).
+template <int DT, bool ONCE, bool JOIN>
 __global__ __launch_bounds__(kSliceBlock) void distill_grad_kernel(DistillArgs a, int tiles,
-                                                                   DtWs ws) {
-  const int tile = blockIdx.x % tiles;
-  const long long r = blockIdx.x / tiles;
+                                                                   int slices, DtWs ws) {
+  __shared__ DtRow joined;
+  const int tile = blockIdx.x % tiles, lane = __lane_id();
+  const long long r = a.rows - 1 - (long long)(blockIdx.x / tiles);
   unsigned char* out = a.grad + r * a.grad_stride_bytes;
-  const DtRow d = ws.rows[r];
+  float own = 0.0f;   // the entry's gradient, in the first wavefront
+  DtRow d;
+  if constexpr (JOIN) {
+    d.weight = a.weight ? a.weight[r] : 1.0f;
+    if (d.weight != 0.0f) {
+      if (threadIdx.x < kWave) {
+        Entries e;
+        const RowSums sums = join_row<DT>(a, r, ws.sums + r * slices, slices, e);
+        const RowGrad g = row_grad_of(a, d.weight, e, sums);
+        own = g.entry;
+        if (lane == 0) joined = DtRow{g.A, g.M, d.weight};
+        if (tile == 0) put_loss(a, r, d.weight, e, sums);
+      }
+      __syncthreads();
+      d = joined;
+    } else if (tile == 0 && threadIdx.x == 0) {
+      put_nothing(a, r);
+    }
+  } else {
+    d = ws.rows[r];
+    if (lane < a.k && d.weight != 0.0f) own = ws.entry[r * a.k + lane];
+  }
   if (d.weight == 0.0f) {
     zero_tile<DT>(out, a.V, tile);
     return;
   }
-  const int id = valid_id(a, raw_id(a, r)), lane = __lane_id();
-  const float own = lane < a.k ? ws.entry[r * a.k + lane] : 0.0f;
-  put_tile<DT, false>(a.logits + r * a.stride_bytes, out, a.V, tile, GradRow(d.M, a.c, d.A, 0.0));
+  const int id = valid_id(a, raw_id(a, r));
+  put_tile<DT, ONCE>(a.logits + r * a.stride_bytes, out, a.V, tile, GradRow(d.M, a.c, d.A, 0.0));
   const bool here = id >= 0 && id / kTileIds<DT> == tile;
   if (!__any(here)) return;   // the same for all of the workgroup
   __syncthreads();
   // an id that comes twice has the same value with each
   if (threadIdx.x < kWave && here) store_elem<DT>(out, id, own);
 }
-
 
 // Rows of up to this many chunks take one workgroup each, and are read once.
 constexpr int kHalfBlock = 512, kRowBlock = 1024;
@@ -379,6 +411,9 @@ void launch_slices(const DistillArgs& a, const Cut& cut, const DtWs& ws, hipStre
   }
 }
 
+// Batches of up to this many tiles join their rows in each.
+constexpr int kJoinTiles = 4096;
+
 // Rows whose slices and tiles a batch holds: 2^23 workgroups of a launch at most.
 int dt_batch(const Cut& cut, int rows, int tiles) {
   return std::min(batch_of(cut, rows), max(1, (1 << 23) / tiles));
@@ -387,8 +422,8 @@ int dt_batch(const Cut& cut, int rows, int tiles) {
 template <int DT>
 hipError_t launch_dt(const DistillArgs& all, void* workspace, hipStream_t s) {
   const Cut cut = dt_cut(DT, all.rows, all.V);
+  const long long bytes = 2ll * all.rows * all.V * Fmt<DT>::ESZ;
   if (cut.slices == 1) {
-    const long long bytes = 2ll * all.rows * all.V * Fmt<DT>::ESZ;
     all.grad && bytes > kOnceBytes ? launch_rows<DT, true>(all, cut, s)
                                    : launch_rows<DT, false>(all, cut, s);
     return hipGetLastError();
@@ -411,15 +446,25 @@ hipError_t launch_dt(const DistillArgs& all, void* workspace, hipStream_t s) {
     launch_slices<DT>(a, cut, ws, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((distill_join_kernel<DT>), dim3((a.rows + kSliceWaves - 1) / kSliceWaves),
-                       dim3(kSliceBlock), 0, s, a, cut.slices, ws);
-    e = hipGetLastError();
-    if (e != hipSuccess || !a.grad) {
+    const dim3 block(kSliceBlock);
+    const bool join = a.grad && (long long)a.rows * tiles <= kJoinTiles;
+    if (!join) {
+      hipLaunchKernelGGL((distill_join_kernel<DT>),
+                         dim3((a.rows + kSliceWaves - 1) / kSliceWaves), block, 0, s, a, cut.slices,
+                         ws);
+      e = hipGetLastError();
       if (e != hipSuccess) return e;
-      continue;
+      if (!a.grad) continue;
     }
-    hipLaunchKernelGGL((distill_grad_kernel<DT>), dim3(a.rows * tiles), dim3(kSliceBlock), 0, s, a,
-                       tiles, ws);
+    const auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(a.rows * tiles), block, 0, s, a, tiles, cut.slices, ws);
+    };
+    if (join)
+      launch(distill_grad_kernel<DT, false, true>);
+    else if (bytes > kOnceBytes)
+      launch(distill_grad_kernel<DT, true, false>);
+    else
+      launch(distill_grad_kernel<DT, false, false>);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

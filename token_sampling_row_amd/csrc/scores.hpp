@@ -48,7 +48,7 @@ struct Pass {
 __device__ __forceinline__ double exp_small(double x) {
   const double r = fmax(x, -740.0) * 0x1p-16;
   double y = fma(r, fma(r, fma(r, fma(r, 1.0 / 24.0, 1.0 / 6.0), 0.5), 1.0), 1.0);
-#pragma unroll 1
+#pragma unroll
   for (int i = 0; i < 16; ++i) y *= y;
   return x < -740.0 ? 0.0 : y;
 }
