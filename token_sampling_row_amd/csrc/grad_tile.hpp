@@ -21,8 +21,8 @@ __device__ __forceinline__ void store16(void* p, uint4 v) {
   }
 }
 
-// Ids [tile * kTileIds, ...) of a row of V. ONCE: written past the caches.
-template <int DT, bool ONCE>
+// Ids [tile * kTileIds, ...) of a row of V. READ_ONCE, WRITE_ONCE: past the caches.
+template <int DT, bool READ_ONCE, bool WRITE_ONCE>
 __device__ __forceinline__ void put_tile(const unsigned char* row, unsigned char* out, int V,
                                          int tile, const GradRow& g) {
   constexpr int EPC = Fmt<DT>::EPC;
@@ -30,9 +30,10 @@ __device__ __forceinline__ void put_tile(const unsigned char* row, unsigned char
   const int first = tile * kSliceBlock * kTileChunks + (int)threadIdx.x;
   uint4 c[kTileChunks];
 #pragma unroll
-  for (int j = 0; j < kTileChunks; ++j)   // chunks past the last whole one repeat it
-    c[j] = whole ? load16(row + (long long)min(first + j * kSliceBlock, whole - 1) * 16)
-                 : make_uint4(0, 0, 0, 0);
+  for (int j = 0; j < kTileChunks; ++j) {   // chunks past the last whole one repeat it
+    const unsigned char* p = row + (long long)min(first + j * kSliceBlock, whole - 1) * 16;
+    c[j] = whole == 0 ? make_uint4(0, 0, 0, 0) : READ_ONCE ? load16_once(p) : load16(p);
+  }
   const auto all = [&](auto&& of) {
 #pragma unroll
     for (int j = 0; j < kTileChunks; ++j) {
@@ -41,7 +42,7 @@ __device__ __forceinline__ void put_tile(const unsigned char* row, unsigned char
 #pragma unroll
       for (int e = 0; e < EPC; ++e) v[e] = of(v[e]);
       const int i = first + j * kSliceBlock;
-      if (i < whole) store16<ONCE>(out + (long long)i * 16, pack<DT>(v));
+      if (i < whole) store16<WRITE_ONCE>(out + (long long)i * 16, pack<DT>(v));
     }
   };
   if (g.plain)

@@ -226,7 +226,7 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
 #pragma unroll
       for (int i = 0; i < EPC; ++i) v[i] = of(v[i]);
       unsigned char* base = out + j * BLOCK * 16;   // uniform
-      if (j * BLOCK + (int)threadIdx.x < whole) store16<ONCE>(base + threadIdx.x * 16u, pack<DT>(v));
+      if (j * BLOCK + (int)threadIdx.x < whole) store16<false>(base + threadIdx.x * 16u, pack<DT>(v));
       sched_fence();
     }
   };
@@ -351,7 +351,7 @@ __global__ __launch_bounds__(kSliceBlock) void distill_grad_kernel(DistillArgs a
     return;
   }
   const int id = valid_id(a, raw_id(a, r));
-  put_tile<DT, ONCE>(a.logits + r * a.stride_bytes, out, a.V, tile, GradRow(d.M, a.c, d.A, 0.0));
+  put_tile<DT, false, ONCE>(a.logits + r * a.stride_bytes, out, a.V, tile, GradRow(d.M, a.c, d.A, 0.0));
   const bool here = id >= 0 && id / kTileIds<DT> == tile;
   if (!__any(here)) return;   // the same for all of the workgroup
   __syncthreads();
@@ -374,9 +374,11 @@ Cut dt_cut(int dtype, int rows, int vocab) {
   return cut_of(whole, std::min({1024 / max(rows, 1), 64, (whole + kSliceBlock - 1) / kSliceBlock}));
 }
 
-// Batches of more bytes than this, logits and gradient together, are read and written past
-// the caches, which could not keep them.
-constexpr long long kOnceBytes = 192ll << 20;   // TUNE
+// Batches of more bytes than this, logits and gradient together, are read past the caches,
+// which could not keep them: 1024 x 128256 bf16 105 us against 128, 1022 x 64000 50 against
+// 58. (Slices are read from the caches again, and it is their gradient that is written
+// past them: 512 x 128256 fp32 132 us against 157.)
+constexpr long long kOnceBytes = 192ll << 20;
 
 template <int DT, bool ONCE>
 void launch_rows(const DistillArgs& a, const Cut& cut, hipStream_t s) {

@@ -126,6 +126,11 @@ __device__ __forceinline__ double wave_max_f64(double x) {
   return wave_reduce(x, [](double a, double b) { return fmax(a, b); });
 }
 
+template <bool ONCE>
+__device__ __forceinline__ uint4 load_chunk(const unsigned char* p) {
+  return ONCE ? load16_once(p) : load16(p);
+}
+
 // A float that the compiler does not know: what is formed of it is formed where it is
 // used and not kept from an earlier use.
 __device__ __forceinline__ float opaque(float x) {
@@ -133,8 +138,9 @@ __device__ __forceinline__ float opaque(float x) {
   return x;
 }
 
-// Rows in registers, NC chunks a lane; WPR wavefronts to a row, four in a workgroup.
-template <int DT, int WT, int WPR, int NC>
+// Rows in registers, NC chunks a lane; WPR wavefronts to a row, four in a workgroup. ONCE:
+// read past the caches.
+template <int DT, int WT, int WPR, int NC, bool ONCE>
 __global__ __launch_bounds__(kNormBlock) void norm_kernel(NormArgs a) {
   constexpr int EPC = Fmt<DT>::EPC, T = WPR * kWave, RPB = kNormBlock / T;
   constexpr bool SHORT = DT == 1 && WT == 1;   // 16 bits of a product: exact in float32
@@ -151,7 +157,8 @@ __global__ __launch_bounds__(kNormBlock) void norm_kernel(NormArgs a) {
   const unsigned char* x = a.x + at * a.x_stride;
   uint4 c[NC], rest{};
 #pragma unroll
-  for (int j = 0; j < NC; ++j) c[j] = load16(x + (long long)min(j * T + t, whole - 1) * 16);
+  for (int j = 0; j < NC; ++j)
+    c[j] = load_chunk<ONCE>(x + (long long)min(j * T + t, whole - 1) * 16);
   if (partial) rest = load_chunk_zero<DT>(x, (long long)whole * EPC, a.width);
   float w[NC][EPC], wr[EPC];
 #pragma unroll
@@ -160,7 +167,8 @@ __global__ __launch_bounds__(kNormBlock) void norm_kernel(NormArgs a) {
     const unsigned char* res = a.residual + at * a.r_stride;
     uint4 d[NC];
 #pragma unroll
-    for (int j = 0; j < NC; ++j) d[j] = load16(res + (long long)min(j * T + t, whole - 1) * 16);
+    for (int j = 0; j < NC; ++j)
+      d[j] = load_chunk<ONCE>(res + (long long)min(j * T + t, whole - 1) * 16);
 #pragma unroll
     for (int j = 0; j < NC; ++j)
       load_weights<EPC, WT>(a.weight, min(j * T + t, whole - 1) * EPC, a.width, w[j]);
@@ -360,12 +368,21 @@ __global__ __launch_bounds__(kNormBlock) void norm_wide_kernel(NormArgs a) {
   }
 }
 
+// Inputs of more bytes than this are read past the caches, which could not keep them: 16384 x
+// 4096 bf16 with a residual 75 us against 84. Smaller ones may be there still: 4096 x 4096
+// 23 us read from them, 26 past them.
+constexpr long long kNormOnceBytes = 192ll << 20;
+
 template <int DT, int WT, int WPR, int NC>
 hipError_t launch_nc(const NormArgs& a, hipStream_t s) {
   constexpr int RPB = kNormBlock / (WPR * kWave);
-  const int blocks = (a.rows + RPB - 1) / RPB;
-  hipLaunchKernelGGL((norm_kernel<DT, WT, WPR, NC>), dim3(blocks), dim3(kNormBlock), 0, s, a);
-  return hipGetLastError();
+  const auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((a.rows + RPB - 1) / RPB), dim3(kNormBlock), 0, s, a);
+    return hipGetLastError();
+  };
+  const long long bytes = (long long)a.rows * a.width * Fmt<DT>::ESZ * (a.residual ? 2 : 1);
+  return bytes > kNormOnceBytes ? launch(norm_kernel<DT, WT, WPR, NC, true>)
+                                : launch(norm_kernel<DT, WT, WPR, NC, false>);
 }
 
 template <int DT, int WT>
