@@ -462,7 +462,7 @@ int verify_probs_workspace(int dtype, int rows, int vocab);
  * h w holds NaN or an infinity (h rounded to its type, h w in 64 bits) gets scale
  * NaN and codes 0, as in quantize_rows. eps is finite and >= 0. Bytes between
  * the rows are left as they are. Outputs that overlap inputs or each other in any
- * other way are TSR_EINVAL.
+ * other way are TSR_EINVAL (rows of the same stride may lie between each other's).
  * rows is not bound by the handle's max_rows; rows < 2^24, width <= 2^30 and
  * strides < 2^36 (TSR_EUNSUPPORTED beyond). Uses no workspace. */
 int norm_quantize_rows(tsr_handle h, const void* x, int64_t x_stride, const void* residual,
@@ -498,7 +498,7 @@ typedef struct {
  * and a teacher's top tokens for distill_topk.
  *  logits [rows][vocab] of type dtype, row_stride elements apart. Logits of -inf
  *      (tokens that are not allowed) have p = 0 and log p = -inf.
- *  temperature: finite, >= 1e-30.
+ *  temperature: 1e-30 .. 1e30.
  *  tokens [rows][n_tokens] int32 (NULL with n_tokens 0); -1 is padding, as the
  *      verify steps leave behind the last token: its log p is 0.
  *  workspace: 16-byte aligned device memory of at least token_logprobs_workspace

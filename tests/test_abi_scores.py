@@ -62,6 +62,38 @@ def test_norm_quantize_rows(lib, handle, mem):  # noqa: F811
                          (dict(qs=1 << 36), EUNSUPPORTED)])
 
 
+def test_rows_between_each_others(lib, handle, mem):  # noqa: F811
+    """Columns of one larger matrix do not overlap: such calls come as far as the device,
+    which is not there (TSR_EDEVICE), or is (TSR_OK would run them: only without one)."""
+    if torch.cuda.is_available():
+        pytest.skip("would run on host memory")
+
+    def norm(x, xs, r, rs, oh, hs, q, qs, rows=4, width=16, sc=mem + 20480):
+        return lib.norm_quantize_rows(handle, x, xs, r, rs, 0, None, 0, 1e-6, rows, width, oh, hs, q,
+                                      qs, sc, None)
+
+    at, W = mem, 16
+    # x | residual | sum | codes in rows of 64 floats, the codes in the last quarter
+    assert norm(at, 64, at + 64, 64, at + 128, 64, at + 192, 256) == 3
+    assert norm(at + 192, 64, at + 128, 64, at + 64, 64, at, 256) == 3
+    # the last row's columns wrap into the next row's: still apart
+    assert norm(at + 64, 64, at + 128, 64, at + 192, 64, at + 256, 256) == 3
+    for bad in (at + 4, at + 60, at + 128 + 64 - 4):   # a column too many
+        assert norm(at, 64, at + 128, 64, bad, 64, at + 8192, 64) == 1
+    assert norm(at, 64, at + 128, 64, at + 64, 48, at + 8192, 64) == 1   # other strides
+    # a single row in a gap, and one that is no gap
+    assert norm(at, 64, None, 0, None, 0, at + 64, 64, rows=1, width=W) == 3
+    assert norm(at, 64, None, 0, None, 0, at + 63, 64, rows=1, width=W) == 1
+
+    def grad(z_at, out, zs=64, os=64):
+        return lib.token_logprobs_grad(handle, z_at, 0, 4, 16, zs, 1.0, None, 0, mem + 9000 // 4 * 4,
+                                       None, None, None, out, os, None)
+
+    assert grad(at, at + 64) == 3 and grad(at + 64, at) == 3 and grad(at, at + 192) == 3
+    assert grad(at, at + 60) == 1 and grad(at, at + 196) == 1 and grad(at, at) == 1
+    assert grad(at, at + 64, 64, 32) == 1
+
+
 def test_token_logprobs(lib, handle, mem):  # noqa: F811
     def call(h, z, dt, rows, V, stride, T, tok, n, k, out, ws=None, size=0):
         o = None if out is None else ctypes.byref(tsr._Logprobs(*out))
@@ -77,7 +109,7 @@ def test_token_logprobs(lib, handle, mem):  # noqa: F811
 
     bad = [dict(h=None), dict(z=None), dict(out=None), dict(dt=-1), dict(rows=-1), dict(V=0),
            dict(stride=63), dict(z=mem + 1), dict(z=mem + 2), dict(T=0.0), dict(T=-1.0),
-           dict(T=float("nan")), dict(T=float("inf")), dict(T=1e-31), dict(tok=None), dict(n=-1),
+           dict(T=float("nan")), dict(T=float("inf")), dict(T=1e-31), dict(T=1e31), dict(tok=None), dict(n=-1),
            dict(k=-1), dict(tok=mem + 4098), out(0, None), out(2, None), out(3, None)]
     bad += [out(i, good[i] + 2) for i in range(6)]
     refused(call, base, [(c, EINVAL) for c in bad])

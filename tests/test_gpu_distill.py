@@ -87,6 +87,39 @@ def test_many_rows(s, dtype, rows, V, tail):
         assert bool((d <= lim).all())
 
 
+@pytest.mark.parametrize("dtype,rows,V", [("f32", 200, 32000), ("bf16", 140, 128256),
+                                          ("bf16", 130, 33003), ("f32", 400, 32003),
+                                          ("bf16", 1000, 128253), ("bf16", 120, 300005),
+                                          ("f32", 8195, 100003), ("bf16", 20000, 1003),
+                                          ("bf16", 3000, 33003), ("bf16", 2, 5_000_011)])
+def test_every_way_that_rows_are_divided(s, dtype, rows, V):
+    """A workgroup of each size to a row, slices joined in each tile or by themselves, more
+    rows than the workspace holds at a time, read from the caches or past them: rows on
+    either side of the limits against the reference."""
+    g = torch.Generator(device()).manual_seed(V)
+    z = torch.empty(rows, V, dtype=TD[dtype], device=device()).normal_(generator=g)
+    ids = torch.randint(0, V, (rows, 12), device=device(), generator=g).int()
+    ids[:, 5] = ids[:, 6]
+    ids[:, 7] = V - 1
+    ids[:, 8] = -1
+    lp = torch.log_softmax(2 * torch.randn(rows, 13, device=device(), generator=g), 1)[:, :12]
+    lp = lp.contiguous()
+    w = torch.rand(rows, device=device(), generator=g)
+    st = new_status(rows)
+    if rows > 2:
+        w[1] = 0.0
+        z[rows - 2, V - 1] = float("nan")
+    some = sorted({0, 1, 8191 % rows, 8192 % rows, rows // 2, max(0, rows - 2), rows - 1})
+    for tail in (True, False):
+        loss, grad = s.distill_topk(z, ids, lp, 1.3, tail, w, status=st)
+        check((loss[some], grad[some]), z[some], ids[some].cpu().numpy(), lp[some].cpu().numpy(),
+              1.3, tail, w[some].cpu().numpy(), st[some])
+        alone, _ = s.distill_topk(z, ids, lp, 1.3, tail, w, grad=False)
+        d = (alone - loss).abs()   # the sums may be divided otherwise: twice their bound
+        assert bool((d <= 4 * 60 * sc.U * (1 + loss.abs())).logical_or(d.isnan()).all())
+        assert int((st != 0).sum()) == (rows > 2)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [50, 40003])
 def test_special_rows(s, dtype, V):
@@ -178,6 +211,39 @@ def test_strided_rows(s, dtype, off, V):
     got = s.distill_topk(z, dev(ids), dev(lp), tail=True, grad=out[:, off:off + V])
     check(got, z, ids, lp, 1.0, True)
     assert bool((out[:, :off] == 77).all()) and bool((out[:, off + V:] == 77).all())
+
+
+@pytest.mark.parametrize("T", [1e-6, 1e6, 1e30])
+@pytest.mark.parametrize("V", [9001, 150003])
+def test_temperatures_far_from_one(s, T, V):
+    rng = np.random.default_rng(12)
+    z = rng.normal(0, 3, (3, V)).astype(np.float32)
+    z[1, ::5] = -np.inf
+    z[2] *= 1e10
+    ids = np.stack([rng.permutation(V)[:4] for _ in range(3)]).astype(np.int32)
+    ids[:, 0] = z.argmax(1)
+    ids[1, 1:] = [1, 2, 3]
+    lp = np.log(np.full((3, 4), 0.2, dtype=np.float32))
+    for tail in (False, True):
+        t = dev(z)
+        check(s.distill_topk(t, dev(ids), dev(lp), T, tail), t, ids, lp, T, tail)
+
+
+@pytest.mark.parametrize("rows", [3, 130])
+def test_gradient_in_columns_of_one_matrix(s, rows):
+    """The gradient beside its logits in the rows of one tensor."""
+    rng = np.random.default_rng(13)
+    V = 40001
+    big = torch.zeros(rows, 2 * V, device=device())
+    z = big[:, :V]
+    z.copy_(logits(rng, rows, V, "f32"))
+    ids, lp = teacher_of(rng, z, 5, 1.0)
+    before = z.clone()
+    got = s.distill_topk(z, dev(ids), dev(lp), 1.0, True, grad=big[:, V:])
+    assert torch.equal(z, before)
+    check(got, z, ids, lp, 1.0, True, rows=[0, rows - 1])
+    with pytest.raises(tsr.TsrError):
+        s.distill_topk(z, dev(ids), dev(lp), 1.0, True, grad=big[:, V - 1:-1])
 
 
 def test_refusals(s):

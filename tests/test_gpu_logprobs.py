@@ -114,6 +114,30 @@ def test_many_rows(s, dtype, rows, V, k):
             assert bool(((a - b).abs() <= 2 * 45 * sc.U * (1 + b.abs())).all()), name
 
 
+@pytest.mark.parametrize("dtype,rows,V,k", [("bf16", 1100, 70001, 20), ("bf16", 1100, 70001, 0),
+                                            ("bf16", 9000, 8190, 5), ("f32", 9000, 4101, 64),
+                                            ("f32", 20000, 1001, 3), ("bf16", 17000, 33001, 50),
+                                            ("f32", 8195, 20011, 0), ("bf16", 35000, 2500, 0)])
+def test_batches_past_the_caches_and_the_workspace(s, dtype, rows, V, k):
+    """More than 128 MB of logits, more than 8192 rows: rows on either side of each limit
+    against the reference, forward and backward."""
+    g = torch.Generator(device()).manual_seed(V)
+    z = torch.empty(rows, V, dtype=TD[dtype], device=device()).normal_(generator=g)
+    tok = torch.randint(0, V, (rows, 2), device=device(), generator=g).int()
+    st = new_status(rows)
+    z[rows - 2] = float("nan")
+    z[rows - 3, 5] = float("inf")
+    got = s.token_logprobs(z, tok, top_k=k, status=st)
+    some = sorted({0, 1, 8191 % rows, 8192 % rows, 16383 % rows, 16384 % rows, rows // 2, rows - 3,
+                   rows - 2, rows - 1})
+    part = tsr.TokenLogprobs(*(None if t is None else t[some] for t in got))
+    check(part, z[some], tok[some].cpu().numpy(), k, 1.0)
+    up = torch.randn(rows, 2, device=device(), generator=g)
+    grad = s.token_logprobs_grad(z, tok, got.norm, up)
+    check_grad(grad[some], z[some], tok[some].cpu().numpy(), got.norm[some], up[some])
+    assert int((st != 0).sum()) == 2
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_special_rows(s, dtype):
     V = 40003
@@ -315,6 +339,26 @@ def test_many_tokens(s):
         s.token_logprobs(z, temperature=0.0)
     with pytest.raises(tsr.TsrError):   # the gradient in the logits' place
         s.token_logprobs_grad(z, dev(tok), fwd.norm, g, out=z)
+
+
+@pytest.mark.parametrize("T", [1e-30, 1e-6, 1e6, 1e30])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_temperatures_far_from_one(s, dtype, T):
+    """Down to the largest logit alone, up to all finite logits alike."""
+    rng = np.random.default_rng(11)
+    z = rng.normal(0, 3, (3, 33001)).astype(np.float32)
+    z[1, ::5] = -np.inf
+    z[2] *= 1e20
+    t = dev(z).to(TD[dtype])
+    tok = np.tile(np.array([[7, 5]], dtype=np.int32), (3, 1))
+    tok[:, 1] = t.float().cpu().numpy().argmax(1)
+    got = s.token_logprobs(t, dev(tok), top_k=4, temperature=T)
+    check(got, t, tok, 4, T)
+    g = dev(rng.normal(0, 1, (3, 2)).astype(np.float32))
+    ge = dev(rng.normal(0, 1, 3).astype(np.float32))
+    if T >= 1e-6:   # 1 / T times a gradient is a float32 number
+        grad = s.token_logprobs_grad(t, dev(tok), got.norm, g, got.entropy, ge, temperature=T)
+        check_grad(grad, t, tok, got.norm, g, T, got.entropy, ge)
 
 
 def test_a_vocabulary_of_millions(s):

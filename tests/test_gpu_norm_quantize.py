@@ -83,6 +83,22 @@ def test_many_rows(s, dtype, rows, width):
             assert bool(((a == b) | ((a != a) & (b != b))).all())
 
 
+@pytest.mark.parametrize("dtype,rows,width", [("bf16", 100001, 1007), ("bf16", 200003, 511),
+                                              ("bf16", 24581, 4097), ("f32", 9001, 5603),
+                                              ("f32", 66003, 763), ("bf16", 13001, 8195),
+                                              ("f32", 190001, 255)])
+def test_large_inputs(s, dtype, rows, width):
+    """Inputs that outgrow the caches, against the same rows in small batches."""
+    g = torch.Generator(device()).manual_seed(rows)
+    x = torch.empty(rows, width, dtype=TD[dtype], device=device()).normal_(generator=g)
+    w = torch.rand(width, device=device(), generator=g) + 0.5
+    got = s.norm_quantize_rows(x, w, 1e-6, x)
+    check([t[-3:] for t in got], x[-3:], w, 1e-6, x[-3:])
+    for r0 in range(0, rows, 8000):
+        part = s.norm_quantize_rows(x[r0:r0 + 8000], w, 1e-6, x[r0:r0 + 8000])
+        assert all(torch.equal(a, b[r0:r0 + 8000]) for a, b in zip(part, got))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_special_rows(s, dtype):
     W = 515
@@ -184,6 +200,19 @@ def test_the_sum_in_place(s, dtype, rows, width, on):
     assert got[2] is target
     check(got, x, None, 1e-6, res, before)
     assert torch.equal(other, res if on == "x" else x)
+
+
+def test_columns_of_one_matrix(s):
+    """x, the residual and the sum side by side in the rows of one tensor."""
+    rng = np.random.default_rng(4)
+    big = rows_of(rng, 7, 3 * 301, "f32")
+    x, res, keep = big[:, :301], big[:, 301:602], big[:, 602:]
+    before = (vals(x), vals(res))
+    got = s.norm_quantize_rows(x, None, 1e-6, res, out_residual=keep)
+    check(got, x, None, 1e-6, res, before)
+    assert np.array_equal(vals(x), before[0]) and np.array_equal(vals(res), before[1])
+    with pytest.raises(tsr.TsrError):
+        s.norm_quantize_rows(x, None, 1e-6, res, out_residual=big[:, 300:601])
 
 
 def test_the_same_codes_as_of_rows_normed_before(s):

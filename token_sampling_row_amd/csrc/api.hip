@@ -42,6 +42,7 @@ static_assert(offsetof(tsr::RowParams, temperature) == offsetof(tsr_params, temp
               "tsr_params layout");
 
 constexpr double kTemperatureMin = 1e-30;
+constexpr double kTemperatureMax = 1e30;   // of the scoring calls
 constexpr int kMaxDraft = 32;
 constexpr int kMaxTreeNodes = 32;
 
@@ -152,15 +153,29 @@ constexpr int kMaxScoreRows = (1 << 22) - 1;    // 256 threads a slice of a row,
 constexpr int64_t kMaxScoreStride = 1ll << 36;   // rows times it, in bytes, within 2^63
 constexpr int kMaxScoreTokens = 1024;           // the gradient compares a row's tokens in pairs
 
-// Whether [a, a + n) and [b, b + m) have a byte in common.
-bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a && b && n > 0 && m > 0 && x < y + (uintptr_t)m && y < x + (uintptr_t)n;
-}
+// Memory of `rows` rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+  const void* at;
+  int64_t stride, width;
+  int rows;
+};
 
-// Bytes from the first row's start to the last one's end.
-int64_t extent(int rows, int width, int64_t stride, int size) {
-  return rows > 0 ? ((int64_t)(rows - 1) * stride + width) * size : 0;
+// Whether a and b have a byte in common. Rows of the same stride may lie between each
+// other's (columns of one larger matrix); of other strides, what lies from the first byte
+// to the last counts.
+bool overlap(Rows a, Rows b) {
+  if (!a.at || !b.at || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return false;
+  const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+  const uint64_t xs = (uint64_t)((a.rows - 1) * a.stride + a.width);
+  const uint64_t ys = (uint64_t)((b.rows - 1) * b.stride + b.width);
+  if (x >= y + ys || y >= x + xs) return false;
+  if (a.rows == 1) a.stride = b.stride;
+  if (b.rows == 1) b.stride = a.stride;
+  if (a.stride != b.stride || a.stride < 1) return true;
+  const int64_t s = a.stride;
+  const int64_t d = y >= x ? (int64_t)((y - x) % (uint64_t)s)
+                           : (s - (int64_t)((x - y) % (uint64_t)s)) % s;
+  return d < a.width || d + b.width > s;   // b's rows between a's end and its next
 }
 
 // Arguments of rows of logits that the scoring calls share. Strides times rows stay
@@ -171,7 +186,9 @@ int check_scores(const void* logits, int dtype, int rows, int vocab, int64_t row
   if (dtype != TSR_F32 && dtype != TSR_BF16) return TSR_EINVAL;
   if (rows < 0 || vocab < 1 || row_stride < vocab || !elem_aligned(logits, dtype))
     return TSR_EINVAL;
-  if (!isfinite(temperature) || temperature < kTemperatureMin) return TSR_EINVAL;
+  // log2(e) / T stays a float32 number
+  if (!(temperature >= kTemperatureMin && temperature <= kTemperatureMax))
+    return TSR_EINVAL;
   if (vocab > kMaxWideVocab || rows > kMaxScoreRows || row_stride >= kMaxScoreStride)
     return TSR_EUNSUPPORTED;
   return TSR_OK;
@@ -701,26 +718,21 @@ int norm_quantize_rows(tsr_handle h, const void* x, int64_t x_stride, const void
     return TSR_EUNSUPPORTED;
   if (rows == 0) return TSR_OK;
   const int es = esize(dtype);
-  const int64_t nx = extent(rows, width, x_stride, es);
-  const int64_t nr = residual ? extent(rows, width, residual_stride, es) : 0;
-  const int64_t nh = out_residual ? extent(rows, width, out_residual_stride, es) : 0;
-  const int64_t nq = extent(rows, width, codes_stride, 1);
-  const int64_t nw = weight ? (int64_t)width * esize(weight_dtype) : 0, ns = (int64_t)rows * 4;
+  const Rows mx{x, x_stride * es, (int64_t)width * es, rows};
+  const Rows mr{residual, residual_stride * es, (int64_t)width * es, rows};
+  const Rows mh{out_residual, out_residual_stride * es, (int64_t)width * es, rows};
+  const Rows mq{out_codes, codes_stride, width, rows};
+  const Rows mw{weight, 0, (int64_t)width * esize(weight_dtype), 1};
+  const Rows ms{out_scale, 0, (int64_t)rows * 4, 1};
   // the sum may take the place of x or of the residual, row for row
   const bool on_x = out_residual == x && (rows == 1 || out_residual_stride == x_stride);
   const bool on_r =
       out_residual == residual && (rows == 1 || out_residual_stride == residual_stride);
-  if ((!on_x && overlap(out_residual, nh, x, nx)) ||
-      (!on_r && overlap(out_residual, nh, residual, nr)) ||
-      overlap(out_residual, nh, weight, nw) || overlap(out_residual, nh, out_scale, ns))
+  if ((!on_x && overlap(mh, mx)) || (!on_r && overlap(mh, mr)) || overlap(mh, mw) ||
+      overlap(mh, ms) || overlap(mh, mq))
     return TSR_EINVAL;
-  if (overlap(out_codes, nq, x, nx) || overlap(out_codes, nq, residual, nr) ||
-      overlap(out_codes, nq, out_residual, nh) || overlap(out_codes, nq, weight, nw) ||
-      overlap(out_codes, nq, out_scale, ns))
-    return TSR_EINVAL;
-  if (overlap(out_scale, ns, x, nx) || overlap(out_scale, ns, residual, nr) ||
-      overlap(out_scale, ns, weight, nw))
-    return TSR_EINVAL;
+  if (overlap(mq, mx) || overlap(mq, mr) || overlap(mq, mw) || overlap(mq, ms)) return TSR_EINVAL;
+  if (overlap(ms, mx) || overlap(ms, mr) || overlap(ms, mw)) return TSR_EINVAL;
   tsr::NormArgs a{};
   a.x = static_cast<const unsigned char*>(x);
   a.x_stride = (long long)x_stride * es;
@@ -807,8 +819,9 @@ int token_logprobs_grad(tsr_handle h, const void* logits, int dtype, int rows, i
   if (n_tokens > kMaxScoreTokens || grad_stride >= kMaxScoreStride) return TSR_EUNSUPPORTED;
   if (rows == 0) return TSR_OK;
   // the logits are read again where the tokens are: the gradient has memory of its own
-  if (overlap(out_grad, extent(rows, vocab, grad_stride, esize(dtype)), logits,
-              extent(rows, vocab, row_stride, esize(dtype))))
+  const int es = esize(dtype);
+  if (overlap(Rows{out_grad, grad_stride * es, (int64_t)vocab * es, rows},
+              Rows{logits, row_stride * es, (int64_t)vocab * es, rows}))
     return TSR_EINVAL;
   tsr::LogprobGradArgs a{};
   a.logits = static_cast<const unsigned char*>(logits);
@@ -854,8 +867,9 @@ int distill_topk(tsr_handle h, const void* logits, int dtype, int rows, int voca
   if (k > tsr::kMaxTop || (out_grad && grad_stride >= kMaxScoreStride)) return TSR_EUNSUPPORTED;
   if (rows == 0) return TSR_OK;
   // the logits are read more than once: the gradient has memory of its own
-  if (out_grad && overlap(out_grad, extent(rows, vocab, grad_stride, esize(dtype)), logits,
-                          extent(rows, vocab, row_stride, esize(dtype))))
+  const int es = esize(dtype);
+  if (overlap(Rows{out_grad, grad_stride * es, (int64_t)vocab * es, rows},
+              Rows{logits, row_stride * es, (int64_t)vocab * es, rows}))
     return TSR_EINVAL;
   const int64_t need = (int64_t)tsr::distill_ws_bytes(dtype, rows, vocab, out_grad != nullptr);
   if (need && (!workspace || ((uintptr_t)workspace % 16) != 0 || workspace_bytes < need))

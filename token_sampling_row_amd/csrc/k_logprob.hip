@@ -553,8 +553,8 @@ void launch_slices(const LogprobArgs& a, const Cut& cut, const LpWs& ws, hipStre
   };
   if (cut.block == kRowBlock) {
     if (cut.nc == 2) return launch(logprob_slice_kernel<DT, 2, kRowBlock, TOP, false>);
-    if (cut.nc == 4) return launch(logprob_slice_kernel<DT, 4, kRowBlock, TOP, ONCE>);
-    return launch(logprob_slice_kernel<DT, 8, kRowBlock, TOP, ONCE>);
+    if (cut.nc == 4) return launch(logprob_slice_kernel<DT, 4, kRowBlock, TOP, false>);
+    return launch(logprob_slice_kernel<DT, 8, kRowBlock, TOP, false>);   // 67 MB at most
   }
   if (cut.nc == 1) return launch(logprob_slice_kernel<DT, 1, kSliceBlock, TOP, false>);
   if (cut.nc == 2) return launch(logprob_slice_kernel<DT, 2, kSliceBlock, TOP, false>);
