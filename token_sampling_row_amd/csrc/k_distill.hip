@@ -221,6 +221,7 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
   const auto put = [&](auto&& of) {
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
+      if (!s.has(j)) continue;
       float v[EPC];
       pass.unpack<DT>(s.c[j], v);
 #pragma unroll

@@ -115,8 +115,6 @@ template <int DT, int NC, int BLOCK = kSliceBlock>
 struct Slice {
   static constexpr int EPC = Fmt<DT>::EPC;
   const unsigned char* row;
-  const unsigned char* base;   // of the slice's chunks, the last of which is `last`
-  uint32_t last;
   uint4 c[NC];
   uint4 rest;   // the elements behind the last whole chunk, with one thread of the last slice
   int lo, hi;   // the slice's whole chunks
@@ -126,36 +124,29 @@ struct Slice {
     return lo + j * BLOCK + (int)threadIdx.x;
   }
 
+  // Whether any thread has a j-th chunk (the same for all of them).
+  __device__ __forceinline__ bool has(int j) const { return j * BLOCK < hi - lo; }
+
   // Loads are addressed from a uniform base; threads past the slice's last chunk repeat
   // it, and `largest` puts -inf in its place.
   template <bool ONCE>
   __device__ __forceinline__ void load(const unsigned char* at, int V, int slice, const Cut& cut) {
+    row = at;
     const int whole = V / EPC;
     lo = slice * cut.per;
     hi = min(lo + cut.per, whole);
     ragged = slice == cut.slices - 1 && whole * EPC < V;
-    from(at, V);
+    const unsigned char* base =
+        whole > 0 ? row + (long long)min(lo, whole - 1) * 16
+                  : reinterpret_cast<const unsigned char*>(&g_neg_inf_chunk[DT]);
+    const uint32_t last = (uint32_t)max(hi - lo - 1, 0);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) load_chunk<ONCE>(j);
-    load_rest(V);
-  }
-  // The same in steps: where the loads come from (nullptr: nowhere, chunks of -inf), each
-  // chunk's, and what is behind the last whole one.
-  __device__ __forceinline__ void from(const unsigned char* at, int V) {
-    const int whole = V / EPC;
-    row = at;
-    base = at && whole > 0 ? at + (long long)min(lo, whole - 1) * 16
-                           : reinterpret_cast<const unsigned char*>(&g_neg_inf_chunk[DT]);
-    last = at ? (uint32_t)max(hi - lo - 1, 0) : 0u;
-  }
-  template <bool ONCE>
-  __device__ __forceinline__ void load_chunk(int j) {
-    const unsigned char* p = base + min((uint32_t)(j * BLOCK) + threadIdx.x, last) * 16u;
-    c[j] = ONCE ? load16_once(p) : load16(p);
-  }
-  __device__ __forceinline__ void load_rest(int V) {
+    for (int j = 0; j < NC; ++j) {
+      const unsigned char* p = base + min((uint32_t)(j * BLOCK) + threadIdx.x, last) * 16u;
+      c[j] = ONCE ? load16_once(p) : load16(p);
+    }
     rest = neg_inf_chunk<DT>();
-    if (ragged && row && threadIdx.x == BLOCK - 1) rest = load_chunk_slow<DT>(row, V / EPC, V);
+    if (ragged && threadIdx.x == BLOCK - 1) rest = load_chunk_slow<DT>(row, whole, V);
   }
 
   // f(values, number of the first) for each chunk of the thread
@@ -165,6 +156,7 @@ struct Slice {
     float v[EPC];
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
+      if (!has(j)) continue;
       pass.unpack<DT>(c[j], v);
       f(v, chunk_id(j) * EPC);
       sched_fence();
@@ -250,6 +242,10 @@ struct Slice {
     float v[EPC], m = kNegInf;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
+      if (!has(j)) {
+        of(j, kNegInf);
+        continue;
+      }
       if ((j + 1) * BLOCK > hi - lo) {   // the same for all threads
         const uint4 none = neg_inf_chunk<DT>();
         const bool in = chunk_id(j) < hi;
@@ -307,8 +303,10 @@ struct Slice {
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         float v[EPC];
-        pass.unpack<DT>(c[j], v);
-        add(v, x_of);
+        if (has(j)) {
+          pass.unpack<DT>(c[j], v);
+          add(v, x_of);
+        }
         if (j % GROUP == GROUP - 1) flush();
         sched_fence();
       }
