@@ -240,15 +240,19 @@ __global__ __launch_bounds__(BLOCK) void logprob_slice_kernel(LogprobArgs a, Cut
     if (row_status(all.M) == 0) gather(s, a.V, cmax, tau, a.k, cands, hits, scratch);
   }
   if (cut.slices == 1) {
-    const double logZ = log(all.Z);
-    if (threadIdx.x < kWave) put_row<DT>(a, r, all, logZ, given);
     if constexpr (TOP) {
       for (int i = cands.n + (int)threadIdx.x; i < a.k; i += BLOCK)
-        put_top(a, r, i, 0, all, logZ);   // past the last
+        put_top(a, r, i, 0, all, 0.0);   // past the last
+      if ((int)threadIdx.x >= max(cands.n, kWave)) return;
+    } else if (threadIdx.x >= kWave) {
+      return;
+    }
+    const double logZ = log(all.Z);   // not by wavefronts that have nothing to put
+    if (threadIdx.x < kWave) put_row<DT>(a, r, all, logZ, given);
+    if constexpr (TOP)
       rank_candidates(cands, a.k, [&](int rank, unsigned long long key) {
         put_top(a, r, rank, key, all, logZ);
       });
-    }
     return;
   }
   const long long at = r * cut.slices + slice;
