@@ -1,6 +1,9 @@
 // A row's gradient p (A + B x), written in tiles (token_logprobs_grad, distill_topk).
 //
-// Bound by memory: each logit is read once and each element written once.
+// Bound by memory: each logit is read once and each element written once. No
+// loop and no state from one tile to the next. Tiles of 4 chunks a thread: 1024 x 128256
+// bf16 with the entropy's gradient, reading past the caches, 87 us (525 MB at 6.0 TB/s;
+// without it 80, 6.6), of 2 chunks 95 and of 8 87; 64 x 32000 fp32 6.1 us, 5.5 and 6.4.
 #pragma once
 
 #include "row_slice.hpp"

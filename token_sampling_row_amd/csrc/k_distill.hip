@@ -8,6 +8,18 @@
 //
 // p_r is summed over the ids outside S themselves, and their weights are taken against
 // their own largest: as 1 - sum_S p it would be lost where S holds nearly everything.
+//
+// Bound by memory: a logit is read once and its gradient written once where a workgroup's
+// registers hold the row, which is all that the row kernel moves. Wider rows, and few of
+// them, go through slices, and the gradient reads the logits again, from the caches where
+// they are no more than those hold. Measured, bf16, kernel and TB/s of the logits and the
+// gradient together:
+//   1024 x 151936, 64 entries, tail   126 to 132 us (4.9 to 4.7): a row takes its compute
+//                   unit's registers whole, so a row's stores and the next one's loads
+//                   overlap only as far as wavefronts end
+//   1024 x 128256, tail 105 us (5.0), without 100; 256 x 128256, 20 entries 24 us (5.5)
+//   33 x 8191 fp32  7 us: one row's latencies
+//   512 x 128256 fp32   slices 47 us, join 8, gradient 76
 #include <algorithm>
 
 #include "grad_tile.hpp"
@@ -72,12 +84,13 @@ __device__ __forceinline__ Entries entries_of(const DistillArgs& a, int id, floa
   bool twice = false;
   for (int l = 0; l < a.k; ++l)
     twice |= (int)readlane_u32((uint32_t)e.id, l) == e.id && l != lane;
-  if (__any(twice && e.first)) {   // an id that comes again
+  if (__any(twice && e.first)) {   // an id that comes again: one order for all of its lanes
+    e.same = 0.0;
     for (int l = 0; l < a.k; ++l) {
-      const bool again = (int)readlane_u32((uint32_t)e.id, l) == e.id && l != lane;
+      const bool is = (int)readlane_u32((uint32_t)e.id, l) == e.id;
       const double q = readlane_f64(e.q, l);
-      if (again) e.same += q;
-      if (again && l < lane) e.first = false;
+      if (is) e.same += q;
+      if (is && l < lane) e.first = false;
     }
   }
   return e;
@@ -227,7 +240,8 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
 #pragma unroll
       for (int i = 0; i < EPC; ++i) v[i] = of(v[i]);
       unsigned char* base = out + j * BLOCK * 16;   // uniform
-      if (j * BLOCK + (int)threadIdx.x < whole) store16<false>(base + threadIdx.x * 16u, pack<DT>(v));
+      if (j * BLOCK + (int)threadIdx.x < whole)
+        store16<false>(base + threadIdx.x * 16u, pack<DT>(v));
       sched_fence();
     }
   };
@@ -352,7 +366,8 @@ __global__ __launch_bounds__(kSliceBlock) void distill_grad_kernel(DistillArgs a
     return;
   }
   const int id = valid_id(a, raw_id(a, r));
-  put_tile<DT, false, ONCE>(a.logits + r * a.stride_bytes, out, a.V, tile, GradRow(d.M, a.c, d.A, 0.0));
+  const unsigned char* row = a.logits + r * a.stride_bytes;
+  put_tile<DT, false, ONCE>(row, out, a.V, tile, GradRow(d.M, a.c, d.A, 0.0));
   const bool here = id >= 0 && id / kTileIds<DT> == tile;
   if (!__any(here)) return;   // the same for all of the workgroup
   __syncthreads();
@@ -364,15 +379,22 @@ __global__ __launch_bounds__(kSliceBlock) void distill_grad_kernel(DistillArgs a
 constexpr int kHalfBlock = 512, kRowBlock = 1024;
 constexpr int kRowChunks = 20 * kRowBlock;
 
-// How rows are cut; one slice: not at all.
+// How rows are cut; one slice: not at all (us, calls back to back).
+//  - Up to 4096 chunks: one workgroup of 256 threads and one launch. 1 x 8192 bf16 9.5, in
+//    slices and tiles 12.5; 64 x 8192 9.7 against 18.5, 64 x 32000 11.3 against 12.0.
+//  - Up to 20480 chunks from 128 rows on: one workgroup of 512 or 1024 threads. 128 x 128256
+//    bf16 20.8 against 22.4 in slices, 256 rows 24.7 against 39.5; but 64 rows 19.4 against
+//    15.2 and 1 row 16.5 against 11.9.
+//  - Else slices: as many as give a thousand workgroups, at least what holds the row.
 Cut dt_cut(int dtype, int rows, int vocab) {
   const int whole = vocab / (dtype == 0 ? 4 : 8);
-  if (whole <= kMaxSliceChunks) return cut_of(whole, 1);   // TUNE
+  if (whole <= kMaxSliceChunks) return cut_of(whole, 1);
   if (whole <= kRowChunks && rows >= 128) {
     const int block = whole <= 16 * kHalfBlock ? kHalfBlock : kRowBlock;
     return Cut{1, whole, (whole + block - 1) / block, block};
   }
-  return cut_of(whole, std::min({1024 / max(rows, 1), 64, (whole + kSliceBlock - 1) / kSliceBlock}));
+  const int want = std::min({1024 / max(rows, 1), 64, (whole + kSliceBlock - 1) / kSliceBlock});
+  return cut_of(whole, want);
 }
 
 // Batches of more bytes than this, logits and gradient together, are read past the caches,

@@ -7,6 +7,10 @@
 // elements and known exactly (one fma): it goes into the factor that joins the
 // thread to the others. That is one fma an element where (z - m) c takes two
 // roundings and two instructions.
+//
+// Slices are of 16 chunks a thread at most (64 registers): 256 threads hold 32768 bf16
+// logits, and a row of 151936 is five slices. Wider workgroups hold whole rows where that
+// saves a second read (distill_topk) or a second launch (token_logprobs of few rows).
 #pragma once
 
 #include "kernels.hpp"
