@@ -9,11 +9,12 @@
 // Bound by memory: a logit is read once, and the gradient writes as much again. Rows are
 // cut into slices that registers hold, and the largest logit, the sums and the likeliest
 // ids are all taken from there; a wavefront to a row joins the slices. Measured, bf16:
-//   1024 x 151936   slices 49 us (6.3 TB/s), join 5. With 64 alternatives 64 and 9: there
-//                   vector instructions alone take 53 (1580 a wavefront)
+//   1024 x 151936   slices 49 us (6.3 TB/s), join 5. With 64 alternatives 64 to 66 and
+//                   9: there the vector pipes are busy throughout (1580 instructions
+//                   a wavefront, 128 of them exponentials at a quarter of the rate)
 //   1 x 128256, 20 alternatives   5.6 us and 7.2: latencies of loads and exchanges
 //   320 x 32000 fp32   11 us in one launch, from the caches
-//   gradient, 1024 x 128256   80 us (6.6 TB/s), with the entropy's 84 to 87
+//   gradient, 1024 x 128256   80 us (6.6 TB/s), with the entropy's 84 to 88
 #include <algorithm>
 #include <type_traits>
 
