@@ -504,6 +504,7 @@ typedef struct {
  *  workspace: 16-byte aligned device memory of at least token_logprobs_workspace
  *      bytes, the call's own until it is done (NULL where that is 0). Its
  *      contents do not matter before the call or after it.
+ * Neither outputs nor the workspace lie over inputs or each other (TSR_EINVAL).
  * rows and vocab are not bound by the handle's. n_tokens <= 1024, top_k <= 64,
  * rows < 2^22, vocab <= 2^30, row_stride < 2^36 (TSR_EUNSUPPORTED beyond). */
 int token_logprobs(tsr_handle h, const void* logits, int dtype, int rows, int vocab,
@@ -526,7 +527,7 @@ int token_logprobs_workspace(int dtype, int rows, int vocab, int top_k);
  *  grad_logprob [rows][n_tokens] (NULL with n_tokens 0); grad_entropy [rows], or
  *      NULL: no gradient comes back to the entropy (entropy may then be NULL).
  *  out_grad [rows][vocab] of type dtype, grad_stride elements apart, none of it in
- *      the logits' memory (TSR_EINVAL). What lies between vocab and grad_stride is
+ *      an input's memory (TSR_EINVAL). What lies between vocab and grad_stride is
  *      left as it is. Each element is rounded once.
  * A row to which only zeros come back gets zeros, and its logits are not looked at.
  * Limits as token_logprobs'. Uses no workspace. */
@@ -556,13 +557,14 @@ int token_logprobs_grad(tsr_handle h, const void* logits, int dtype, int rows, i
  *  out_grad [rows][vocab] of type dtype, grad_stride elements apart: the gradient of the
  *      sum of out_loss by the logits, (row_weight / temperature) times Q p_j - q_j at
  *      entries and p_j (Q - q_r / p_r) elsewhere, Q = sum q + q_r; each rounded once.
- *      NULL: the loss alone. None of it in the logits' memory (TSR_EINVAL). For a
- *      loss over temperatures the usual factor temperature^2 goes into row_weight.
+ *      NULL: the loss alone. For a loss over temperatures the usual factor temperature^2
+ *      goes into row_weight.
  *  out_status [rows] (nullable): TSR_ROW_OK, else loss and gradient are NaN: the first
  *      that holds of TSR_ROW_BADTOKEN (an id neither -1 nor in [0, vocab)),
  *      TSR_ROW_NONFINITE (a NaN or +inf log probability), TSR_ROW_EMPTY (no entry with
  *      q > 0), TSR_ROW_NONFINITE, TSR_ROW_EMPTY (the logits, as in token_logprobs).
  *  workspace: as token_logprobs', of distill_topk_workspace bytes.
+ * Neither outputs nor the workspace lie over inputs or each other (TSR_EINVAL).
  * 1 <= k; k <= 64 and the limits of token_logprobs (TSR_EUNSUPPORTED beyond). */
 int distill_topk(tsr_handle h, const void* logits, int dtype, int rows, int vocab,
                  int64_t row_stride, double temperature, const int32_t* ids,

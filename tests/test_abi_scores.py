@@ -155,6 +155,70 @@ def test_distill_topk(lib, handle, mem):  # noqa: F811
                          (dict(stride=1 << 36), EUNSUPPORTED), (dict(rows=1 << 22), EUNSUPPORTED)])
 
 
+def test_outputs_over_inputs_or_each_other(lib, handle, mem):  # noqa: F811
+    """Every output over every input, by its last or first word, and over each other output;
+    side by side they come as far as the device (only where there is none)."""
+    R, V, n, k = 4, 64, 2, 3
+    apart = 3 if not torch.cuda.is_available() else None
+
+    def pairs(call, outs, ins):
+        """outs, ins: name -> bytes. Each lies 4096 bytes from the next but for one pair."""
+        at = {name: mem + 4096 * i for i, name in enumerate((*outs, *ins))}
+        if apart is not None:
+            assert call(at) == apart
+        for o in outs:
+            for other in (*outs, *ins):
+                if other == o:
+                    continue
+                size = {**outs, **ins}[other]
+                for where in (at[other], at[other] + size - 4, at[other] - outs[o] + 4):
+                    if where >= mem:
+                        assert call(dict(at, **{o: where})) == EINVAL, (o, other, where - at[other])
+                if apart is not None and at[other] >= mem + 4096:
+                    assert call(dict(at, **{o: at[other] + size})) == apart, (o, other)
+                    assert call(dict(at, **{o: at[other] - outs[o]})) == apart, (o, other)
+
+    def logprobs(p):
+        o = tsr._Logprobs(p["lp"], p["H"], p["ids"], p["top"], p["norm"], p["status"])
+        return lib.token_logprobs(handle, p["z"], 0, R, V, V, 1.0, p["tok"], n, k, ctypes.byref(o),
+                                  None, 0, None)
+
+    pairs(logprobs, dict(lp=4 * R * n, H=4 * R, ids=4 * R * k, top=4 * R * k, norm=8 * R,
+                         status=4 * R), dict(z=4 * R * V, tok=4 * R * n))
+
+    def grad(p):
+        return lib.token_logprobs_grad(handle, p["z"], 0, R, V, V, 1.0, p["tok"], n, p["norm"],
+                                       p["g"], p["H"], p["ge"], p["out"], V, None)
+
+    pairs(grad, dict(out=4 * R * V), dict(z=4 * R * V, tok=4 * R * n, norm=8 * R, g=4 * R * n,
+                                          H=4 * R, ge=4 * R))
+
+    def distill(p):
+        return lib.distill_topk(handle, p["z"], 0, R, V, V, 1.0, p["ids"], p["t"], k, 1, p["w"],
+                                p["loss"], p["grad"], V, p["status"], None, 0, None)
+
+    pairs(distill, dict(grad=4 * R * V, loss=4 * R, status=4 * R),
+          dict(z=4 * R * V, ids=4 * R * k, t=4 * R * k, w=4 * R))
+
+
+def test_a_workspace_over_other_memory(lib, handle, mem):  # noqa: F811
+    """Large rows of one id each other: the workspace lies over an output, then an input.
+    Nothing is read: the calls are refused."""
+    rows, V = 3, 1 << 20
+    far = 1 << 40   # addresses that no call gets as far as to use
+    need = lib.token_logprobs_workspace(0, rows, V, 4)
+    good = [far + (i << 30) for i in range(1, 7)]
+    if need:
+        for ws in (good[0], (good[5] - need) // 16 * 16 + 16, far, far + 4 * rows * V - 16, 2 * far):
+            assert lib.token_logprobs(handle, far, 0, rows, V, V, 1.0, 2 * far, 1, 4,
+                                      ctypes.byref(tsr._Logprobs(*good)), ws, need, None) == EINVAL
+    need = lib.distill_topk_workspace(0, rows, V, 0)
+    if need:
+        for ws in (good[0], good[1], (good[2] - need) // 16 * 16 + 16, good[3], far):
+            assert lib.distill_topk(handle, far, 0, rows, V, V, 1.0, good[0], good[1], 1, 0, good[2],
+                                    good[3], None, 0, None, ws, need, None) == EINVAL
+
+
 def test_a_workspace_that_does_not_do(lib, handle, mem):  # noqa: F811
     """Where a call takes one: none, too small, not aligned."""
     rows, V = 3, 1 << 20

@@ -178,6 +178,21 @@ bool overlap(Rows a, Rows b) {
   return d < a.width || d + b.width > s;   // b's rows between a's end and its next
 }
 
+// Memory without gaps.
+Rows block_of(const void* at, int64_t bytes) { return Rows{at, bytes, bytes, 1}; }
+
+// Whether an output lies over an input or another output.
+template <size_t O, size_t I>
+bool clash(const Rows (&outs)[O], const Rows (&ins)[I]) {
+  for (size_t i = 0; i < O; ++i) {
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+    for (size_t j = 0; j < I; ++j)
+      if (overlap(outs[i], ins[j])) return true;
+  }
+  return false;
+}
+
 // Arguments of rows of logits that the scoring calls share. Strides times rows stay
 // within 64 bits.
 int check_scores(const void* logits, int dtype, int rows, int vocab, int64_t row_stride,
@@ -780,6 +795,15 @@ int token_logprobs(tsr_handle h, const void* logits, int dtype, int rows, int vo
   const int64_t need = (int64_t)tsr::logprobs_ws_bytes(dtype, rows, vocab, top_k);
   if (need && (!workspace || ((uintptr_t)workspace % 16) != 0 || workspace_bytes < need))
     return TSR_EINVAL;
+  const int es = esize(dtype);
+  const int64_t words = (int64_t)rows * 4;
+  const Rows outs[] = {block_of(out->logprob, words * n_tokens), block_of(out->entropy, words),
+                       block_of(out->top_ids, words * top_k),
+                       block_of(out->top_logprob, words * top_k), block_of(out->norm, words * 2),
+                       block_of(out->status, words), block_of(workspace, need)};
+  const Rows ins[] = {Rows{logits, row_stride * es, (int64_t)vocab * es, rows},
+                      block_of(tokens, words * n_tokens)};
+  if (clash(outs, ins)) return TSR_EINVAL;
   tsr::LogprobArgs a{};
   a.logits = static_cast<const unsigned char*>(logits);
   a.stride_bytes = (long long)row_stride * esize(dtype);
@@ -820,9 +844,13 @@ int token_logprobs_grad(tsr_handle h, const void* logits, int dtype, int rows, i
   if (rows == 0) return TSR_OK;
   // the logits are read again where the tokens are: the gradient has memory of its own
   const int es = esize(dtype);
-  if (overlap(Rows{out_grad, grad_stride * es, (int64_t)vocab * es, rows},
-              Rows{logits, row_stride * es, (int64_t)vocab * es, rows}))
-    return TSR_EINVAL;
+  const int64_t words = (int64_t)rows * 4;
+  const Rows outs[] = {Rows{out_grad, grad_stride * es, (int64_t)vocab * es, rows}};
+  const Rows ins[] = {Rows{logits, row_stride * es, (int64_t)vocab * es, rows},
+                      block_of(tokens, words * n_tokens), block_of(grad_logprob, words * n_tokens),
+                      block_of(norm, words * 2), block_of(entropy, words),
+                      block_of(grad_entropy, words)};
+  if (clash(outs, ins)) return TSR_EINVAL;
   tsr::LogprobGradArgs a{};
   a.logits = static_cast<const unsigned char*>(logits);
   a.stride_bytes = (long long)row_stride * esize(dtype);
@@ -866,14 +894,19 @@ int distill_topk(tsr_handle h, const void* logits, int dtype, int rows, int voca
     return TSR_EINVAL;
   if (k > tsr::kMaxTop || (out_grad && grad_stride >= kMaxScoreStride)) return TSR_EUNSUPPORTED;
   if (rows == 0) return TSR_OK;
-  // the logits are read more than once: the gradient has memory of its own
-  const int es = esize(dtype);
-  if (overlap(Rows{out_grad, grad_stride * es, (int64_t)vocab * es, rows},
-              Rows{logits, row_stride * es, (int64_t)vocab * es, rows}))
-    return TSR_EINVAL;
   const int64_t need = (int64_t)tsr::distill_ws_bytes(dtype, rows, vocab, out_grad != nullptr);
   if (need && (!workspace || ((uintptr_t)workspace % 16) != 0 || workspace_bytes < need))
     return TSR_EINVAL;
+  // inputs are read more than once, and by several workgroups: outputs have memory of their own
+  const int es = esize(dtype);
+  const int64_t words = (int64_t)rows * 4;
+  const Rows outs[] = {Rows{out_grad, grad_stride * es, (int64_t)vocab * es, rows},
+                       block_of(out_loss, words), block_of(out_status, words),
+                       block_of(workspace, need)};
+  const Rows ins[] = {Rows{logits, row_stride * es, (int64_t)vocab * es, rows},
+                      block_of(ids, words * k), block_of(teacher_logprob, words * k),
+                      block_of(row_weight, words)};
+  if (clash(outs, ins)) return TSR_EINVAL;
   tsr::DistillArgs a{};
   a.logits = static_cast<const unsigned char*>(logits);
   a.stride_bytes = (long long)row_stride * esize(dtype);
