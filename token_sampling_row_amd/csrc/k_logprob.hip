@@ -9,9 +9,9 @@
 // Bound by memory: a logit is read once, and the gradient writes as much again. Rows are
 // cut into slices that registers hold, and the largest logit, the sums and the likeliest
 // ids are all taken from there; a wavefront to a row joins the slices. Measured, bf16:
-//   1024 x 151936   slices 49 us (6.3 TB/s), join 5. With 64 alternatives 64 to 66 and
-//                   9: there the vector pipes are busy throughout (1580 instructions
-//                   a wavefront, 128 of them exponentials at a quarter of the rate)
+//   1024 x 151936   slices 49 us (6.3 TB/s), join 5. With 64 alternatives 61 and 9: there
+//                   the vector pipes are busy throughout (some 1500 instructions a
+//                   wavefront, 128 of them exponentials at a quarter of the rate)
 //   1 x 128256, 20 alternatives   5.6 us and 7.2: latencies of loads and exchanges
 //   320 x 32000 fp32   11 us in one launch, from the caches
 //   gradient, 1024 x 128256   80 us (6.6 TB/s), with the entropy's 84 to 88
@@ -39,7 +39,6 @@ template <int WAVES>
 struct Hits {
   uint4 chunk[WAVES][kHits];
   int id[WAVES][kHits];   // of the chunk's first element
-  int n[WAVES];
 };
 
 __device__ __forceinline__ int lanes_below(unsigned long long who) {
@@ -62,64 +61,58 @@ __device__ __forceinline__ void rank_candidates(const Candidates& c, int k, F&& 
 // The slice's candidates: its logits of at least `tau` (a key of values), of which there
 // are k at least and few more: every wavefront has j = ceil(k / wavefronts) threads whose
 // largest logit is at least that. `cmax`: the largest of each chunk. A wavefront lists its
-// chunks that hold any, and the workgroup then looks at their elements together: taken
-// where they lie, each chunk would cost its wavefront eight tests for one or two that pass
-// (1024 x 151936 with 64 alternatives: slices 78 us against 98). c.n is 0 before the call.
+// chunks that hold any, and looks at the elements of those alone: taken where they lie,
+// each chunk would cost it eight tests for one or two that pass (1024 x 151936 with 64
+// alternatives: slices 78 us against 98 when the workgroup looked at its lists together;
+// each wavefront at its own 60.5 against 63.4). c.n is 0 before the call.
 template <int DT, int NC, int BLOCK>
 __device__ __forceinline__ void gather(const Slice<DT, NC, BLOCK>& s, int V, const float* cmax,
                                        uint32_t tau, int k, Candidates& c,
                                        Hits<BLOCK / kWave>& hits, BlockScratch& scratch) {
-  constexpr int EPC = Fmt<DT>::EPC, WAVES = BLOCK / kWave;
+  constexpr int EPC = Fmt<DT>::EPC;
   const int wave = threadIdx.x / kWave;
-  const float least = key2f(tau);
-  int n = 0;
+  uint4* chunks = hits.chunk[wave];
+  int* ids = hits.id[wave];
+  const float least = fmaxf(key2f(tau), -3.4028235e38f);   // -inf is none
+  int n = 0;   // the same for the wavefront
   const auto list = [&](float most, uint4 chunk, int id) {
-    const bool in = most >= least && most > kNegInf;
+    const bool in = most >= least;
     const unsigned long long who = __ballot(in);
-    if (who == 0) return;
-    const int at = n + lanes_below(who);
-    if (in && at < kHits) {
-      hits.chunk[wave][at] = chunk;
-      hits.id[wave][at] = id;
+    const int next = n + (int)__popcll(who);
+    if (next != n && next <= kHits && in) {
+      const int at = n + lanes_below(who);
+      chunks[at] = chunk;
+      ids[at] = id;
     }
-    n += __popcll(who);
+    n = next;
   };
 #pragma unroll
   for (int j = 0; j < NC; ++j) list(cmax[j], s.c[j], s.chunk_id(j) * EPC);
   if (s.ragged) list(cmax[NC], s.rest, V / EPC * EPC);
-  if (__lane_id() == 0) hits.n[wave] = n;
-  __syncthreads();
-  int count[WAVES], total = 0, most = 0;
-#pragma unroll
-  for (int w = 0; w < WAVES; ++w) {
-    total += count[w] = hits.n[w];
-    most = max(most, count[w]);
-  }
-  if (most <= kHits) {
-    for (int i0 = wave * kWave; i0 < total * EPC; i0 += BLOCK) {
-      const int i = i0 + (int)__lane_id();
-      int at = i / EPC, w = 0;
-      const int e = i % EPC;
-      while (w < WAVES - 1 && at >= count[w]) at -= count[w++];
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (n <= kHits) {
+    for (int i0 = 0; i0 < n * EPC; i0 += kWave) {
+      const int i = i0 + (int)__lane_id(), at = i / EPC, e = i % EPC;
       float v = kNegInf;
-      if (i < total * EPC) {
+      if (i < n * EPC) {
         if constexpr (DT == 0)
-          v = reinterpret_cast<const float*>(&hits.chunk[w][at])[e];
+          v = reinterpret_cast<const float*>(&chunks[at])[e];
         else
-          v = __uint_as_float(
-              (uint32_t) reinterpret_cast<const uint16_t*>(&hits.chunk[w][at])[e] << 16);
+          v = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(&chunks[at])[e] << 16);
       }
-      const bool in = v >= least && v > kNegInf;
+      const bool in = v >= least;
       const unsigned long long who = __ballot(in);
       int first = 0;
       if (__lane_id() == 0) first = atomicAdd(&c.n, (int)__popcll(who));
       const int to = __builtin_amdgcn_readfirstlane(first) + lanes_below(who);
-      if (in && to < kKeys) c.key[to] = top_key(v, hits.id[w][at] + e);
+      if (in && to < kKeys) c.key[to] = top_key(v, ids[at] + e);
     }
-    __syncthreads();
-    if (c.n <= kKeys) return;
-    __syncthreads();
+  } else if (__lane_id() == 0) {
+    atomicAdd(&c.n, kKeys + 1);
   }
+  __syncthreads();
+  if (c.n <= kKeys) return;
+  __syncthreads();
   // Too many (equal logits, or the largest with few threads): one at a time. Each thread
   // keeps its largest key below those taken, and looks for its next when it is taken.
   unsigned long long best = 0, last = ~0ull;
