@@ -14,6 +14,14 @@ constexpr int kTileChunks = 4;   // 16-byte chunks a thread
 template <int DT>
 constexpr int kTileIds = kSliceBlock * kTileChunks * Fmt<DT>::EPC;
 
+// Gradients of more bytes than the 256 MiB of the last cache are written past it: they could
+// not stay, and what they push out costs more. token_logprobs_grad, gradients to memory of
+// their own (to the same memory again; and read whole afterwards), us: 1024 x 151936 bf16 105
+// against 116 (105, 112; 270, 287), 2048 x 128256 175 against 193 (175, 191; 444, 470).
+// Smaller ones gain alone and lose as soon as they are read: 1024 x 128256 90 against 97 (90,
+// 85; 230, 188). distill_topk, 1024 x 151936: 124 against 131, 2048 x 128256 196 against 204.
+constexpr long long kGradOnceBytes = 256ll << 20;
+
 template <bool ONCE>
 __device__ __forceinline__ void store16(void* p, uint4 v) {
   if constexpr (ONCE) {

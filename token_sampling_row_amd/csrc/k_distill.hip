@@ -14,7 +14,7 @@
 // them, go through slices, and the gradient reads the logits again, from the caches where
 // they are no more than those hold. Measured, bf16, kernel and TB/s of the logits and the
 // gradient together:
-//   1024 x 151936, 64 entries, tail   126 to 132 us (4.9 to 4.7): a row takes its compute
+//   1024 x 151936, 64 entries, tail   124 to 128 us (5.0 to 4.9): a row takes its compute
 //                   unit's registers whole, so a row's stores and the next one's loads
 //                   overlap only as far as wavefronts end
 //   1024 x 128256, tail 105 us (5.0), without 100; 256 x 128256, 20 entries 24 us (5.5)
@@ -167,8 +167,9 @@ __device__ __forceinline__ void put_nothing(const DistillArgs& a, long long r) {
 }
 
 // ------------------------------------------------------------ a row in one workgroup
-// Read once: the gradient is formed from the registers that the sums were.
-template <int DT, int NC, int BLOCK, bool ONCE>
+// Read once: the gradient is formed from the registers that the sums were. PAST: past the
+// caches are 1 the logits read, 2 the gradient written as well.
+template <int DT, int NC, int BLOCK, int PAST>
 __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
   constexpr int EPC = Fmt<DT>::EPC;
   __shared__ Sums each[BLOCK / kWave];
@@ -198,7 +199,7 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
   const float t = teacher_of(a, r);
   const unsigned char* row = a.logits + r * a.stride_bytes;
   Slice<DT, NC, BLOCK> s;
-  s.template load<ONCE>(row, a.V, 0, Cut{1, whole, NC});
+  s.template load<PAST != 0>(row, a.V, 0, Cut{1, whole, NC});
   float z = kNegInf;
   if (threadIdx.x < kWave) {   // the row is on its way
     if (valid_id(a, id) >= 0) z = load_elem<DT>(row, id);
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DistillArgs a) {
       for (int i = 0; i < EPC; ++i) v[i] = of(v[i]);
       unsigned char* base = out + j * BLOCK * 16;   // uniform
       if (j * BLOCK + (int)threadIdx.x < whole)
-        store16<false>(base + threadIdx.x * 16u, pack<DT>(v));
+        store16<PAST == 2>(base + threadIdx.x * 16u, pack<DT>(v));
       sched_fence();
     }
   };
@@ -400,28 +401,29 @@ Cut dt_cut(int dtype, int rows, int vocab) {
 // Batches of more bytes than this, logits and gradient together, are read past the caches,
 // which could not keep them: 1024 x 128256 bf16 105 us against 128, 1022 x 64000 50 against
 // 58. (Slices are read from the caches again, and it is their gradient that is written
-// past them: 512 x 128256 fp32 132 us against 157.)
+// past them: 512 x 128256 fp32 128 us against 157, with a reader of the gradient behind it
+// 207 against 220.)
 constexpr long long kOnceBytes = 192ll << 20;
 
-template <int DT, bool ONCE>
+template <int DT, int PAST>
 void launch_rows(const DistillArgs& a, const Cut& cut, hipStream_t s) {
   const auto launch = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(a.rows), dim3(cut.block), 0, s, a);
   };
   if (cut.block == kSliceBlock) {
-    if (cut.nc == 1) return launch(distill_row_kernel<DT, 1, kSliceBlock, false>);
-    if (cut.nc == 2) return launch(distill_row_kernel<DT, 2, kSliceBlock, false>);
-    if (cut.nc == 4) return launch(distill_row_kernel<DT, 4, kSliceBlock, false>);
-    if (cut.nc == 8) return launch(distill_row_kernel<DT, 8, kSliceBlock, ONCE>);
-    return launch(distill_row_kernel<DT, 16, kSliceBlock, ONCE>);
+    if (cut.nc == 1) return launch(distill_row_kernel<DT, 1, kSliceBlock, 0>);
+    if (cut.nc == 2) return launch(distill_row_kernel<DT, 2, kSliceBlock, 0>);
+    if (cut.nc == 4) return launch(distill_row_kernel<DT, 4, kSliceBlock, 0>);
+    if (cut.nc == 8) return launch(distill_row_kernel<DT, 8, kSliceBlock, PAST>);
+    return launch(distill_row_kernel<DT, 16, kSliceBlock, PAST>);
   }
   if (cut.block == kHalfBlock) {
-    if (cut.nc <= 12) return launch(distill_row_kernel<DT, 12, kHalfBlock, ONCE>);
-    return launch(distill_row_kernel<DT, 16, kHalfBlock, ONCE>);
+    if (cut.nc <= 12) return launch(distill_row_kernel<DT, 12, kHalfBlock, PAST>);
+    return launch(distill_row_kernel<DT, 16, kHalfBlock, PAST>);
   }
-  if (cut.nc <= 12) return launch(distill_row_kernel<DT, 12, kRowBlock, ONCE>);
-  if (cut.nc <= 16) return launch(distill_row_kernel<DT, 16, kRowBlock, ONCE>);
-  launch(distill_row_kernel<DT, 20, kRowBlock, ONCE>);
+  if (cut.nc <= 12) return launch(distill_row_kernel<DT, 12, kRowBlock, PAST>);
+  if (cut.nc <= 16) return launch(distill_row_kernel<DT, 16, kRowBlock, PAST>);
+  launch(distill_row_kernel<DT, 20, kRowBlock, PAST>);
 }
 
 template <int DT>
@@ -449,8 +451,12 @@ hipError_t launch_dt(const DistillArgs& all, void* workspace, hipStream_t s) {
   const Cut cut = dt_cut(DT, all.rows, all.V);
   const long long bytes = 2ll * all.rows * all.V * Fmt<DT>::ESZ;
   if (cut.slices == 1) {
-    all.grad && bytes > kOnceBytes ? launch_rows<DT, true>(all, cut, s)
-                                   : launch_rows<DT, false>(all, cut, s);
+    if (all.grad && bytes > 2 * kGradOnceBytes)
+      launch_rows<DT, 2>(all, cut, s);
+    else if (all.grad && bytes > kOnceBytes)
+      launch_rows<DT, 1>(all, cut, s);
+    else
+      launch_rows<DT, 0>(all, cut, s);
     return hipGetLastError();
   }
   const int tiles = tiles_of<DT>(all.V), batch = dt_batch(cut, all.rows, tiles);

@@ -446,8 +446,8 @@ __global__ __launch_bounds__(kLpBlock) void logprob_wide_kernel(LogprobArgs a) {
 
 // ------------------------------------------------------------ the gradient
 // One workgroup to a tile of a row; every wavefront forms the row's factors for itself.
-// ONCE: the logits are read past the caches.
-template <int DT, bool ONCE>
+// PAST: past the caches are 1 the logits read, 2 the gradient written as well.
+template <int DT, int PAST>
 __global__ __launch_bounds__(kSliceBlock) void logprob_grad_kernel(LogprobGradArgs a, int tiles) {
   const int tile = blockIdx.x % tiles;
   const long long r = blockIdx.x / tiles;
@@ -481,7 +481,7 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_grad_kernel(LogprobGradAr
     B = -each * (double)ge * kLn2;
   }
   const GradRow p(a.norm[2 * r], a.c, A, B);
-  put_tile<DT, ONCE, false>(row, out, a.V, tile, p);
+  put_tile<DT, PAST >= 1, PAST == 2>(row, out, a.V, tile, p);
   if (!__any(here)) return;   // the same for all of the workgroup
   __syncthreads();
   for (int i = threadIdx.x; i < a.n; i += kSliceBlock) {
@@ -641,7 +641,7 @@ hipError_t launch_grad(const LogprobGradArgs& all, hipStream_t s) {
   const int batch = max(1, (1 << 23) / tiles);   // workgroups of a launch: fewer than 2^24
   // Logits that the caches could not keep beside the gradient are read past them: 1024 x
   // 128256 bf16 80 us against 101 (6.6 TB/s), but 256 x 128256 26 against 22.
-  const bool once = (long long)all.rows * all.V * Fmt<DT>::ESZ > kOnceBytes;
+  const long long bytes = (long long)all.rows * all.V * Fmt<DT>::ESZ;
   for (int r0 = 0; r0 < all.rows; r0 += batch) {
     LogprobGradArgs a = all;
     a.rows = min(batch, all.rows - r0);
@@ -653,7 +653,12 @@ hipError_t launch_grad(const LogprobGradArgs& all, hipStream_t s) {
     const auto launch = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3(a.rows * tiles), dim3(kSliceBlock), 0, s, a, tiles);
     };
-    once ? launch(logprob_grad_kernel<DT, true>) : launch(logprob_grad_kernel<DT, false>);
+    if (bytes > kGradOnceBytes)
+      launch(logprob_grad_kernel<DT, 2>);
+    else if (bytes > kOnceBytes)
+      launch(logprob_grad_kernel<DT, 1>);
+    else
+      launch(logprob_grad_kernel<DT, 0>);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
