@@ -9,12 +9,13 @@
 // Bound by memory: a logit is read once, and the gradient writes as much again. Rows are
 // cut into slices that registers hold, and the largest logit, the sums and the likeliest
 // ids are all taken from there; a wavefront to a row joins the slices. Measured, bf16:
-//   1024 x 151936   slices 49 us (6.3 TB/s), join 5. With 64 alternatives 61 and 9: there
-//                   the vector pipes are busy throughout (some 1500 instructions a
-//                   wavefront, 128 of them exponentials at a quarter of the rate)
+//   1024 x 151936   slices 49 us (6.3 TB/s), join 5. With 64 alternatives 61 to 66 and
+//                   9: there the vector pipes are busy throughout (1490 instructions
+//                   a wavefront, 128 of them exponentials at a quarter of the rate)
 //   1 x 128256, 20 alternatives   5.6 us and 7.2: latencies of loads and exchanges
 //   320 x 32000 fp32   11 us in one launch, from the caches
-//   gradient, 1024 x 128256   80 us (6.6 TB/s), with the entropy's 84 to 88
+//   gradient, 1024 x 128256   80 us (6.6 TB/s), with the entropy's 85 (6.2), into the
+//                   same memory again; 98 into other memory (5.4)
 #include <algorithm>
 #include <type_traits>
 
