@@ -87,6 +87,41 @@ def test_many_rows(s, dtype, rows, V, tail):
         assert bool((d <= lim).all())
 
 
+@pytest.mark.parametrize("dtype,rows,V", [("bf16", 11200, 12003), ("f32", 9100, 7499),
+                                          ("bf16", 4500, 30001), ("f32", 3400, 20001),
+                                          ("bf16", 2800, 50001), ("f32", 2100, 32003),
+                                          ("bf16", 1500, 90001), ("f32", 1600, 45003),
+                                          ("bf16", 1100, 128253), ("f32", 1100, 65531),
+                                          ("bf16", 900, 151935), ("f32", 850, 80003),
+                                          ("bf16", 700, 200003)])
+def test_gradients_larger_than_the_caches(s, dtype, rows, V):
+    """More than 256 MiB, by workgroups of each size: entries' own values over what was put
+    past the caches, twice over the same memory."""
+    assert rows * V * (4 if dtype == "f32" else 2) > 256 << 20
+    g = torch.Generator(device()).manual_seed(V)
+    z = torch.empty(rows, V, dtype=TD[dtype], device=device()).normal_(generator=g)
+    ids = torch.randint(0, V, (rows, 9), device=device(), generator=g).int()
+    ids[:, 2] = ids[:, 6]
+    ids[:, 3] = V - 1
+    lp = torch.log_softmax(2 * torch.randn(rows, 10, device=device(), generator=g), 1)[:, :9]
+    lp = lp.contiguous()
+    w = torch.rand(rows, device=device(), generator=g)
+    w[1] = 0.0
+    some = sorted({0, 1, rows // 3, rows - 1})
+    out = torch.full((rows, V), 7.0, dtype=TD[dtype], device=device())
+    for tail in (True, False):
+        loss, grad = s.distill_topk(z, ids, lp, 0.9, tail, w, grad=out)
+        check((loss[some], grad[some]), z[some], ids[some].cpu().numpy(), lp[some].cpu().numpy(),
+              0.9, tail, w[some].cpu().numpy())
+        # of every row the sum is 0 but for roundings: half a step of each element (counted of
+        # the rounded ones: 1 + 2^-7 of it), 4 x 60 U of each as in test_many_rows, 8 x 60 U of
+        # each entry and twice that of q_r / p_r for all the others together
+        total = grad.sum(1, dtype=torch.float64).abs()
+        size = grad.abs().sum(1, dtype=torch.float64)
+        lim = (sc.HALF_STEP[dtype] * (1 + 2.0 ** -7) + 240 * sc.U) * size + 11 * 480 * sc.U
+        assert bool((total <= lim).all())
+
+
 @pytest.mark.parametrize("dtype,rows,V", [("f32", 200, 32000), ("bf16", 140, 128256),
                                           ("bf16", 130, 33003), ("f32", 400, 32003),
                                           ("bf16", 1000, 128253), ("bf16", 120, 300005),
