@@ -205,6 +205,45 @@ def test_the_likeliest_wherever_they_are(s, dtype, V, k):
     assert torch.equal(alone.top_ids, got.top_ids[4:5])
 
 
+# a mask's finite fill and flat rows: the k-th largest is one of many equal values
+FILLS = [-1.5, -1e4, float(torch.finfo(torch.bfloat16).min), 0.0, 2.5]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [100003, 128256])
+@pytest.mark.parametrize("k", [20, 41, 64])
+@pytest.mark.parametrize("fill", FILLS)
+def test_ties_of_a_fill(s, dtype, V, k, fill):
+    """A few larger logits, the last slices' among them, over a fill: in a row alone and in
+    several whose neighbours are ordinary."""
+    rng = np.random.default_rng(13)
+    z = rng.normal(0, 2, (9, V)).astype(np.float32)
+    z[2:5] = z[7:] = fill
+    for r in (2, 4, 7, 8):
+        z[r, [50, 70000, V - 3001, V - 1]] = [fill / 2 + 0.5, fill / 4 + 1, 3.5, 3.25]
+    z[8, rng.permutation(V)[:30]] = rng.normal(4, 1, 30)
+    t = dev(z).to(TD[dtype])
+    check(s.token_logprobs(t, top_k=k, status=new_status(9)), t, None, k, 1.0)
+    for r in (2, 3, 8):
+        check(s.token_logprobs(t[r:r + 1], top_k=k), t[r:r + 1], None, k, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,V", [(300, 33001), (700, 70001)])
+@pytest.mark.parametrize("k", [20, 64])
+@pytest.mark.parametrize("fill", FILLS)
+def test_ties_of_a_fill_in_large_batches(s, dtype, rows, V, k, fill):
+    """Every other row a fill with larger logits at its ends."""
+    g = torch.Generator(device()).manual_seed(V)
+    z = (2 * torch.randn(rows, V, device=device(), generator=g)).to(TD[dtype])
+    z[::2] = fill
+    z[::2, 7], z[::2, V - 5] = 3.0, 3.5
+    got = s.token_logprobs(z, top_k=k)
+    want = torch.sort(z.float(), dim=1, descending=True, stable=True)[1][:, :k]
+    assert torch.equal(got.top_ids.long(), want)
+    check(got, z, None, k, 1.0, [0, 1, rows // 2, rows - 1])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("off", [0, 1, 5])
 @pytest.mark.parametrize("V", [13, 9001, 70003])

@@ -337,6 +337,9 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_top_join_kernel(LogprobAr
       if (n >= need) found = more;
       if (n == need) break;
     }
+    // bf16: what the search leaves out is set throughout in the keys of negative values, and 0
+    // in the others'
+    if (DT == 1 && !(found & 0x80000000u)) found |= 0xFFFFu;
     least = (unsigned long long)found << 32;
     if (how_many(least) > 2 * kWave) {   // so many equal values: the lower ids of them
 #pragma unroll 1
@@ -346,12 +349,13 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_top_join_kernel(LogprobAr
       }
     }
   }
-  int n = 0;
+  int n = 0;   // 128 at most, by the search
 #pragma unroll
   for (int q = 0; q < EACH; ++q) {
     const bool in = key[q] >= least && key[q] != 0;
     const unsigned long long who = __ballot(in);
-    if (in) kept[wave][n + lanes_below(who)] = key[q];
+    const int to = n + lanes_below(who);
+    if (in && to < 2 * kWave) kept[wave][to] = key[q];
     n += __popcll(who);
   }
   const double logZ = log(all.Z);
