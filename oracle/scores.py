@@ -146,7 +146,9 @@ def logprobs_grad(z, tokens, norm, g, T=1.0, H=0.0, ge=0.0, dtype="f32"):
     off += p * abs(ge) * 4 * U * U * abs(M / T / LN2)
     for t, gi in real:
         out[t] += gi
-        off[t] += abs(gi) * (len(real) + 2) * U   # their sum in float32, one fma
+        off[t] += abs(gi) * len(real) * 2.0 ** -52   # their sum in 64 bits
+    for t in {t for t, _ in real}:
+        off[t] += U * abs(out[t])   # with the id's own weight, rounded to float32 first
     off += TINY * (abs(G) + abs(ge) * (88 + 2 * np.log(Z) + abs(H)))
     out, off = out / T, off / T * (1 + 4 * U)
     return out, off + HALF_STEP[dtype] * (np.abs(out) + off) + TINY

@@ -380,6 +380,32 @@ def test_many_tokens(s):
         s.token_logprobs_grad(z, dev(tok), fwd.norm, g, out=z)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("ids", [[77], [0, 77, 4095, 4999]])
+@pytest.mark.parametrize("entropy", [False, True])
+def test_gradients_of_one_token_that_cancel(s, dtype, ids, entropy):
+    """1024 tokens of few ids, whose gradients of some 10^4 leave a sum of some 10 to each id:
+    as one token of each with the sum. Sums in 64 bits are off by 1024 * 2^-53 of their
+    terms' sizes, in the id's own sum and in the row's."""
+    rng = np.random.default_rng(len(ids))
+    T, n = 0.7, 1024 // len(ids)
+    z = logits(rng, 2, 5000, dtype)
+    g = rng.normal(0, 1e4, (2, len(ids), n)).astype(np.float32)
+    g[:, :, n // 2:] = -g[:, :, :n // 2]
+    g[:, :, 0] += rng.normal(0, 10, g.shape[:2]).astype(np.float32)
+    order = rng.permutation(1024)
+    tok = np.tile(np.repeat(np.array(ids, dtype=np.int32), n)[order], (2, 1))
+    fwd = s.token_logprobs(z, dev(tok), temperature=T)
+    ge = dev(rng.normal(0, 1, 2).astype(np.float32)) if entropy else None
+    grad = s.token_logprobs_grad(z, dev(tok), fwd.norm, dev(g.reshape(2, 1024)[:, order]),
+                                 fwd.entropy, ge, temperature=T).float().cpu().numpy()
+    zv, norm, size = z.float().cpu().numpy(), fwd.norm.cpu().numpy(), np.abs(g).sum()
+    for r in range(2):
+        want, off = sc.logprobs_grad(zv[r], ids, norm[r], g[r].astype(np.float64).sum(1), T,
+                                     fwd.entropy[r].item(), ge[r].item() if entropy else 0.0, dtype)
+        within(grad[r], want, off + 2 * 1024 * 2.0 ** -53 * size / T)
+
+
 @pytest.mark.parametrize("T", [1e-30, 1e-6, 1e6, 1e30])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_temperatures_far_from_one(s, dtype, T):

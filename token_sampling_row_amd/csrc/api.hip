@@ -857,7 +857,7 @@ int token_logprobs_grad(tsr_handle h, const void* logits, int dtype, int rows, i
   a.rows = rows;
   a.V = vocab;
   a.c = (float)(1.4426950408889634 / temperature);
-  a.inv_t = (float)(1.0 / temperature);
+  a.inv_t = 1.0 / temperature;
   a.tokens = tokens;
   a.n = n_tokens;
   a.norm = norm;

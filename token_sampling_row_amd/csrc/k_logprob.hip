@@ -479,7 +479,7 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_grad_kernel(LogprobGradAr
   }
   G = wave_sum(G);
   const float Z = a.norm[2 * r + 1];
-  const double each = (double)a.inv_t / (double)Z;
+  const double each = a.inv_t / (double)Z;
   double A = -G * each, B = 0.0;
   if (ge != 0.0f) {
     A -= each * (double)ge * ((double)a.entropy[r] - log((double)Z));
@@ -492,14 +492,15 @@ __global__ __launch_bounds__(kSliceBlock) void logprob_grad_kernel(LogprobGradAr
   for (int i = threadIdx.x; i < a.n; i += kSliceBlock) {
     const int t = tokens[i];
     if (t < t0 || t >= t1) continue;
-    float g = 0.0f;
+    double g = 0.0;   // gradients of one id may cancel
     bool first = true;
     for (int k = 0; k < a.n; ++k) {
       if (tokens[k] != t) continue;
       if (k < i) first = false;
-      g += gs[k];
+      g += (double)gs[k];
     }
-    if (first) store_elem<DT>(out, t, fmaf(g, a.inv_t, p.at(load_elem<DT>(row, t))));
+    if (first)
+      store_elem<DT>(out, t, (float)fma(g, a.inv_t, (double)p.at(load_elem<DT>(row, t))));
   }
 }
 

@@ -226,7 +226,7 @@ struct LogprobGradArgs {
   long long stride_bytes;
   int rows, V;
   float c;
-  float inv_t;
+  double inv_t;
   const int32_t* tokens;    // [rows][n]
   int n;
   const float* norm;        // [rows][2]
