@@ -356,3 +356,17 @@ def test_binding_distill(s):
         with pytest.raises(ValueError):
             s.distill_topk(*args, **kw)
         assert len(s.calls) == n
+
+
+def test_binding_keeps_few_sizes(s):
+    """A server whose batches never have the same rows twice."""
+    z, p = torch.zeros(3000, 4), torch.zeros(3000, 2, 4)
+    fake = tsr.load_library()
+    fake.verify_probs_ex, fake.verify_probs_workspace = fake.token_logprobs, lambda *a: 0
+    s._vp_bytes = {}
+    x, u, v = torch.zeros(3000, 1, dtype=torch.int32), torch.zeros(3000, 1), torch.zeros(3000)
+    for rows in range(1, 3000):
+        s.token_logprobs(z[:rows])
+        s.verify_probs(p[:rows], None, x[:rows], u[:rows], v[:rows])
+    assert len(s.calls) == 2 * 2999 and all(c[12] == 48 for c in s.calls[::2])
+    assert 0 < len(s._ws_bytes) <= 1024 and 0 < len(s._vp_bytes) <= 1024

@@ -253,6 +253,18 @@ def _new_like(stream, t, *shape):
         return t.new_empty(*shape)
 
 
+_SIZES_KEPT = 1024
+
+
+def _keep(sizes, key, need):
+    """need, kept in `sizes` for the next call: no more than _SIZES_KEPT, however many
+    batch sizes a server sees."""
+    if len(sizes) >= _SIZES_KEPT:
+        sizes.clear()
+    sizes[key] = need
+    return need
+
+
 def pack_row_params(params_list):
     """Per-row parameters as the bytes of a tsr_params array (host uint8
     numpy array; copy it to the device for sample_rows_ex's row_params)."""
@@ -675,8 +687,8 @@ class Sampler:
         if raw:
             need = self._vp_bytes.get((dt, rows, vocab))
             if need is None:
-                need = self._vp_bytes[dt, rows, vocab] = \
-                    load_library().verify_probs_workspace(dt, rows, vocab)
+                need = _keep(self._vp_bytes, (dt, rows, vocab),
+                             load_library().verify_probs_workspace(dt, rows, vocab))
             if need:
                 ws = new(need // 4)
                 ws_ptr = ws.data_ptr()
@@ -821,7 +833,7 @@ class Sampler:
         key = (name, *sizes)
         need = self._ws_bytes.get(key)
         if need is None:
-            need = self._ws_bytes[key] = getattr(load_library(), name)(*sizes)
+            need = _keep(self._ws_bytes, key, getattr(load_library(), name)(*sizes))
         if need <= 0:
             return None, None, 0
         if raw:
