@@ -434,6 +434,35 @@ def test_a_vocabulary_of_millions(s):
     check(s.token_logprobs(z, tok, top_k=9), z, tok.cpu().numpy()[:, None], 9, 1.0)
 
 
+@pytest.mark.parametrize("dtype,V,k", [("bf16", 524301, 64), ("bf16", 1048589, 20),
+                                       ("f32", 262155, 64), ("f32", 524303, 20)])
+def test_special_rows_of_wide_vocabularies(s, dtype, V, k):
+    """Just past the widest rows that are cut into slices for so many alternatives."""
+    rng = np.random.default_rng(V)
+    z = rng.normal(0, 3, (12, V)).astype(np.float32)
+    z[0, V - 1] = np.nan
+    z[1, 17] = np.inf
+    z[2] = -np.inf
+    z[3] = -np.inf
+    z[3, [5, V // 2, V - 1]] = [1.0, 1.0, 3.0]   # fewer than k are left
+    z[4] = 0.0
+    z[4, ::2] = -0.0
+    z[5] = torch.finfo(torch.bfloat16).min
+    z[5, [9, V - 2]] = [-1.0, 2.0]
+    z[6] = np.round(z[6])
+    z[7] = -1.5
+    z[8] = np.sort(z[8])
+    z[9] *= 1e30
+    z[10, 0], z[10, 1:] = np.nan, -np.inf
+    t = dev(z).to(TD[dtype])
+    tok = np.tile(np.array([0, 17, V - 1, -1, V, -5, V // 2], dtype=np.int32), (12, 1))
+    tok[11] = [0, 17, V - 1, -1, 3, 3, V // 2]
+    for T in (1.0, 0.3):
+        got = s.token_logprobs(t, dev(tok), top_k=k, temperature=T, status=new_status(12))
+        check(got, t, tok, k, T)
+    assert got.status.tolist() == [1, 1, 2] + [3] * 7 + [1, 0]
+
+
 def test_rows_past_2_31_bytes(s):
     rows, stride, V = 4, (1 << 31) // 3, 9000
     big = torch.zeros(3 * stride + V, dtype=torch.float32, device=device())
