@@ -785,7 +785,9 @@ class Sampler:
         float32 or bfloat16, tokens [rows] or [rows, n] int32 (-1: padding, 0) or None
         -> TokenLogprobs, with the entropy, the top_k likeliest ids and what
         token_logprobs_grad takes (norm). ``status``: a preallocated [rows] int32
-        tensor, or None."""
+        tensor, or None. The results carry no autograd graph, whether or not the logits
+        require a gradient: token_logprobs_grad forms it, for logits.backward(gradient) or
+        the backward of a torch.autograd.Function."""
         dt, rows, vocab, stride = self._matrix(logits, "logits")
         torch = _torch
         dev = logits.device
@@ -891,7 +893,9 @@ class Sampler:
         mass counts as one entry for all other ids; else the entries are
         renormalised. ``row_weight`` [rows] float32 multiplies loss and gradient.
         ``grad``: True (a new tensor), a tensor to hold it, or False. Returns (loss
-        [rows] float32, gradient [rows, V] of the logits' type, or None)."""
+        [rows] float32, gradient [rows, V] of the logits' type, or None). The loss carries
+        no autograd graph, whether or not the logits require a gradient: the gradient goes
+        on with logits.backward(gradient)."""
         dt, rows, vocab, stride = self._matrix(logits, "logits")
         f32 = _torch.float32
         if ids.dim() != 2 or ids.shape[1] < 1:

@@ -325,7 +325,9 @@ __global__ __launch_bounds__(kNormBlock) void norm_kernel(NormArgs a) {
                             : (float)(m / (127.0 * sqrt(ss / a.width + a.eps)));
 }
 
-// Rows of any width: read twice, one workgroup to a row.
+// Rows of any width: read twice, an element at a time and with a quotient in 64 bits for each, one
+// workgroup to a row. 4096 x 12288 fp32 119 us, 4096 x 20480 bf16 241 us, 1 x 20480 bf16 52 us;
+// in registers 4096 x 8192 fp32 takes 33 us and 4096 x 16384 bf16 63 us.
 template <int DT, int WT>
 __global__ __launch_bounds__(kNormBlock) void norm_wide_kernel(NormArgs a) {
   __shared__ BlockScratch scratch;
