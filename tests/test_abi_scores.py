@@ -370,3 +370,13 @@ def test_binding_keeps_few_sizes(s):
         s.verify_probs(p[:rows], None, x[:rows], u[:rows], v[:rows])
     assert len(s.calls) == 2 * 2999 and all(c[12] == 48 for c in s.calls[::2])
     assert 0 < len(s._ws_bytes) <= 1024 and 0 < len(s._vp_bytes) <= 1024
+
+
+def test_binding_refuses_tokens_without_rows(s):
+    """A single number is no [rows] of tokens, though there is but one row."""
+    z, t = torch.zeros(1, 10), torch.tensor(3, dtype=torch.int32)
+    for call in (lambda: s.token_logprobs(z, t),
+                 lambda: s.token_logprobs_grad(z, t, torch.zeros(1, 2), torch.zeros(()))):
+        with pytest.raises(ValueError):
+            call()
+    assert s.calls == []

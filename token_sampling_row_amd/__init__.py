@@ -774,7 +774,7 @@ class Sampler:
         """Pointer to tokens [rows] or [rows, n] int32, and n."""
         shape = tokens.shape
         n = shape[1] if len(shape) == 2 else 1
-        if tokens.dtype is not _torch.int32 or shape[0] != rows or len(shape) > 2 or \
+        if tokens.dtype is not _torch.int32 or len(shape) not in (1, 2) or shape[0] != rows or \
                 tokens.get_device() != self.device or not tokens.is_contiguous():
             self._vector(tokens, _torch.int32, "tokens", *((rows, n) if len(shape) == 2 else (rows,)))
         return tokens.data_ptr(), n
