@@ -530,6 +530,8 @@ int token_logprobs_workspace(int dtype, int rows, int vocab, int top_k);
  *      an input's memory (TSR_EINVAL). What lies between vocab and grad_stride is
  *      left as it is. Each element is rounded once.
  * A row to which only zeros come back gets zeros, and its logits are not looked at.
+ * Where a row's gradients over the temperature pass float32's range, its elements are
+ * not finite, those of weight 0 among them.
  * Limits as token_logprobs'. Uses no workspace. */
 int token_logprobs_grad(tsr_handle h, const void* logits, int dtype, int rows, int vocab,
                         int64_t row_stride, double temperature, const int32_t* tokens,
@@ -558,7 +560,7 @@ int token_logprobs_grad(tsr_handle h, const void* logits, int dtype, int rows, i
  *      sum of out_loss by the logits, (row_weight / temperature) times Q p_j - q_j at
  *      entries and p_j (Q - q_r / p_r) elsewhere, Q = sum q + q_r; each rounded once.
  *      NULL: the loss alone. For a loss over temperatures the usual factor temperature^2
- *      goes into row_weight.
+ *      goes into row_weight. row_weight / temperature within float32's range.
  *  out_status [rows] (nullable): TSR_ROW_OK, else loss and gradient are NaN: the first
  *      that holds of TSR_ROW_BADTOKEN (an id neither -1 nor in [0, vocab)),
  *      TSR_ROW_NONFINITE (a NaN or +inf log probability), TSR_ROW_EMPTY (no entry with
